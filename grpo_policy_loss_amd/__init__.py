@@ -34,4 +34,10 @@ from ._lib import (  # noqa: F401
     grpo_workspace_bytes,
     lib,
 )
-from .autograd import grpo_loss  # noqa: F401,E402
+from ._ops import (  # noqa: F401,E402
+    NORM_LAYER,
+    NORM_RMS,
+    grpo_norm_bwd,
+    grpo_norm_fwd,
+)
+from .autograd import grpo_loss, grpo_norm  # noqa: F401,E402

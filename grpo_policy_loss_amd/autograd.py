@@ -1,7 +1,8 @@
-"""torch.autograd wrapper over the C ABI: the loss as a differentiable function of
-the hidden states H and the LM head W, for use inside a PyTorch training step.
+"""torch.autograd wrappers over the C ABI, for use inside a PyTorch training step:
+the loss as a differentiable function of the hidden states H and the LM head W, and
+the norm in front of it as one of its input, weight and bias.
 
-The forward is grpo_loss_fwd; the backward is grpo_loss_bwd with the upstream
+The loss's forward is grpo_loss_fwd; the backward is grpo_loss_bwd with the upstream
 gradient of the loss as its grad_loss (Unsloth docs, "Offloading activations
 for log softmax": the backward recomputes the chunk's logits instead of
 keeping them).  Marshalling only: both passes run in libgrpo.so.
@@ -11,6 +12,7 @@ from __future__ import annotations
 import torch
 
 from ._lib import grpo_loss_bwd, grpo_loss_fwd
+from ._ops import NORM_LAYER, NORM_RMS, grpo_norm_bwd, grpo_norm_fwd
 
 
 class _GrpoLoss(torch.autograd.Function):
@@ -49,3 +51,31 @@ def grpo_loss(H, W, y, mask, adv, ref_lp, B: int, L: int, beta: float = 0.04,
     accumulator keeps it in float32).  The backward reads the upstream gradient of
     the loss on the host (one synchronisation)."""
     return _GrpoLoss.apply(H, W, y, mask, adv, ref_lp, B, L, beta, chunk, opts)
+
+
+class _GrpoNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, weight, bias, eps, kind):
+        Y, mean, rstd = grpo_norm_fwd(X, weight, bias, eps, kind)
+        ctx.save_for_backward(X, weight, rstd, *([mean] if kind == NORM_LAYER else []))
+        ctx.kind = kind
+        return Y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dY):
+        X, weight, rstd, *mean = ctx.saved_tensors
+        need_x, need_w, need_b = ctx.needs_input_grad[:3]
+        # an upstream gradient may be a broadcast view (that of a sum is)
+        dX, dw, db = grpo_norm_bwd(dY.contiguous(), X, weight, mean[0] if mean else None, rstd,
+                                   ctx.kind, bias=need_b)
+        return (dX if need_x else None, dw.to(weight.dtype) if need_w else None,
+                db.to(weight.dtype) if need_b else None, None, None)
+
+
+def grpo_norm(X, weight, bias=None, eps: float = 1e-5, kind: int = NORM_RMS):
+    """The norm of the rows of X [rows, cols], differentiable (once) with respect to X,
+    weight and bias.  Arguments as for grpo_norm_fwd.  The gradients of weight and bias
+    are formed in float32 and returned in the weight's type (grpo_norm_bwd with float32
+    accumulators keeps them in float32)."""
+    return _GrpoNorm.apply(X, weight, bias, eps, kind)

@@ -11,15 +11,17 @@
 #include <mutex>
 
 #include "../../include/grpo.h"
+#include "api.hpp"
 #include "kernels.hpp"
 #include "tile_mma.hpp"
 #include "timing.hpp"
 
+namespace grpo {
+
 namespace {
-
 thread_local char g_last_error[512] = "";
+}
 
-int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 int fail(int code, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -32,8 +34,18 @@ int hip_fail(hipError_t e, const char* where) {
   return fail(GRPO_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
 }
 
-constexpr size_t kAlign = 256;
-inline size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
+void clear_error() { g_last_error[0] = 0; }
+
+const char* last_error() { return g_last_error; }
+
+}  // namespace grpo
+
+namespace {
+
+using grpo::align_up;
+using grpo::fail;
+using grpo::hip_fail;
+
 inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 inline size_t esize(int dtype) { return dtype == GRPO_F32 ? 4 : dtype == GRPO_FP8_E4M3 ? 1 : 2; }
@@ -208,17 +220,6 @@ int check_shape(int64_t N, int64_t d, int64_t V, int dtype, int64_t chunk, bool 
   return GRPO_OK;
 }
 
-#define GRPO_CHECK_PTR(p)                                                          \
-  do {                                                                             \
-    if ((p) == nullptr) return fail(GRPO_ERR_INVALID_ARG, "null pointer: %s", #p); \
-  } while (0)
-
-#define GRPO_HIP(call)                                    \
-  do {                                                    \
-    hipError_t e_ = (call);                               \
-    if (e_ != hipSuccess) return hip_fail(e_, #call);     \
-  } while (0)
-
 // The kernels' form of the logit transform of a grpo_opts (NULL: identity).
 int make_xform(const grpo_opts* o, grpo::LogitXform* xf) {
   *xf = grpo::LogitXform{1.f, 1.f, 1.f, 0};
@@ -378,7 +379,7 @@ const char* grpo_strerror(int code) {
   }
 }
 
-const char* grpo_last_error(void) { return g_last_error; }
+const char* grpo_last_error(void) { return grpo::last_error(); }
 
 // The fp8 backward runs the bf16 backward on exact bf16 copies of H and W,
 // which come first in its workspace; the bf16 plan (with its slab) follows.
@@ -421,7 +422,7 @@ size_t grpo_workspace_bytes(int op, int64_t N, int64_t d, int64_t V, int dtype, 
 
 int64_t grpo_auto_chunk(int64_t B, int64_t L, int64_t d, int64_t V, int dtype,
                         size_t budget_bytes) {
-  g_last_error[0] = 0;
+  grpo::clear_error();
   if (B <= 0 || L <= 0) {
     fail(GRPO_ERR_INVALID_ARG, "B and L must be positive");
     return 0;
@@ -443,7 +444,7 @@ int64_t grpo_auto_chunk(int64_t B, int64_t L, int64_t d, int64_t V, int dtype,
 
 int grpo_advantages(const float* rewards, int64_t num_groups, int64_t group_size, float eps,
                     float* adv, void* stream) {
-  g_last_error[0] = 0;
+  grpo::clear_error();
   GRPO_CHECK_PTR(rewards);
   GRPO_CHECK_PTR(adv);
   if (num_groups <= 0 || group_size <= 0)
@@ -458,7 +459,7 @@ int grpo_advantages(const float* rewards, int64_t num_groups, int64_t group_size
 int grpo_ref_logprobs_ex(const void* H_ref, const void* W, const int32_t* y, int64_t N, int64_t d,
                          int64_t V, int dtype, int64_t chunk, const grpo_opts* opts,
                          float* ref_lp, void* workspace, size_t workspace_bytes, void* stream) {
-  g_last_error[0] = 0;
+  grpo::clear_error();
   grpo::LogitXform xf;
   grpo::LossVariant lv;
   if (make_xform(opts, &xf) != GRPO_OK || make_variant(opts, &lv) != GRPO_OK)
@@ -495,7 +496,7 @@ int grpo_loss_fwd_ex(const void* H, const void* W, const int32_t* y, const uint8
                      int64_t V, int dtype, float beta, int64_t chunk, const grpo_opts* opts,
                      float* loss, float* lp, float* kl, float* lse, void* workspace,
                      size_t workspace_bytes, void* stream) {
-  g_last_error[0] = 0;
+  grpo::clear_error();
   grpo::LogitXform xf;
   grpo::LossVariant lv;
   if (make_xform(opts, &xf) != GRPO_OK || make_variant(opts, &lv) != GRPO_OK)
@@ -541,7 +542,7 @@ int grpo_loss_bwd_ex(const void* H, const void* W, const int32_t* y, const uint8
                      int64_t B, int64_t L, int64_t d, int64_t V, int dtype, float beta,
                      float grad_loss, int64_t chunk, const grpo_opts* opts, void* dH,
                      float* dW, void* workspace, size_t workspace_bytes, void* stream) {
-  g_last_error[0] = 0;
+  grpo::clear_error();
   grpo::LogitXform xf;
   grpo::LossVariant lv;
   if (make_xform(opts, &xf) != GRPO_OK || make_variant(opts, &lv) != GRPO_OK)
@@ -600,7 +601,7 @@ size_t grpo_quantize_fp8_workspace_bytes(void) { return kQuantParts * 4 + 256; }
 int grpo_quantize_fp8(const void* X, int dtype, int64_t rows, int64_t cols, int per_row,
                       uint8_t* codes, float* scales, void* workspace, size_t workspace_bytes,
                       void* stream) {
-  g_last_error[0] = 0;
+  grpo::clear_error();
   GRPO_CHECK_PTR(X);
   GRPO_CHECK_PTR(codes);
   GRPO_CHECK_PTR(scales);
@@ -630,7 +631,7 @@ int grpo_quantize_fp8(const void* X, int dtype, int64_t rows, int64_t cols, int 
 
 int grpo_dequantize_fp8(const uint8_t* codes, const float* scales, int64_t rows, int64_t cols,
                         int per_row, void* out, void* stream) {
-  g_last_error[0] = 0;
+  grpo::clear_error();
   GRPO_CHECK_PTR(codes);
   GRPO_CHECK_PTR(scales);
   GRPO_CHECK_PTR(out);
@@ -648,7 +649,7 @@ int grpo_ref_logprobs_fp8(const uint8_t* H8, const float* h_scale, const uint8_t
                           const float* w_scale, const int32_t* y, int64_t N, int64_t d, int64_t V,
                           int64_t chunk, const grpo_opts* opts, float* ref_lp, void* workspace,
                           size_t workspace_bytes, void* stream) {
-  g_last_error[0] = 0;
+  grpo::clear_error();
   grpo::LogitXform xf;
   grpo::LossVariant lv;
   if (make_xform(opts, &xf) != GRPO_OK || make_variant(opts, &lv) != GRPO_OK)
@@ -676,7 +677,7 @@ int grpo_loss_fwd_fp8(const uint8_t* H8, const float* h_scale, const uint8_t* W8
                       int64_t V, float beta, int64_t chunk, const grpo_opts* opts, float* loss,
                       float* lp, float* kl, float* lse, void* workspace, size_t workspace_bytes,
                       void* stream) {
-  g_last_error[0] = 0;
+  grpo::clear_error();
   grpo::LogitXform xf;
   grpo::LossVariant lv;
   if (make_xform(opts, &xf) != GRPO_OK || make_variant(opts, &lv) != GRPO_OK)
@@ -713,7 +714,7 @@ int grpo_loss_bwd_fp8(const uint8_t* H8, const float* h_scale, const uint8_t* W8
                       int64_t B, int64_t L, int64_t d, int64_t V, float beta, float grad_loss,
                       int64_t chunk, const grpo_opts* opts, void* dH, float* dW, void* workspace,
                       size_t workspace_bytes, void* stream) {
-  g_last_error[0] = 0;
+  grpo::clear_error();
   grpo::LogitXform xf;
   grpo::LossVariant lv;
   if (make_xform(opts, &xf) != GRPO_OK || make_variant(opts, &lv) != GRPO_OK)
@@ -807,7 +808,7 @@ int grpo_loss_fwd_noalloc(const void* H, const void* W, const int32_t* y, const 
                           const float* adv, const float* ref_lp, int64_t B, int64_t L, int64_t d,
                           int64_t V, int dtype, float beta, int64_t chunk, const grpo_opts* opts,
                           float* loss, float* lp, float* kl, float* lse, void* stream) {
-  g_last_error[0] = 0;
+  grpo::clear_error();
   if (B <= 0 || L <= 0) return fail(GRPO_ERR_INVALID_ARG, "B and L must be positive");
   if (B > INT32_MAX / L) return fail(GRPO_ERR_UNSUPPORTED, "B*L exceeds int32");
   const int st = check_shape(B * L, d, V, dtype, chunk);
@@ -829,7 +830,7 @@ int grpo_loss_fwd_noalloc(const void* H, const void* W, const int32_t* y, const 
 
 int grpo_gemm_nt(const void* A, const void* B, int64_t M, int64_t N, int64_t K, int dtype,
                  float* C, void* stream) {
-  g_last_error[0] = 0;
+  grpo::clear_error();
   GRPO_CHECK_PTR(A);
   GRPO_CHECK_PTR(B);
   GRPO_CHECK_PTR(C);

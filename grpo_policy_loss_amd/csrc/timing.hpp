@@ -27,6 +27,14 @@ enum KernelKind {
   KK_SEQ_COUNTS,
   KK_FP8_QUANT,
   KK_FP8_DEQUANT,
+  KK_NORM_FWD,
+  KK_NORM_BWD,
+  KK_NORM_REDUCE,
+  KK_ADAMW,
+  KK_MOMENT_VALUES,
+  KK_SAMPLE_MASS,
+  KK_SAMPLE_CUT,
+  KK_SAMPLE_PICK,
   KK_COUNT
 };
 

@@ -328,6 +328,34 @@ int grpo_loss_fwd_noalloc(const void* H, const void* W, const int32_t* y, const 
                           float* loss, float* lp, float* kl, float* lse, void* stream);
 
 /*
+ * The norm in front of the LM head, whose output is H and whose backward takes
+ * dH.  For each row x of X [rows, cols]:
+ *   mu = mean(x) (GRPO_NORM_LAYER; 0 for GRPO_NORM_RMS)
+ *   r  = 1 / sqrt(mean((x - mu)^2) + eps)
+ *   y  = (x - mu) r weight + bias
+ * grpo_norm_fwd: X, weight [cols], bias [cols] (NULL: none) and Y [rows, cols]
+ *   are `dtype` (GRPO_F32 or GRPO_BF16); mean and rstd [rows] are float32,
+ *   written (mean is not used for GRPO_NORM_RMS and may be NULL).  eps finite
+ *   and >= 0.
+ * grpo_norm_bwd: dY [rows, cols] the gradient of Y; X, weight, mean and rstd
+ *   as in the forward.  dX [rows, cols] dtype, OVERWRITTEN; dweight [cols] and
+ *   dbias [cols] (NULL: not formed) float32, ACCUMULATED (+=) as dW is in
+ *   grpo_loss_bwd.  workspace: grpo_norm_workspace_bytes(rows, cols, dtype),
+ *   256-byte aligned.
+ * Any cols from 1 to 2^24 and any element alignment.  Sums are float32, in a
+ * fixed order: results are bitwise reproducible.
+ */
+typedef enum { GRPO_NORM_LAYER = 0, GRPO_NORM_RMS = 1 } grpo_norm_kind;
+
+size_t grpo_norm_workspace_bytes(int64_t rows, int64_t cols, int dtype);
+int grpo_norm_fwd(const void* X, const void* weight, const void* bias, int64_t rows, int64_t cols,
+                  int dtype, int kind, float eps, void* Y, float* mean, float* rstd, void* stream);
+int grpo_norm_bwd(const void* dY, const void* X, const void* weight, const float* mean,
+                  const float* rstd, int64_t rows, int64_t cols, int dtype, int kind, void* dX,
+                  float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/*
  * Diagnostic: C[M, N] (float32, row-major, written) = A[M, K] . B[N, K]^T,
  * through the same MFMA tile main loop the loss kernels use (A, B dtype
  * elements, both rows contiguous along K).  K times the element size must be
