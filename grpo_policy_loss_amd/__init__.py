@@ -37,6 +37,12 @@ from ._lib import (  # noqa: F401
 from ._ops import (  # noqa: F401,E402
     NORM_LAYER,
     NORM_RMS,
+    AdamWPlan,
+    Moment8,
+    adamw_moments,
+    adamw_plan,
+    dequantize_moment,
+    grpo_adamw,
     grpo_norm_bwd,
     grpo_norm_fwd,
 )

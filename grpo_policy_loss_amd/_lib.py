@@ -38,6 +38,21 @@ AGG_TOKEN_MEAN, AGG_SEQUENCE_MEAN = 0, 1
 
 _OPTS_P = ctypes.POINTER(Opts)
 
+
+class AdamWTensor(ctypes.Structure):
+    """grpo_adamw_tensor."""
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("param", "grad", "master", "exp_avg", "exp_avg_sq", "exp_avg_scales",
+                 "exp_avg_sq_scales")] + [("n", ctypes.c_int64)]
+
+
+class AdamWOpts(ctypes.Structure):
+    """grpo_adamw_opts."""
+    _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay")] \
+        + [("step", ctypes.c_int64)] \
+        + [(name, ctypes.c_void_p) for name in ("step_dev", "lr_dev", "grad_scale")]
+
+
 # name -> (restype, argtypes); mirrors include/grpo.h
 SIGNATURES = {
     "grpo_workspace_bytes": (_sz, [_int, _i64, _i64, _i64, _int, _i64]),
@@ -71,6 +86,10 @@ SIGNATURES = {
     "grpo_norm_fwd": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _int, _f32, _vp, _vp, _vp, _vp]),
     "grpo_norm_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp,
                              _sz, _vp]),
+    "grpo_adamw_plan_bytes": (_sz, [_i64]),
+    "grpo_adamw_plan": (_int, [ctypes.POINTER(AdamWTensor), _i64, _int, _int, _int, _vp, _sz]),
+    "grpo_adamw": (_int, [_vp, _vp, ctypes.POINTER(AdamWOpts), _vp]),
+    "grpo_moment_values": (_int, [_vp, _vp, _i64, _int, _vp, _vp]),
     "grpo_timing_begin": (_int, []),
     "grpo_timing_end": (_int, [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(_int),
                                ctypes.POINTER(ctypes.c_double), _int]),

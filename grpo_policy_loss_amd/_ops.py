@@ -1,5 +1,5 @@
 """ctypes binding of the operators around the loss (include/grpo.h): the norm in
-front of the LM head.
+front of the LM head and the optimizer's step.
 
 Argument marshalling only, as in _lib.  Every call checks that its tensors share
 one GPU and runs on that GPU's current torch stream, whichever device is current.
@@ -7,10 +7,11 @@ one GPU and runs on that GPU's current torch stream, whichever device is current
 from __future__ import annotations
 
 import contextlib
+import ctypes
 
 import torch
 
-from ._lib import _arg, _check, _dev, _dt, _matrix, _ptr, lib
+from ._lib import (AdamWOpts, AdamWTensor, _arg, _check, _dev, _dt, _matrix, _ptr, lib)
 
 # grpo_norm_kind
 NORM_LAYER, NORM_RMS = 0, 1
@@ -95,3 +96,135 @@ def grpo_norm_bwd(dY, X, weight, mean, rstd, kind: int = NORM_RMS, bias: bool = 
             _ptr(dY), _ptr(X), _ptr(weight), _ptr(mean), _ptr(rstd), rows, cols, dt, kind,
             _ptr(dX), _ptr(dweight), _ptr(dbias), _ptr(ws), ws.numel(), stream))
     return dX, dweight, dbias
+
+
+# ---------------------------------------------------------------- AdamW
+QUANT_BLOCK = 256   # elements per scale of an 8-bit moment
+
+
+class Moment8:
+    """A moment in 8 bits: codes (int8 for the first moment, uint8 for the second, in
+    the parameter's shape) and one float32 scale per 256 elements."""
+
+    def __init__(self, codes, scales):
+        if codes.dtype not in (torch.int8, torch.uint8):
+            raise TypeError(f"codes must be int8 or uint8, got {codes.dtype}")
+        _arg(scales, "scales", dtype=torch.float32, numel=-(-codes.numel() // QUANT_BLOCK))
+        self.codes, self.scales = codes, scales
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+
+def dequantize_moment(q: Moment8, out=None):
+    """grpo_moment_values: the float32 values of q."""
+    out = torch.empty(q.codes.shape, dtype=torch.float32, device=q.codes.device) if out is None \
+        else _arg(out, "out", dtype=torch.float32, numel=q.codes.numel())
+    ctx, stream = _on(q.codes, q.scales, out)
+    with ctx:
+        _check("grpo_moment_values", lib().grpo_moment_values(
+            _ptr(q.codes), _ptr(q.scales), q.codes.numel(), int(q.codes.dtype == torch.uint8),
+            _ptr(out), stream))
+    return out
+
+
+def adamw_moments(params, bits: int = 32):
+    """The moments before the first step: (exp_avg, exp_avg_sq), lists of float32 zeros
+    (bits 32) or of Moment8 zeros (bits 8) for each parameter."""
+    if bits not in (8, 32):
+        raise ValueError(f"bits must be 8 or 32, got {bits}")
+
+    def zeros(p, dtype):
+        if bits == 32:
+            return torch.zeros(p.shape, dtype=torch.float32, device=p.device)
+        return Moment8(torch.zeros(p.shape, dtype=dtype, device=p.device),
+                       torch.zeros(-(-p.numel() // QUANT_BLOCK), device=p.device))
+    return [zeros(p, torch.int8) for p in params], [zeros(p, torch.uint8) for p in params]
+
+
+class AdamWPlan:
+    """What grpo_adamw needs of its tensors, made once by adamw_plan.  It keeps the
+    tensors' memory alive and holds their addresses: a parameter or gradient that is
+    replaced (p.data = ..., zero_grad(set_to_none=True)) needs a new plan."""
+
+    def __init__(self, tensors, params, image, table):
+        self.tensors, self.image, self.table = tensors, image, table
+        self.versioned = [p for p in params if not p.is_inference()]
+        self.device = table.device
+        self.stream = torch.cuda.current_stream(self.device).cuda_stream
+
+
+def adamw_plan(params, grads, exp_avg, exp_avg_sq, master=None) -> AdamWPlan:
+    """The plan of an AdamW step over lists of tensors of one GPU: params (all float32 or
+    all bfloat16), grads (all float32 or all bfloat16, in the parameters' sizes), the
+    moments (float32 tensors, or Moment8) and optionally float32 masters of bfloat16
+    parameters.  Tensors that share memory are refused."""
+    params, grads, exp_avg, exp_avg_sq = (list(x) for x in (params, grads, exp_avg, exp_avg_sq))
+    master = None if master is None else list(master)
+    if not params:
+        raise ValueError("params is empty")
+    for name, x in (("grads", grads), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq),
+                    ("master", master)):
+        if x is not None and len(x) != len(params):
+            raise ValueError(f"{name} has {len(x)} tensors, params has {len(params)}")
+    eight = isinstance(exp_avg[0], Moment8)
+    _arg(params[0], "params[0]")
+    _arg(grads[0], "grads[0]")
+    pt, gt = _dt(params[0]), _dt(grads[0])
+    rows, keep = (AdamWTensor * len(params))(), []
+    for i, (p, g, m, v) in enumerate(zip(params, grads, exp_avg, exp_avg_sq)):
+        _arg(p, f"params[{i}]", dtype=params[0].dtype)
+        n = p.numel()
+        parts = {"param": p, "grad": _arg(g, f"grads[{i}]", dtype=grads[0].dtype, numel=n)}
+        if master is not None:
+            parts["master"] = _arg(master[i], f"master[{i}]", dtype=torch.float32, numel=n)
+        for name, x, dtype in (("exp_avg", m, torch.int8), ("exp_avg_sq", v, torch.uint8)):
+            if isinstance(x, Moment8) != eight:
+                raise TypeError("the moments must be all float32 tensors or all Moment8")
+            if eight:
+                parts[name] = _arg(x.codes, f"{name}[{i}].codes", dtype=dtype, numel=n)
+                parts[name + "_scales"] = x.scales
+            else:
+                parts[name] = _arg(x, f"{name}[{i}]", dtype=torch.float32, numel=n)
+        keep.append(tuple(t.detach() for t in parts.values()))
+        rows[i].n = n
+        for name, t in parts.items():
+            setattr(rows[i], name, t.data_ptr())
+    ctx, _ = _on(*(t for row in keep for t in row))
+    size = int(lib().grpo_adamw_plan_bytes(len(params)))
+    image = (ctypes.c_uint8 * size)()
+    _check("grpo_adamw_plan", lib().grpo_adamw_plan(rows, len(params), pt, gt, 8 if eight else 32,
+                                                    image, size))
+    with ctx:
+        # a copy from pageable memory: it has arrived when the call returns
+        table = torch.frombuffer(image, dtype=torch.uint8).to(params[0].device)
+        return AdamWPlan(keep, params, image, table)
+
+
+def _scalar(x, name, dtype):
+    """A device scalar's tensor, or None for a host number."""
+    return _arg(x, name, dtype=dtype, numel=1) if isinstance(x, torch.Tensor) else None
+
+
+def grpo_adamw(plan: AdamWPlan, step, lr=1e-6, betas=(0.9, 0.999), eps: float = 1e-8,
+               weight_decay: float = 0.01, grad_scale=None):
+    """One AdamW step of the plan's tensors, in place, in one launch.  step counts from 1;
+    a tensor for step (int64, one element) or lr (float32, one element) is read when the
+    kernel runs, so a captured step follows it.  grad_scale: a float32 tensor of one
+    element that multiplies every gradient (a clipping factor), or None.  Gradients are
+    left as they are.  A captured graph needs the plan to live as long as it does."""
+    step_dev, lr_dev = _scalar(step, "step", torch.int64), _scalar(lr, "lr", torch.float32)
+    if grad_scale is not None:
+        _arg(grad_scale, "grad_scale", dtype=torch.float32, numel=1)
+    ctx, stream = _on(*(t for t in (plan.table, step_dev, lr_dev, grad_scale) if t is not None))
+    opts = AdamWOpts(0.0 if lr_dev is not None else lr, betas[0], betas[1], eps, weight_decay,
+                     0 if step_dev is not None else step, _ptr(step_dev), _ptr(lr_dev),
+                     _ptr(grad_scale))
+    with ctx:
+        if stream != plan.stream:   # the allocator must not hand the table on too early
+            plan.table.record_stream(torch.cuda.current_stream(plan.device))
+        _check("grpo_adamw", lib().grpo_adamw(plan.image, _ptr(plan.table), ctypes.byref(opts),
+                                              stream))
+    # autograd has to see that the parameters changed
+    torch.autograd.graph.increment_version(plan.versioned)

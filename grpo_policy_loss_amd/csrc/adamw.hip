@@ -1,0 +1,482 @@
+// adamw.hip -- one AdamW step over many tensors in one launch.
+//
+// For every element, step t >= 1, g the gradient times an optional scale:
+//   m = b1 m + (1 - b1) g          v = b2 v + (1 - b2) g^2
+//   w = w - lr wd w - lr / (1 - b1^t) * m / (sqrt(v / (1 - b2^t)) + eps)
+// w is the float32 master where there is one (the parameter is then its rounding), else the
+// parameter.  The moments are float32, or 8-bit codes in blocks of 256 elements of one
+// tensor with one float32 scale a = max |value| each:
+//   m = sign(c) (c / 127)^2 a,  c = sign(m) floor(127 sqrt(|m| / a) + 1/2)
+//   v = (c / 255)^4 a,          c = floor(255 (v / a)^(1/4) + 1/2), at least 1 where v > 0
+// The powers spend the codes on the small values of a block: m spans 16129 : 1 and sqrt(v),
+// which is what divides, 65025 : 1.  A positive v never reads back as 0, so the quotient
+// never sees a zero under a live m.  A block with a value that is not finite has the scale
+// NaN, so all of it reads back as NaN.
+//
+// The step is bound by memory: 12 to 30 bytes in and out per element against some 20 (32-bit
+// moments) to 60 instructions (8-bit).  One block takes a chunk of 4096 elements of one tensor, 4 elements a
+// lane and load, all loads of the chunk issued before its first use.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "api.hpp"
+#include "elem.hpp"
+#include "timing.hpp"
+
+namespace grpo {
+namespace {
+
+constexpr int kChunk = 4096;        // elements per block of 256 threads
+constexpr int kSteps = kChunk / 1024;
+constexpr int kQuantBlock = 256;    // elements per scale: one wave's load
+
+// The image of a plan: this header, the tensors, then the first chunk of each tensor.
+struct PlanHeader {
+  uint64_t magic;
+  int64_t count, chunks;
+  int32_t param_dtype, grad_dtype, bits, master;
+  int64_t o_tensors, o_first;
+};
+constexpr uint64_t kMagic = 0x314e414c50574441ull;
+
+struct Hyper {
+  double b1, b2, log_b1, log_b2;
+  float lr, wd, eps;
+  float step_size, inv_bc2;      // of the host's step and lr
+  const int64_t* step_dev;       // non-null: the step is read here
+  const float* lr_dev;
+  const float* grad_scale;
+};
+
+template <typename T> struct Vec4;
+template <> struct Vec4<float> {
+  typedef __attribute__((ext_vector_type(4), aligned(4))) float type;
+};
+template <> struct Vec4<__bf16> {
+  typedef __attribute__((ext_vector_type(4), aligned(2))) __bf16 type;
+};
+template <> struct Vec4<int8_t> {
+  typedef __attribute__((ext_vector_type(4), aligned(1))) int8_t type;
+};
+template <> struct Vec4<uint8_t> {
+  typedef __attribute__((ext_vector_type(4), aligned(1))) uint8_t type;
+};
+
+// Elements [e, e + 4) of n; those at n and behind it read as zero and are not written.
+template <typename T>
+__device__ __forceinline__ typename Vec4<T>::type load4(const T* p, int64_t e, int64_t n) {
+  typedef typename Vec4<T>::type V;
+  if (e + 4 <= n) return *(const V*)(p + e);
+  V v = {};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (e + j < n) v[j] = p[e + j];
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, int64_t e, int64_t n, typename Vec4<T>::type v) {
+  typedef typename Vec4<T>::type V;
+  if (e + 4 <= n) {
+    *(V*)(p + e) = v;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (e + j < n) p[e + j] = v[j];
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
+// The last tensor whose first chunk is <= chunk: a 64-way search, one load per level.
+// (A tensor of no elements has the first chunk of the next one and is never the last.)
+__device__ __forceinline__ int owner_of(const int64_t* __restrict__ first, int count,
+                                        int64_t chunk) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, len = count;
+  while (len > 1) {
+    const int stride = (len + 63) / 64;
+    const bool le = lane * stride < len && first[lo + lane * stride] <= chunk;
+    const int k = __popcll(__ballot(le)) - 1;
+    lo += k * stride;
+    len = min(stride, len - k * stride);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// The codes of a value q = (|m| / a) 127^2 or (v / a) 255^4, exactly: a candidate from float32
+// roots, moved to the side of the borders (c -+ 1/2)^k that the float64 q is on.  A float32
+// root alone would put one value in about 10^5 on the wrong side.
+__device__ __forceinline__ int code_m(double q) {
+  const float c = rintf(sqrtf((float)q));
+  const double up = (double)c + 0.5, dn = (double)c - 0.5;
+  int k = (int)c + (q >= up * up ? 1 : 0) - (c > 0.f && q < dn * dn ? 1 : 0);
+  return min(k, 127);
+}
+__device__ __forceinline__ int code_v(double q) {
+  const float c = rintf(sqrtf(sqrtf((float)q)));
+  const double up = ((double)c + 0.5) * ((double)c + 0.5), dn = ((double)c - 0.5) * ((double)c - 0.5);
+  int k = (int)c + (q >= up * up ? 1 : 0) - (c > 0.f && q < dn * dn ? 1 : 0);
+  return min(max(k, q > 0.0 ? 1 : 0), 255);
+}
+
+__device__ __forceinline__ double value_m(int c, double unit) {
+  return (double)(c * abs(c)) * unit;          // unit = a / 127^2
+}
+__device__ __forceinline__ double value_v(unsigned c, double unit) {
+  return (double)(c * c * c * c) * unit;       // unit = a / 255^4; 255^4 < 2^32
+}
+
+template <typename P, typename G, int BITS, bool MASTER>
+__global__ void __launch_bounds__(256)
+    k_adamw(const grpo_adamw_tensor* __restrict__ tensors, const int64_t* __restrict__ first,
+            int count, Hyper h) {
+  const int64_t chunk = blockIdx.x;
+  const int at = owner_of(first, count, chunk);
+  const grpo_adamw_tensor t = tensors[at];
+  const int64_t n = t.n, base = (chunk - first[at]) * kChunk;
+  P* param = (P*)t.param;
+  const G* grad = (const G*)t.grad;
+  float* master = (float*)t.master;
+
+  typename Vec4<P>::type p[kSteps];
+  typename Vec4<G>::type g[kSteps];
+  typename Vec4<float>::type w[kSteps], m[kSteps], v[kSteps];
+  typename Vec4<int8_t>::type mc[kSteps];
+  typename Vec4<uint8_t>::type vc[kSteps];
+  float ma[kSteps], va[kSteps];
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    const int64_t e = base + (k * 256 + threadIdx.x) * 4;
+    g[k] = load4(grad, e, n);
+    if constexpr (MASTER) w[k] = load4(master, e, n);
+    else p[k] = load4(param, e, n);
+    if constexpr (BITS == 32) {
+      m[k] = load4((const float*)t.exp_avg, e, n);
+      v[k] = load4((const float*)t.exp_avg_sq, e, n);
+    } else {
+      mc[k] = load4((const int8_t*)t.exp_avg, e, n);
+      vc[k] = load4((const uint8_t*)t.exp_avg_sq, e, n);
+      const int64_t b = e / kQuantBlock;      // one scale per wave and step
+      ma[k] = e < n ? t.exp_avg_scales[b] : 0.f;
+      va[k] = e < n ? t.exp_avg_sq_scales[b] : 0.f;
+    }
+  }
+
+  float step_size = h.step_size, inv_bc2 = h.inv_bc2, lr = h.lr;
+  if (h.lr_dev != nullptr) lr = *h.lr_dev;
+  if (h.lr_dev != nullptr || h.step_dev != nullptr) {
+    // 1 - b^t = -expm1(t log b), the product in float64: 1 - b^t loses nothing near b = 1
+    const int64_t s = h.step_dev != nullptr ? *h.step_dev : 0;
+    if (h.step_dev != nullptr) {
+      const double td = (double)(s < 1 ? 1 : s);
+      step_size = lr / -expm1f((float)(td * h.log_b1));
+      inv_bc2 = 1.f / -expm1f((float)(td * h.log_b2));
+    } else {
+      step_size = lr * h.step_size;            // the host passed 1 / (1 - b1^t)
+    }
+  }
+  const float scale = h.grad_scale != nullptr ? *h.grad_scale : 1.f;
+  const float decay = lr * h.wd;
+  const float b1 = (float)h.b1, b2 = (float)h.b2, a1 = (float)(1.0 - h.b1), a2 = (float)(1.0 - h.b2);
+
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    const int64_t e = base + (k * 256 + threadIdx.x) * 4;
+    float nm[4], nv[4];
+    double dm[4], dv[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (BITS == 32) {
+        const float x = (float)g[k][j] * scale;
+        nm[j] = m[k][j] * b1 + x * a1;
+        nv[j] = v[k][j] * b2 + x * x * a2;
+      } else {
+        // float64, so that the new codes are those of the exact moments
+        const double x = (double)(float)g[k][j] * (double)scale;
+        dm[j] = value_m(mc[k][j], (double)ma[k] * (1.0 / 16129.0)) * h.b1 + x * (1.0 - h.b1);
+        dv[j] = value_v(vc[k][j], (double)va[k] * (1.0 / 4228250625.0)) * h.b2 + x * x * (1.0 - h.b2);
+        nm[j] = (float)dm[j];
+        nv[j] = (float)dv[j];
+      }
+    }
+    typename Vec4<P>::type np;
+    typename Vec4<float>::type nw;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float old;
+      if constexpr (MASTER) old = w[k][j];
+      else old = (float)p[k][j];
+      nw[j] = (old - decay * old) - step_size * (nm[j] / (sqrtf(nv[j] * inv_bc2) + h.eps));
+      np[j] = (P)nw[j];
+    }
+    store4(param, e, n, np);
+    if constexpr (MASTER) store4(master, e, n, nw);
+    if constexpr (BITS == 32) {
+      store4((float*)t.exp_avg, e, n, typename Vec4<float>::type{nm[0], nm[1], nm[2], nm[3]});
+      store4((float*)t.exp_avg_sq, e, n, typename Vec4<float>::type{nv[0], nv[1], nv[2], nv[3]});
+    } else {
+      // lanes behind n hold zeros and zero codes
+      float top_m = 0.f, top_v = 0.f;
+      bool bad_m = false, bad_v = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        top_m = fmaxf(top_m, fabsf(nm[j]));
+        top_v = fmaxf(top_v, nv[j]);
+        bad_m |= !(fabsf(nm[j]) <= 3.402823466e38f);
+        bad_v |= !(nv[j] <= 3.402823466e38f);
+      }
+      top_m = wave_max(top_m);
+      top_v = wave_max(top_v);
+      bad_m = __any(bad_m);
+      bad_v = __any(bad_v);
+      const bool on_m = !bad_m && top_m > 0.f, on_v = !bad_v && top_v > 0.f;
+      const double to_m = on_m ? 16129.0 / (double)top_m : 0.0;
+      const double to_v = on_v ? 4228250625.0 / (double)top_v : 0.0;
+      typename Vec4<int8_t>::type cm = {};
+      typename Vec4<uint8_t>::type cv = {};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (on_m) {
+          const int c = code_m(fabs(dm[j]) * to_m);
+          cm[j] = (int8_t)(dm[j] < 0.0 ? -c : c);
+        }
+        if (on_v) cv[j] = (uint8_t)code_v(dv[j] * to_v);
+      }
+      store4((int8_t*)t.exp_avg, e, n, cm);
+      store4((uint8_t*)t.exp_avg_sq, e, n, cv);
+      if ((threadIdx.x & 63) == 0 && e < n) {
+        t.exp_avg_scales[e / kQuantBlock] = bad_m ? __builtin_nanf("") : top_m;
+        t.exp_avg_sq_scales[e / kQuantBlock] = bad_v ? __builtin_nanf("") : top_v;
+      }
+    }
+  }
+}
+
+// The float32 values of 8-bit moments.
+template <typename C>
+__global__ void __launch_bounds__(256)
+    k_moment_values(const C* __restrict__ codes, const float* __restrict__ scales, int64_t n,
+                    float* __restrict__ out) {
+  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (e >= n) return;
+  const typename Vec4<C>::type c = load4(codes, e, n);
+  const double a = (double)scales[e / kQuantBlock];
+  typename Vec4<float>::type o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    o[j] = sizeof(C) == 1 && (C)-1 < (C)0 ? (float)value_m((int)c[j], a * (1.0 / 16129.0))
+                                          : (float)value_v((unsigned)c[j], a * (1.0 / 4228250625.0));
+  store4(out, e, n, o);
+}
+
+template <typename P, typename G, bool MASTER>
+void launch_adamw(const PlanHeader& hd, const char* plan, const Hyper& h, hipStream_t s) {
+  const auto* tensors = (const grpo_adamw_tensor*)(plan + hd.o_tensors);
+  const auto* first = (const int64_t*)(plan + hd.o_first);
+  if (hd.bits == 32)
+    k_adamw<P, G, 32, MASTER><<<(unsigned)hd.chunks, 256, 0, s>>>(tensors, first, (int)hd.count, h);
+  else
+    k_adamw<P, G, 8, MASTER><<<(unsigned)hd.chunks, 256, 0, s>>>(tensors, first, (int)hd.count, h);
+}
+
+size_t image_bytes(int64_t count) {
+  return align_up(sizeof(PlanHeader)) + align_up((size_t)count * sizeof(grpo_adamw_tensor)) +
+         align_up((size_t)count * sizeof(int64_t));
+}
+
+struct Range {
+  uintptr_t from, to;
+  bool written;
+};
+
+// Two ranges that share a byte, one of them written, would race.
+bool any_overlap(std::vector<Range>& r) {
+  std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
+  uintptr_t read_end = 0, write_end = 0;
+  for (const Range& x : r) {
+    if (x.from < write_end || (x.written && x.from < read_end)) return true;
+    (x.written ? write_end : read_end) = std::max(x.written ? write_end : read_end, x.to);
+  }
+  return false;
+}
+
+constexpr int64_t kMaxTensors = 1 << 24;
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;   // a grid of 256-thread blocks stays below 2^32 threads
+
+int fill_plan(const grpo_adamw_tensor* tensors, int64_t count, int param_dtype, int grad_dtype,
+              int bits, char* image) {
+  const size_t ps = param_dtype == GRPO_F32 ? 4 : 2, gs = grad_dtype == GRPO_F32 ? 4 : 2;
+  std::vector<Range> ranges;
+  ranges.reserve((size_t)count * 7);
+  PlanHeader hd{kMagic, count, 0, param_dtype, grad_dtype, bits, 0, 0, 0};
+  hd.o_tensors = (int64_t)align_up(sizeof(PlanHeader));
+  hd.o_first = hd.o_tensors + (int64_t)align_up((size_t)count * sizeof(grpo_adamw_tensor));
+  auto* first = (int64_t*)(image + hd.o_first);
+  int64_t with = 0, without = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const grpo_adamw_tensor& t = tensors[i];
+    first[i] = hd.chunks;
+    if (t.n < 0 || t.n > (int64_t)1 << 48)
+      return fail(GRPO_ERR_INVALID_ARG, "tensor %lld has %lld elements", (long long)i,
+                  (long long)t.n);
+    if (t.n == 0) continue;
+    const size_t n = (size_t)t.n, ss = (n + kQuantBlock - 1) / kQuantBlock * 4;
+    const struct {
+      const void* p;
+      size_t bytes, align;
+      bool written, needed;
+      const char* name;
+    } parts[] = {{t.param, n * ps, ps, true, true, "param"},
+                 {t.grad, n * gs, gs, false, true, "grad"},
+                 {t.master, n * 4, 4, true, false, "master"},
+                 {t.exp_avg, n * (bits / 8), (size_t)bits / 8, true, true, "exp_avg"},
+                 {t.exp_avg_sq, n * (bits / 8), (size_t)bits / 8, true, true, "exp_avg_sq"},
+                 {t.exp_avg_scales, ss, 4, true, bits == 8, "exp_avg_scales"},
+                 {t.exp_avg_sq_scales, ss, 4, true, bits == 8, "exp_avg_sq_scales"}};
+    for (const auto& q : parts) {
+      if (q.p == nullptr && q.needed)
+        return fail(GRPO_ERR_INVALID_ARG, "null pointer: %s of tensor %lld", q.name, (long long)i);
+      if (q.p == nullptr || (bits == 32 && &q >= &parts[5])) continue;
+      const uintptr_t from = (uintptr_t)q.p;
+      if (from % q.align != 0)
+        return fail(GRPO_ERR_INVALID_ARG, "%s of tensor %lld is not aligned to its elements",
+                    q.name, (long long)i);
+      ranges.push_back({from, from + q.bytes, q.written});
+    }
+    (t.master != nullptr ? with : without) += 1;
+    hd.chunks += (t.n + kChunk - 1) / kChunk;
+  }
+  if (with != 0 && without != 0)
+    return fail(GRPO_ERR_INVALID_ARG, "%lld tensors have a master and %lld have none: all or none",
+                (long long)with, (long long)without);
+  if (with != 0 && param_dtype == GRPO_F32)
+    return fail(GRPO_ERR_INVALID_ARG, "a float32 parameter takes no master");
+  if (hd.chunks > kMaxBlocks)
+    return fail(GRPO_ERR_UNSUPPORTED, "more than 2^24 - 1 chunks of %d elements", kChunk);
+  if (any_overlap(ranges))
+    return fail(GRPO_ERR_INVALID_ARG, "two of the tensors overlap (the same one twice?)");
+  hd.master = with != 0;
+  memcpy(image, &hd, sizeof hd);
+  if (count > 0) memcpy(image + hd.o_tensors, tensors, (size_t)count * sizeof(grpo_adamw_tensor));
+  return GRPO_OK;
+}
+
+}  // namespace
+}  // namespace grpo
+
+using grpo::fail;
+
+extern "C" {
+
+size_t grpo_adamw_plan_bytes(int64_t count) {
+  return count < 0 || count > grpo::kMaxTensors ? 0 : grpo::image_bytes(count);
+}
+
+int grpo_adamw_plan(const grpo_adamw_tensor* tensors, int64_t count, int param_dtype,
+                    int grad_dtype, int state_bits, void* image, size_t image_bytes) {
+  grpo::clear_error();
+  if (count < 0 || count > grpo::kMaxTensors)
+    return fail(GRPO_ERR_INVALID_ARG, "count %lld is not in [0, 2^24]", (long long)count);
+  if (count > 0) GRPO_CHECK_PTR(tensors);
+  GRPO_CHECK_PTR(image);
+  for (int dt : {param_dtype, grad_dtype})
+    if (dt != GRPO_F32 && dt != GRPO_BF16)
+      return fail(GRPO_ERR_INVALID_ARG, "dtype %d is neither GRPO_F32 nor GRPO_BF16", dt);
+  if (state_bits != 8 && state_bits != 32)
+    return fail(GRPO_ERR_INVALID_ARG, "state_bits %d is neither 8 nor 32", state_bits);
+  if (image_bytes < grpo::image_bytes(count))
+    return fail(GRPO_ERR_WORKSPACE, "the plan's image needs %zu bytes, got %zu",
+                grpo::image_bytes(count), image_bytes);
+  try {
+    return grpo::fill_plan(tensors, count, param_dtype, grad_dtype, state_bits, (char*)image);
+  } catch (const std::bad_alloc&) {
+    return fail(GRPO_ERR_WORKSPACE, "out of host memory");
+  }
+}
+
+int grpo_adamw(const void* image, const void* plan, const grpo_adamw_opts* opts, void* stream) {
+  grpo::clear_error();
+  GRPO_CHECK_PTR(image);
+  GRPO_CHECK_PTR(opts);
+  grpo::PlanHeader hd;
+  memcpy(&hd, image, sizeof hd);
+  if (hd.magic != grpo::kMagic)
+    return fail(GRPO_ERR_INVALID_ARG, "image was not filled by grpo_adamw_plan");
+  const grpo_adamw_opts& o = *opts;
+  const double nonneg[] = {o.lr, o.eps, o.weight_decay};
+  for (double x : nonneg)
+    if (!isfinite(x) || x < 0.0)
+      return fail(GRPO_ERR_INVALID_ARG, "lr, eps and weight_decay must be finite and >= 0 "
+                  "(%g, %g, %g)", o.lr, o.eps, o.weight_decay);
+  if (!(o.beta1 >= 0.0 && o.beta1 < 1.0 && o.beta2 >= 0.0 && o.beta2 < 1.0))
+    return fail(GRPO_ERR_INVALID_ARG, "betas must be in [0, 1) (%g, %g)", o.beta1, o.beta2);
+  if (o.step_dev == nullptr && o.step < 1)
+    return fail(GRPO_ERR_INVALID_ARG, "step %lld: the first step is 1", (long long)o.step);
+  if (hd.chunks == 0) return GRPO_OK;
+  GRPO_CHECK_PTR(plan);
+  grpo::Hyper h{};
+  h.b1 = o.beta1;
+  h.b2 = o.beta2;
+  h.log_b1 = log(o.beta1);
+  h.log_b2 = log(o.beta2);
+  h.lr = (float)o.lr;
+  h.wd = (float)o.weight_decay;
+  h.eps = (float)o.eps;
+  h.step_dev = o.step_dev;
+  h.lr_dev = o.lr_dev;
+  h.grad_scale = o.grad_scale;
+  if (o.step_dev == nullptr) {
+    const double bc1 = -expm1((double)o.step * h.log_b1), bc2 = -expm1((double)o.step * h.log_b2);
+    h.step_size = (float)((o.lr_dev != nullptr ? 1.0 : o.lr) / bc1);
+    h.inv_bc2 = (float)(1.0 / bc2);
+  }
+  hipStream_t s = (hipStream_t)stream;
+  grpo::ScopedKernelTimer timer(grpo::KK_ADAMW, s);
+  const char* p = (const char*)plan;
+  if (hd.param_dtype == GRPO_F32) {
+    if (hd.grad_dtype == GRPO_F32) grpo::launch_adamw<float, float, false>(hd, p, h, s);
+    else grpo::launch_adamw<float, __bf16, false>(hd, p, h, s);
+  } else if (hd.master) {
+    if (hd.grad_dtype == GRPO_F32) grpo::launch_adamw<__bf16, float, true>(hd, p, h, s);
+    else grpo::launch_adamw<__bf16, __bf16, true>(hd, p, h, s);
+  } else {
+    if (hd.grad_dtype == GRPO_F32) grpo::launch_adamw<__bf16, float, false>(hd, p, h, s);
+    else grpo::launch_adamw<__bf16, __bf16, false>(hd, p, h, s);
+  }
+  GRPO_HIP(hipGetLastError());
+  return GRPO_OK;
+}
+
+int grpo_moment_values(const void* codes, const float* scales, int64_t n, int squared, float* out,
+                       void* stream) {
+  grpo::clear_error();
+  if (n < 0) return fail(GRPO_ERR_INVALID_ARG, "n must not be negative");
+  if (squared != 0 && squared != 1)
+    return fail(GRPO_ERR_INVALID_ARG, "squared must be 0 or 1");
+  if (n == 0) return GRPO_OK;
+  GRPO_CHECK_PTR(codes);
+  GRPO_CHECK_PTR(scales);
+  GRPO_CHECK_PTR(out);
+  const int64_t blocks = (n + 1023) / 1024;
+  if (blocks > grpo::kMaxBlocks) return fail(GRPO_ERR_UNSUPPORTED, "n is too large");
+  hipStream_t s = (hipStream_t)stream;
+  grpo::ScopedKernelTimer timer(grpo::KK_MOMENT_VALUES, s);
+  if (squared)
+    grpo::k_moment_values<uint8_t><<<(unsigned)blocks, 256, 0, s>>>((const uint8_t*)codes, scales,
+                                                                    n, out);
+  else
+    grpo::k_moment_values<int8_t><<<(unsigned)blocks, 256, 0, s>>>((const int8_t*)codes, scales, n,
+                                                                   out);
+  GRPO_HIP(hipGetLastError());
+  return GRPO_OK;
+}
+
+}  // extern "C"

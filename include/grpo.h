@@ -356,6 +356,72 @@ int grpo_norm_bwd(const void* dY, const void* X, const void* weight, const float
                   void* stream);
 
 /*
+ * One AdamW step over many tensors in one launch; the consumer of
+ * grpo_loss_bwd's dW and grpo_norm_bwd's dweight.  For every element, with
+ * g = grad * grad_scale and step t >= 1:
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   w = w - lr weight_decay w - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * w is the float32 master where there is one (all tensors have one, or none),
+ * and param its rounding; else w is param itself.
+ *
+ * grpo_adamw_plan (host only) checks the tensors and writes the step's table
+ *   into the HOST buffer `image` of grpo_adamw_plan_bytes(count) bytes.  The
+ *   caller copies image to device memory once (8-byte aligned) and passes
+ *   both to every grpo_adamw: image is read on the host during the call, plan
+ *   (the device copy) by the kernel.  Both hold the tensors' addresses: a tensor that
+ *   moves needs a new plan.  Tensors that share memory (one twice) are
+ *   refused; n = 0 is allowed.
+ *   param_dtype, grad_dtype: GRPO_F32 or GRPO_BF16, the same for all tensors;
+ *   a master goes with bfloat16 parameters only.
+ *   state_bits 32: exp_avg and exp_avg_sq are float32 [n] (scales unused).
+ *   state_bits 8: exp_avg is int8 [n], exp_avg_sq uint8 [n], with one float32
+ *   scale a per 256 elements of the tensor (scales [ceil(n / 256)]), the
+ *   largest |value| of the block (NaN if one is not finite):
+ *     exp_avg    = sign(c) (c / 127)^2 a,  c rounded from 127 sqrt(|m| / a)
+ *     exp_avg_sq = (c / 255)^4 a,          c rounded from 255 (v / a)^(1/4),
+ *                                          at least 1 where v > 0
+ *   All zeros is the state before the first step.  The new codes are those of
+ *   the moments in float64; the weights use the moments before their rounding to
+ *   codes.
+ * grpo_adamw: betas in [0, 1); lr, eps and weight_decay finite and >= 0; step
+ *   the number of this step, from 1.  Device-side values, each read when the
+ *   kernel runs if non-NULL (for a step under graph capture): step_dev [1] int64
+ *   in place of step (below 1 counts as 1), lr_dev [1] float32 in place of lr,
+ *   grad_scale [1] float32 (NULL: 1).
+ * grpo_moment_values: the float32 values of 8-bit codes (squared = 0: exp_avg's
+ *   int8, 1: exp_avg_sq's uint8).
+ */
+typedef struct grpo_adamw_tensor {
+  void* param;
+  const void* grad;
+  float* master;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scales;
+  float* exp_avg_sq_scales;
+  int64_t n;
+} grpo_adamw_tensor;
+
+typedef struct grpo_adamw_opts {
+  double lr;
+  double beta1;
+  double beta2;
+  double eps;
+  double weight_decay;
+  int64_t step;
+  const int64_t* step_dev;
+  const float* lr_dev;
+  const float* grad_scale;
+} grpo_adamw_opts;
+
+size_t grpo_adamw_plan_bytes(int64_t count);
+int grpo_adamw_plan(const grpo_adamw_tensor* tensors, int64_t count, int param_dtype,
+                    int grad_dtype, int state_bits, void* image, size_t image_bytes);
+int grpo_adamw(const void* image, const void* plan, const grpo_adamw_opts* opts, void* stream);
+int grpo_moment_values(const void* codes, const float* scales, int64_t n, int squared, float* out,
+                       void* stream);
+
+/*
  * Diagnostic: C[M, N] (float32, row-major, written) = A[M, K] . B[N, K]^T,
  * through the same MFMA tile main loop the loss kernels use (A, B dtype
  * elements, both rows contiguous along K).  K times the element size must be
