@@ -45,5 +45,6 @@ from ._ops import (  # noqa: F401,E402
     grpo_adamw,
     grpo_norm_bwd,
     grpo_norm_fwd,
+    grpo_sample,
 )
 from .autograd import grpo_loss, grpo_norm  # noqa: F401,E402

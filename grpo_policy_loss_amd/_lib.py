@@ -53,6 +53,14 @@ class AdamWOpts(ctypes.Structure):
         + [(name, ctypes.c_void_p) for name in ("step_dev", "lr_dev", "grad_scale")]
 
 
+class SampleOpts(ctypes.Structure):
+    """grpo_sample_opts."""
+    _fields_ = [(name, ctypes.c_double) for name in ("temperature", "top_p", "min_p")] \
+        + [(name, ctypes.c_int32) for name in ("top_k", "reserved")] \
+        + [(name, ctypes.c_void_p) for name in
+           ("temperature_rows", "top_p_rows", "min_p_rows", "top_k_rows")]
+
+
 # name -> (restype, argtypes); mirrors include/grpo.h
 SIGNATURES = {
     "grpo_workspace_bytes": (_sz, [_int, _i64, _i64, _i64, _int, _i64]),
@@ -90,6 +98,9 @@ SIGNATURES = {
     "grpo_adamw_plan": (_int, [ctypes.POINTER(AdamWTensor), _i64, _int, _int, _int, _vp, _sz]),
     "grpo_adamw": (_int, [_vp, _vp, ctypes.POINTER(AdamWOpts), _vp]),
     "grpo_moment_values": (_int, [_vp, _vp, _i64, _int, _vp, _vp]),
+    "grpo_sample_workspace_bytes": (_sz, [_i64, _i64]),
+    "grpo_sample": (_int, [_vp, _int, _i64, _i64, _i64, _vp, ctypes.POINTER(SampleOpts), _vp, _vp,
+                           _vp, _sz, _vp]),
     "grpo_timing_begin": (_int, []),
     "grpo_timing_end": (_int, [ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(_int),
                                ctypes.POINTER(ctypes.c_double), _int]),

@@ -1,5 +1,5 @@
 """ctypes binding of the operators around the loss (include/grpo.h): the norm in
-front of the LM head and the optimizer's step.
+front of the LM head, the optimizer's step and the sampling of tokens.
 
 Argument marshalling only, as in _lib.  Every call checks that its tensors share
 one GPU and runs on that GPU's current torch stream, whichever device is current.
@@ -11,15 +11,20 @@ import ctypes
 
 import torch
 
-from ._lib import (AdamWOpts, AdamWTensor, _arg, _check, _dev, _dt, _matrix, _ptr, lib)
+from ._lib import (AdamWOpts, AdamWTensor, SampleOpts, _arg, _check, _dev, _dt, _matrix, _ptr, lib)
 
 # grpo_norm_kind
 NORM_LAYER, NORM_RMS = 0, 1
 
 
-def _on(*ts):
-    """The tensors' one GPU made current, and its current stream: (context, stream)."""
+def _on(*ts, strided=()):
+    """The tensors' one GPU made current, and its current stream: (context, stream).
+    All of them are contiguous, except those of `strided`."""
     _dev(*ts)
+    for t in strided:
+        if not t.is_cuda:
+            raise ValueError("all tensors must be on the GPU")
+    ts += strided
     dev = ts[0].device
     for t in ts:
         if t.device != dev:
@@ -228,3 +233,48 @@ def grpo_adamw(plan: AdamWPlan, step, lr=1e-6, betas=(0.9, 0.999), eps: float = 
                                               stream))
     # autograd has to see that the parameters changed
     torch.autograd.graph.increment_version(plan.versioned)
+
+
+# ---------------------------------------------------------------- sampling
+def grpo_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None,
+                workspace=None):
+    """(token, lp): one token (int32 [B]) for each row of logits [B, V] (float32 or
+    bfloat16; rows may lie any distance apart), from u [B] float32 in [0, 1), and its
+    log-probability (float32 [B]) under softmax(logits / temperature) of the whole row.
+    temperature, top_k, top_p and min_p are numbers, or tensors [B] with one for each row
+    (float32; int32 for top_k).  0 is off for each (temperature 0 means 1), and so is
+    top_p 1; top_k 1 takes the largest logit.  out: (token, lp) to write into.  See
+    grpo_sample in include/grpo.h for the order of the filters and rows without a
+    distribution."""
+    B, V = _matrix(logits, "logits")
+    dt = _dt(logits)
+    if V > 1 and logits.stride(1) != 1 or B > 1 and logits.stride(0) < V:
+        raise ValueError("the logits of a row must be adjacent and rows must not overlap")
+    stride = max(V, logits.stride(0))
+    _arg(u, "u", dtype=torch.float32, numel=B)
+    opts, rows = SampleOpts(), []
+    for name, x, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                           ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if isinstance(x, torch.Tensor):
+            rows.append(_arg(x, name, dtype=dtype, numel=B))
+            setattr(opts, name + "_rows", x.data_ptr())
+        else:
+            setattr(opts, name, x)
+    token, lp = (None, None) if out is None else out
+    dev = logits.device
+    token = torch.empty(B, dtype=torch.int32, device=dev) if token is None else \
+        _arg(token, "token", dtype=torch.int32, numel=B)
+    lp = torch.empty(B, dtype=torch.float32, device=dev) if lp is None else \
+        _arg(lp, "lp", dtype=torch.float32, numel=B)
+    need = int(lib().grpo_sample_workspace_bytes(B, V))
+    if need == 0:
+        _check("grpo_sample_workspace_bytes", -3)
+    if workspace is not None:
+        rows.append(_workspace(need, dev, workspace))
+    ctx, stream = _on(u, token, lp, *rows, strided=(logits,))
+    with ctx:
+        ws = _workspace(need, dev, workspace)
+        _check("grpo_sample", lib().grpo_sample(
+            _ptr(logits), dt, B, V, stride, _ptr(u), ctypes.byref(opts), _ptr(token), _ptr(lp),
+            _ptr(ws), ws.numel(), stream))
+    return token, lp

@@ -14,7 +14,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgrpo.so")
-SOURCES = ["kernels.hip", "grpo_api.hip", "timing.hip", "norm.hip", "adamw.hip"]
+SOURCES = ["kernels.hip", "grpo_api.hip", "timing.hip", "norm.hip", "adamw.hip",
+           "sample.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

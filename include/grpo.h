@@ -422,6 +422,48 @@ int grpo_moment_values(const void* codes, const float* scales, int64_t n, int sq
                        void* stream);
 
 /*
+ * One token for each row of logits [B, V] (GRPO_F32 or GRPO_BF16; row b starts at
+ * logits + b * row_stride elements, row_stride >= V), from u [B] float32, one
+ * uniform number in [0, 1) per row (a value outside counts as the nearest
+ * bound).  The rollout's last step: token [B] int32 becomes y, lp [B] float32
+ * the behaviour policy's log-probability.
+ *   z = x / temperature, e = exp(z - max z); the tokens in the order (x down,
+ *   index up).  top_k keeps the first top_k; top_p, of those, the ones whose
+ *   mass before them is below top_p times the mass of those; min_p, of those,
+ *   the ones with e >= min_p.
+ *   token: the lowest index whose running kept mass, in index order, exceeds u
+ *   times the kept mass.
+ *   lp: z[token] - log sum exp z over the whole row, filters or not: what
+ *   grpo_loss_fwd_ex gives as lp for that token and temperature.
+ * Zeros in opts (or opts = NULL) are "off": temperature 1, no filter; top_k >= V
+ * and top_p = 1 are off too, and top_k = 1 takes the largest logit.  The scalars
+ * hold for all rows; a non-NULL ..._rows device array [B] gives each row its own
+ * instead (there, values out of range are off for the filters; min_p above 1
+ * counts as 1).
+ * -inf logits are tokens that cannot be drawn.  A row with a NaN or +inf, with
+ * nothing above -inf, or with a device-side temperature that is negative or
+ * not finite has token -1 and lp NaN.
+ * Whatever decides a token is computed in 64 bits.  V and B at most 2^20.
+ * workspace: grpo_sample_workspace_bytes(B, V), 256-byte aligned.
+ */
+typedef struct grpo_sample_opts {
+  double temperature;
+  double top_p;
+  double min_p;
+  int32_t top_k;
+  int32_t reserved; /* not read */
+  const float* temperature_rows;
+  const float* top_p_rows;
+  const float* min_p_rows;
+  const int32_t* top_k_rows;
+} grpo_sample_opts;
+
+size_t grpo_sample_workspace_bytes(int64_t B, int64_t V);
+int grpo_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                const float* u, const grpo_sample_opts* opts, int32_t* token, float* lp,
+                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Diagnostic: C[M, N] (float32, row-major, written) = A[M, K] . B[N, K]^T,
  * through the same MFMA tile main loop the loss kernels use (A, B dtype
  * elements, both rows contiguous along K).  K times the element size must be

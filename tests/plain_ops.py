@@ -54,3 +54,30 @@ def adamw(w, g, m, v, step, lr, betas, eps, wd, scale=1.0):
     v = betas[1] * v + (1 - betas[1]) * g * g
     mh, vh = m / (1 - betas[0] ** step), v / (1 - betas[1] ** step)
     return w - lr * wd * w - lr * mh / (vh.sqrt() + eps), m, v
+
+
+def sample(x, u, T=1.0, k=0, p=1.0, min_p=0.0):
+    """(token, lp) of one row of logits; (-1, nan) where nothing can be drawn."""
+    x = x.double()
+    T = 1.0 if T == 0 else T
+    if x.isnan().any() or (x == float("inf")).any() or x.max() == float("-inf") or not 0 < T < float("inf"):
+        return -1, float("nan")
+    z = x / T
+    e = (z - z.max()).exp()
+    order = sorted(range(x.numel()), key=lambda i: (-x[i].item(), i)) if x.numel() < 300 else \
+        x.sort(descending=True, stable=True).indices.tolist()
+    if 0 < k < len(order):
+        order = order[:k]
+    if 0 < p < 1:
+        w = e[order]
+        up = w.cumsum(0)
+        before = torch.cat([torch.zeros(1, dtype=torch.float64), up[:-1]])
+        order = [i for i, keep in zip(order, (before < p * up[-1]).tolist()) if keep]
+    keep = torch.zeros_like(e)
+    keep[order] = 1
+    if min_p > 0:
+        keep *= e >= min(min_p, 1.0)
+    run = (e * keep).cumsum(0)
+    hit = (run > min(max(u, 0.0), 1.0) * run[-1]).nonzero()
+    token = hit[0].item() if len(hit) else (e * keep).nonzero()[-1].item()
+    return token, (z[token] - z.max() - e.sum().log()).item()
