@@ -8,8 +8,20 @@
 //
 // A token is right or wrong, so what decides it is computed in 64 bits: a float32 sum over
 // 150 000 tokens would move its borders past u in about one row of a hundred.  Where sums meet
-// in any order (histograms), weights are whole multiples of 2^-42, whose sums over up to 2^20
-// tokens are exact in 64 bits: no result depends on an order.
+// in any order (histograms, lists), weights are whole multiples of 2^-42, whose sums over up to
+// 2^20 tokens are exact in 64 bits: no result depends on an order.
+//
+// Rows by what their filters need, each with the fewest passes over the logits:
+//   PLAIN    no filter: one pass for maxima and sums, then one segment of 2048 tokens.
+//   LIST     top-k up to 2048 (or any filter on a row of at most 4096): the first pass keeps
+//            the maximum of every 32 tokens; at least k of these are at or above the k-th
+//            largest of them, so every kept token is, and only groups whose maximum is get
+//            read again.  The candidates are sorted in LDS, where top-p and min-p are a cut.
+//   MIN_P    the same with the bound max + T log min_p.
+//   NUCLEUS  top-p alone: a histogram of the mass over 4096 bins of x finds the bin that the
+//            cut falls into; one more pass sums what lies above and lists that bin's tokens.
+//   GENERAL  everything else (larger k, lists that overflow as on rows of equal logits): the
+//            cut digit by digit, one pass over the row for each of its 5 digits.
 #include <math.h>
 
 #include <algorithm>
@@ -21,33 +33,48 @@
 namespace grpo {
 namespace {
 
-constexpr int kSeg = 512;                  // tokens per segment: 8 a lane of one wave
+constexpr int kSeg = 2048;                 // tokens per segment: one wave, 32 a lane
 constexpr int64_t kMaxVocab = 1 << 20;     // 2^20 weights of at most 2^42
 constexpr int kMaxSegs = (int)(kMaxVocab / kSeg);
-constexpr int kBins = 2048;
+constexpr int kBins = 2048;                // of one digit, and of the groups' maxima
+constexpr int kNucleusBins = 4096;
+constexpr int kList = 4096;                // candidates that are sorted in LDS
+constexpr int kListK = 2048;               // largest top-k that goes by the groups' maxima
 
 struct SampleArgs {
   const void* logits;
   const float* u;
   int64_t stride;
-  int V, segs;
+  int V, segs, splits;
   double T, p, min_p;
   int k;
   const float* T_rows;
   const int32_t* k_rows;
   const float* p_rows;
   const float* min_p_rows;
-  float* seg_max;      // [B, segs]
-  double* seg_sum;     // [B, segs], relative to the segment's own maximum
+  float* seg_max;      // [B, segs]; NaN where the segment holds a NaN or +inf
+  float* seg_min;      // [B, segs], of what is above -inf
+  double* seg_sum;     // [B, segs], relative to the segment's own maximum (not for NUCLEUS)
+  float* grp_max;      // [B, segs, 64]: a lane's 32 tokens (LIST and MIN_P)
+  // NUCLEUS
+  uint64_t* hist;      // [B, splits, kNucleusBins]
+  double* z_part;      // [B, splits]
+  uint64_t* above;     // [B]: mass above the cut's bin
+  uint64_t* whole;     // [B]: mass of the row
+  uint64_t* seg_kept;  // [B, segs]: mass above the cut's bin, by segment
+  int* listed;         // [B]: tokens in the cut's bin
+  uint64_t* list;      // [B, kList]: their places
   int32_t* token;
   float* lp;
 };
+
+enum RowClass { PLAIN, LIST, MIN_P, NUCLEUS, GENERAL };
 
 // The parameters of one row, where 0 (or anything out of range in a device array) is off.
 struct RowParams {
   double T, inv_T, p, min_p;
   int k;
-  bool filtered;
+  RowClass cls;
 };
 __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row) {
   RowParams r;
@@ -61,8 +88,33 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row
   r.min_p = a.min_p_rows != nullptr ? (double)a.min_p_rows[row] : a.min_p;
   if (!(r.min_p > 0.0)) r.min_p = 0.0;
   if (r.min_p > 1.0) r.min_p = 1.0;
-  r.filtered = r.k != 0 || r.p != 0.0 || r.min_p != 0.0;
+  if (r.k == 0 && r.p == 0.0 && r.min_p == 0.0) r.cls = PLAIN;
+  else if (a.V <= kList || (r.k != 0 && r.k <= kListK)) r.cls = LIST;
+  else if (r.k != 0) r.cls = GENERAL;
+  else r.cls = r.p != 0.0 ? NUCLEUS : MIN_P;
   return r;
+}
+
+// exp(t) for t <= 0, 0 below -700: t = n ln 2 + r with |r| <= ln 2 / 2, and the Taylor series
+// of exp(r) to the twelfth power (remainder below 2e-16).  19 instructions.
+__device__ __forceinline__ double exp_down(double t) {
+  const double n = rint(t * 1.4426950408889634);
+  double r = fma(n, -0x1.62e42fefa39efp-1, t);
+  r = fma(n, -0x1.abc9e3b39803fp-56, r);
+  double q = 1.0 / 479001600.0;
+  q = fma(q, r, 1.0 / 39916800.0);
+  q = fma(q, r, 1.0 / 3628800.0);
+  q = fma(q, r, 1.0 / 362880.0);
+  q = fma(q, r, 1.0 / 40320.0);
+  q = fma(q, r, 1.0 / 5040.0);
+  q = fma(q, r, 1.0 / 720.0);
+  q = fma(q, r, 1.0 / 120.0);
+  q = fma(q, r, 1.0 / 24.0);
+  q = fma(q, r, 1.0 / 6.0);
+  q = fma(q, r, 0.5);
+  q = fma(q, r, 1.0);
+  q = fma(q, r, 1.0);
+  return t < -700.0 ? 0.0 : ldexp(q, (int)fmax(n, -1100.0));
 }
 
 // 8 consecutive logits from token c on; those at V and behind it read as -inf.  Minus zero
@@ -92,6 +144,7 @@ __device__ __forceinline__ float wave_top(float v) {
   for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
   return v;
 }
+__device__ __forceinline__ float wave_low(float v) { return -wave_top(-v); }
 // Sums of the lanes below this one, and (total) of all.
 template <typename V> __device__ __forceinline__ V wave_before(V v, V& total) {
   const int lane = threadIdx.x & 63;
@@ -106,33 +159,43 @@ template <typename V> __device__ __forceinline__ V wave_before(V v, V& total) {
 }
 
 // ---------------------------------------------------------------- maxima and sums
-// One wave per segment of one row.  A NaN or +inf makes the segment's maximum NaN.
+// One wave per segment of one row.
 template <typename T>
 __global__ void __launch_bounds__(256) k_sample_mass(SampleArgs a, int64_t waves) {
   const int lane = threadIdx.x & 63;
   for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); w < waves; w += (int64_t)gridDim.x * 4) {
     const int64_t row = w / a.segs;
     const int seg = (int)(w - row * a.segs);
-    float x[8];
-    load8((const T*)a.logits + row * a.stride, seg * kSeg + lane * 8, a.V, x);
-    float m = x[0];
+    const RowParams r = row_params(a, row);
+    float x[4][8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      load8((const T*)a.logits + row * a.stride, seg * kSeg + q * 512 + lane * 8, a.V, x[q]);
+    float m = x[0][0], low = __builtin_huge_valf();
     bool bad = false;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m = fmaxf(m, x[j]);
-      bad |= !(x[j] < __builtin_huge_valf());
-    }
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m = fmaxf(m, x[q][j]);
+        if (x[q][j] > -__builtin_huge_valf()) low = fminf(low, x[q][j]);
+        bad |= !(x[q][j] < __builtin_huge_valf());
+      }
+    if (r.cls == LIST || r.cls == MIN_P) a.grp_max[w * 64 + lane] = m;
     m = wave_top(m);
     bad = __any(bad);
     double s = 0.0;
-    if (!bad && m > -__builtin_huge_valf()) {
-      const double inv_T = row_params(a, row).inv_T;
+    if (r.cls == NUCLEUS) low = wave_low(low);
+    else if (!bad && m > -__builtin_huge_valf()) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += exp(((double)x[j] - (double)m) * inv_T);
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += exp_down(((double)x[q][j] - (double)m) * r.inv_T);
+      s = wave_total(s);
     }
-    s = wave_total(s);
     if (lane == 0) {
       a.seg_max[w] = bad ? __builtin_nanf("") : m;
+      a.seg_min[w] = low;
       a.seg_sum[w] = s;
     }
   }
@@ -152,11 +215,33 @@ __device__ __forceinline__ uint64_t units(double e) {
   return (uint64_t)(__double_as_longlong(e + 1024.0) & ((1ll << 52) - 1));
 }
 
+__device__ __forceinline__ float value_at(uint64_t place) {
+  const uint32_t key = (uint32_t)(place >> 20);
+  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
+}
+__device__ __forceinline__ int index_at(uint64_t place) {
+  return (int)(kMaxVocab - 1) - (int)(place & (kMaxVocab - 1));
+}
+
 struct RowState {
   float max;
   RowParams r;
   __device__ __forceinline__ double weight(float x) const {
-    return exp(((double)x - (double)max) * r.inv_T);
+    return exp_down(((double)x - (double)max) * r.inv_T);
+  }
+};
+
+// Bins of x from the maximum down, in float32: rounding keeps the order, so the bins are in the
+// order of x.  -inf and what lies below the last bin's lower end are in the last bin.
+struct Binning {
+  float max, scale;
+  int last;
+  __device__ __forceinline__ Binning(float top, float range, int bins) : max(top), last(bins - 1) {
+    scale = (float)last / range;
+    if (!(scale < __builtin_huge_valf())) scale = 0.f;
+  }
+  __device__ __forceinline__ int operator()(float x) const {
+    return (int)fminf((max - x) * scale, (float)last);   // fminf drops the NaN of inf * 0
   }
 };
 
@@ -178,13 +263,176 @@ __device__ __forceinline__ V block_before(V v, V* lds, V& total) {
   return off + before;
 }
 
+// A row's maximum over its segments, whether it holds a NaN or +inf, and its minimum above
+// -inf, for a block of 1024 threads (lds: 16 of each).
+struct RowRange {
+  float top, low;
+  bool bad;
+};
+__device__ __forceinline__ RowRange row_range(const SampleArgs& a, int64_t row, float (*lds)[16]) {
+  const int i = threadIdx.x;
+  RowRange r;
+  r.top = i < a.segs ? a.seg_max[row * a.segs + i] : -__builtin_huge_valf();
+  r.low = i < a.segs ? a.seg_min[row * a.segs + i] : __builtin_huge_valf();
+  r.bad = __any(r.top != r.top);
+  r.top = wave_top(r.top);
+  r.low = wave_low(r.low);
+  if ((threadIdx.x & 63) == 0) {
+    lds[0][i >> 6] = r.top;
+    lds[1][i >> 6] = r.low;
+    lds[2][i >> 6] = r.bad ? 1.f : 0.f;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 16; ++w) {
+    r.top = fmaxf(r.top, lds[0][w]);
+    r.low = fminf(r.low, lds[1][w]);
+    r.bad |= lds[2][w] != 0.f;
+  }
+  return r;
+}
+// Whether there is anything to draw from.
+__device__ __forceinline__ bool drawable(const RowRange& g, const RowParams& r) {
+  return !g.bad && g.top > -__builtin_huge_valf() && r.T > 0.0 && r.T < __builtin_huge_val();
+}
+// Over 30 T below the maximum, 2^20 tokens weigh less than 10^-6 of it.
+__device__ __forceinline__ Binning nucleus_bins(const RowRange& g, const RowParams& r) {
+  return Binning(g.top, fminf(g.top - g.low, (float)(30.0 * r.T)), kNucleusBins);
+}
+
+// ---------------------------------------------------------------- NUCLEUS
+// Block (split, row): the mass of the split's tokens by bin.
+template <typename T>
+__global__ void __launch_bounds__(1024) k_sample_hist(SampleArgs a) {
+  const int64_t row = blockIdx.y;
+  RowState st;
+  st.r = row_params(a, row);
+  if (st.r.cls != NUCLEUS) return;
+  __shared__ uint64_t bins[kNucleusBins];
+  __shared__ float range[3][16];
+  __shared__ double zs[16];
+  for (int i = threadIdx.x; i < kNucleusBins; i += 1024) bins[i] = 0;
+  const RowRange g = row_range(a, row, range);      // its barrier is also the bins'
+  if (!drawable(g, st.r)) return;
+  st.max = g.top;
+  const Binning bin = nucleus_bins(g, st.r);
+  const int per = (a.segs + a.splits - 1) / a.splits * kSeg;
+  const int from = blockIdx.x * per, to = min(a.V, from + per);
+  const T* x = (const T*)a.logits + row * a.stride;
+  double z = 0.0;
+  for (int c = from + threadIdx.x * 8; c < to; c += 1024 * 8) {
+    float v[8];
+    load8(x, c, a.V, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const double e = st.weight(v[j]);
+      z += e;
+      const uint64_t n = units(e);
+      if (n) atomicAdd((unsigned long long*)&bins[bin(v[j])], (unsigned long long)n);
+    }
+  }
+  double total;
+  block_before<double>(z, zs, total);
+  uint64_t* out = a.hist + (row * a.splits + blockIdx.x) * kNucleusBins;
+  for (int i = threadIdx.x; i < kNucleusBins; i += 1024) out[i] = bins[i];
+  if (threadIdx.x == 0) {
+    a.z_part[row * a.splits + blockIdx.x] = total;
+    if (blockIdx.x == 0) a.listed[row] = 0;
+  }
+}
+
+// Block (split, row): the bin that the cut falls into, the mass above it by segment and the
+// places of its tokens.
+template <typename T>
+__global__ void __launch_bounds__(1024) k_sample_gather(SampleArgs a) {
+  const int64_t row = blockIdx.y;
+  RowState st;
+  st.r = row_params(a, row);
+  if (st.r.cls != NUCLEUS) return;
+  __shared__ float range[3][16];
+  __shared__ uint64_t sums[16];
+  __shared__ uint64_t mine[kList];
+  __shared__ int found, count, at;
+  const RowRange g = row_range(a, row, range);
+  if (!drawable(g, st.r)) return;
+  st.max = g.top;
+  const Binning bin = nucleus_bins(g, st.r);
+  // thread t holds bins 4t .. 4t + 3
+  uint64_t h[4] = {0, 0, 0, 0}, total;
+  for (int s = 0; s < a.splits; ++s) {
+    const uint64_t* in = a.hist + (row * a.splits + s) * kNucleusBins + 4 * threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h[j] += in[j];
+  }
+  if (threadIdx.x == 0) {
+    found = kNucleusBins - 1;
+    count = 0;
+  }
+  uint64_t run = block_before<uint64_t>(h[0] + h[1] + h[2] + h[3], sums, total);
+  const double mass = st.r.p * (double)total;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (h[j] && (double)run < mass && (double)(run + h[j]) >= mass) {
+      found = 4 * threadIdx.x + j;       // one thread's: the sums ascend
+      if (blockIdx.x == 0) {
+        a.above[row] = run;
+        a.whole[row] = total;
+      }
+    }
+    run += h[j];
+  }
+  __syncthreads();
+  const int cut_bin = found, lane = threadIdx.x & 63;
+  const int per = (a.segs + a.splits - 1) / a.splits;
+  const T* x = (const T*)a.logits + row * a.stride;
+  const int end = min(a.segs, (int)(blockIdx.x + 1) * per);
+  for (int seg = blockIdx.x * per + (threadIdx.x >> 6); seg < end; seg += 16) {
+    uint64_t part = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = seg * kSeg + q * 512 + lane * 8;
+      float v[8];
+      load8(x, c, a.V, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int b = bin(v[j]);
+        if (b < cut_bin) {
+          const double e = st.weight(v[j]);
+          if (e >= st.r.min_p) part += units(e);
+        } else if (b == cut_bin && c + j < a.V) {
+          const int slot = atomicAdd(&count, 1);
+          if (slot < kList) mine[slot] = place(v[j], c + j);
+        }
+      }
+    }
+    part = wave_total(part);
+    if (lane == 0) a.seg_kept[row * a.segs + seg] = part;
+  }
+  __syncthreads();
+  const int n = count;
+  if (threadIdx.x == 0) at = n ? atomicAdd(&a.listed[row], n) : 0;
+  __syncthreads();
+  // more than kList in all, or in this block: the pick sees the count and goes by digits
+  for (int i = threadIdx.x; i < min(n, kList); i += 1024)
+    if (at + i < kList) a.list[row * kList + at + i] = mine[i];
+}
+
+// ---------------------------------------------------------------- the pick
 struct Lds {
-  uint64_t bins[kBins];
-  double segs[kMaxSegs];
+  union {
+    uint64_t bins[kBins];
+    uint64_t list[kList];
+    unsigned counts[kBins];
+  };
+  union {
+    uint64_t segs_u[kMaxSegs];
+    double segs[kMaxSegs];
+  };
   uint64_t wave_u[16];
   double wave_d[16];
-  uint64_t found_place, found_sum;
-  int found;
+  float range[3][16];
+  uint64_t found_sum;
+  int found, count;
 };
 
 // The place of the last kept token when tokens are kept in order while fewer than k were
@@ -240,179 +488,300 @@ __device__ uint64_t find_cut(const T* x, int V, const RowState& st, uint64_t flo
   return prefix;
 }
 
+// Sorts list[0, n) downwards (bitonic; the rest up to a power of two is filled with 0).
+__device__ void sort_list(uint64_t* list, int n) {
+  int size = 2;
+  while (size < n) size <<= 1;
+  for (int i = n + threadIdx.x; i < size; i += 1024) list[i] = 0;
+  for (int k = 2; k <= size; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      __syncthreads();
+      for (int t = threadIdx.x; t < size / 2; t += 1024) {
+        const int lo = ((t & ~(j - 1)) << 1) | (t & (j - 1)), hi = lo | j;
+        const uint64_t p = list[lo], q = list[hi];
+        if ((p < q) == ((lo & k) == 0)) {
+          list[lo] = q;
+          list[hi] = p;
+        }
+      }
+    }
+  __syncthreads();
+}
+
+// The tokens that may be kept, into l.list; their number (over kList: too many).  A group is
+// 32 tokens that one lane of k_sample_mass read; only groups whose maximum may be kept are read.
+template <typename T>
+__device__ int candidates(const SampleArgs& a, int64_t row, const T* x, const RowState& st, Lds& l) {
+  const int groups = a.segs * 64, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const float* gm = a.grp_max + row * groups;
+  const float none = -__builtin_huge_valf();
+  Binning bin(st.max, 0.f, kBins);
+  int last = kBins - 1;
+  if (st.r.cls == LIST && a.V > kList) {
+    // bins over the range of the groups' maxima; the last bin that the k largest reach into
+    float low = __builtin_huge_valf();
+    for (int i = threadIdx.x; i < kBins; i += 1024) l.counts[i] = 0;
+    for (int i = threadIdx.x; i < groups; i += 1024)
+      if (gm[i] > none) low = fminf(low, gm[i]);
+    low = wave_low(low);
+    if (lane == 0) l.range[0][wave] = low;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) low = fminf(low, l.range[0][i]);
+    bin = Binning(st.max, st.max - low, kBins);
+    for (int i = threadIdx.x; i < groups; i += 1024)
+      if (gm[i] > none) atomicAdd(&l.counts[bin(gm[i])], 1u);
+    __syncthreads();
+    const int b = 2 * threadIdx.x;
+    const uint64_t c0 = l.counts[b], c1 = l.counts[b + 1], k = (uint64_t)st.r.k;
+    uint64_t total;
+    if (threadIdx.x == 0) l.found = kBins - 1;     // fewer groups than k: all of them
+    const uint64_t before = block_before<uint64_t>(c0 + c1, l.wave_u, total);
+    if (before < k && before + c0 >= k) l.found = b;
+    else if (before + c0 < k && before + c0 + c1 >= k) l.found = b + 1;
+    __syncthreads();
+    last = l.found;
+    if (total < k) bin = Binning(st.max, 0.f, kBins);
+  }
+  // by bins (a scale of 0 puts all that is above -inf into bin 0), or by min_p
+  auto wanted = [&](float v) {
+    if (!(v > none)) return false;
+    return st.r.cls == MIN_P ? st.weight(v) >= st.r.min_p : bin(v) <= last;
+  };
+  if (threadIdx.x == 0) l.count = 0;
+  __syncthreads();
+  // one wave takes 64 groups, and of those the wanted ones two at a time, 32 lanes each
+  for (int g0 = wave * 64; g0 < groups; g0 += 16 * 64) {
+    uint64_t todo = __ballot(wanted(gm[g0 + lane]));
+    while (todo) {
+      const int one = __ffsll((unsigned long long)todo) - 1;
+      todo &= todo - 1;
+      const int two = todo ? __ffsll((unsigned long long)todo) - 1 : -1;
+      todo &= todo - 1;
+      const int gl = lane < 32 ? one : two;
+      // token q * 512 + lane * 8 + j of the segment, for q < 4 and j < 8
+      const int i = lane & 31, c = g0 / 64 * kSeg + (i >> 3) * 512 + gl * 8 + (i & 7);
+      const bool in = gl >= 0 && c < a.V;
+      const float v = in ? (float)x[c] + 0.f : none;
+      const bool take = in && wanted(v);
+      const uint64_t who = __ballot(take);
+      int base = 0;
+      if (lane == 0) base = atomicAdd(&l.count, __popcll(who));
+      base = __builtin_amdgcn_readfirstlane(base);
+      const int slot = base + __popcll(who & ((1ull << lane) - 1));
+      if (take && slot < kList) l.list[slot] = place(v, c);
+    }
+  }
+  __syncthreads();
+  return l.count;
+}
+
+// The place of the last kept token (0: all), from a row's sorted list of n places that follow
+// on `above` units of mass; `whole` the mass that top-p is a share of (0: that of the list's
+// first k).  Adds the kept tokens' masses to l.segs_u.
+__device__ uint64_t cut_list(const RowState& st, int n, uint64_t above, uint64_t whole, Lds& l) {
+  sort_list(l.list, n);
+  uint64_t m[4], sum = 0, total;
+  double e[4];
+  const int first = 4 * threadIdx.x, k = st.r.k != 0 ? min(n, st.r.k) : n;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    e[j] = first + j < k ? st.weight(value_at(l.list[first + j])) : 0.0;
+    m[j] = first + j < k ? units(e[j]) : 0;
+    sum += m[j];
+  }
+  if (threadIdx.x == 0) l.found = k - 1;
+  uint64_t run = above + block_before<uint64_t>(sum, l.wave_u, total);
+  if (st.r.p != 0.0) {
+    const double mass = st.r.p * (double)(whole != 0 ? whole : total);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // the token with which the mass reaches its share is the last kept one
+      if (m[j] && (double)run < mass && (double)(run + m[j]) >= mass) l.found = first + j;
+      run += m[j];
+    }
+  }
+  __syncthreads();
+  const int last = l.found;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (first + j <= last && m[j] && e[j] >= st.r.min_p)
+      atomicAdd((unsigned long long*)&l.segs_u[index_at(l.list[first + j]) / kSeg], (unsigned long long)m[j]);
+  const uint64_t cut = l.list[last];
+  __syncthreads();
+  return cut;
+}
+
 // One block of 1024 threads per row.
 template <typename T>
 __global__ void __launch_bounds__(1024) k_sample_pick(SampleArgs a) {
   __shared__ Lds l;
   const int64_t row = blockIdx.x;
-  const int V = a.V, lane = threadIdx.x & 63;
+  const int V = a.V, lane = threadIdx.x & 63, seg_of = threadIdx.x;
   const T* x = (const T*)a.logits + row * a.stride;
-  const float* sm = a.seg_max + row * a.segs;
-  const double* ss = a.seg_sum + row * a.segs;
   RowState st;
   st.r = row_params(a, row);
-
-  // the row's maximum and mass: each thread takes two neighbouring segments
-  float m[2];
-  bool bad = false;
-  float top = -__builtin_huge_valf();
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int i = 2 * threadIdx.x + j;
-    m[j] = i < a.segs ? sm[i] : -__builtin_huge_valf();
-    bad |= m[j] != m[j];
-    top = fmaxf(top, m[j]);
-  }
-  top = wave_top(top);
-  bad = __any(bad);
-  if (lane == 0) {
-    l.wave_d[threadIdx.x >> 6] = (double)top;
-    l.wave_u[threadIdx.x >> 6] = bad;
-  }
-  __syncthreads();
-  bad = false;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    top = fmaxf(top, (float)l.wave_d[i]);
-    bad |= l.wave_u[i] != 0;
-  }
-  st.max = top;
-  if (bad || !(top > -__builtin_huge_valf()) || !(st.r.T > 0.0) || !(st.r.T < __builtin_huge_val())) {
-    // nothing to draw from: a NaN or +inf, all -inf, or no temperature
+  const RowRange range = row_range(a, row, l.range);
+  st.max = range.top;
+  if (!drawable(range, st.r)) {
     if (threadIdx.x == 0) {
       a.token[row] = -1;
       a.lp[row] = __builtin_nanf("");
     }
     return;
   }
-  double s[2];
+
+  // the row's whole mass, for lp; segment i belongs to thread i
+  const bool has = seg_of < a.segs;
+  double Z, s = 0.0;
+  if (st.r.cls != NUCLEUS) {
+    const double sum = has ? a.seg_sum[row * a.segs + seg_of] : 0.0;
+    if (sum > 0.0) s = sum * st.weight(a.seg_max[row * a.segs + seg_of]);
+  } else if (seg_of < a.splits) {
+    s = a.z_part[row * a.splits + seg_of];
+  }
+  double at = block_before<double>(s, l.wave_d, Z), sum = Z;
+  uint64_t cut = 0;
+  RowClass cls = st.r.cls;
+  if (cls != PLAIN) {
+    if (seg_of < kMaxSegs) l.segs_u[seg_of] = cls == NUCLEUS && has ? a.seg_kept[row * a.segs + seg_of] : 0;
+    if (cls == NUCLEUS) {
+      const int n = a.listed[row];
+      if (n <= kList) {
+        for (int i = threadIdx.x; i < n; i += 1024) l.list[i] = a.list[row * kList + i];
+        cut = cut_list(st, n, a.above[row], a.whole[row], l);
+      } else {
+        cls = GENERAL;
+      }
+    } else if (cls == LIST || cls == MIN_P) {
+      const int n = candidates<T>(a, row, x, st, l);
+      if (n <= kList) cut = cut_list(st, n, 0, 0, l);
+      else cls = GENERAL;
+    }
+    if (cls == GENERAL) {
+      if (st.r.k != 0) cut = find_cut<T, false>(x, V, st, 0, (uint64_t)st.r.k, 0.0, l);
+      if (st.r.p != 0.0) {
+        // the mass of what top-k keeps, exactly
+        uint64_t part = 0, zk;
+        for (int c = threadIdx.x * 8; c < V; c += 1024 * 8) {
+          float v[8];
+          load8(x, c, V, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (c + j < V && place(v[j], c + j) >= cut) part += units(st.weight(v[j]));
+        }
+        block_before<uint64_t>(part, l.wave_u, zk);
+        const uint64_t c2 = find_cut<T, true>(x, V, st, cut, 0, st.r.p * (double)zk, l);
+        cut = c2 > cut ? c2 : cut;
+      }
+      // the kept mass of each segment, one wave a segment
+      for (int g = threadIdx.x >> 6; g < a.segs; g += 16) {
+        uint64_t part = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = g * kSeg + q * 512 + lane * 8;
+          float v[8];
+          load8(x, c, V, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (c + j >= V || place(v[j], c + j) < cut) continue;
+            const double e = st.weight(v[j]);
+            if (e >= st.r.min_p) part += units(e);
+          }
+        }
+        part = wave_total(part);
+        if (lane == 0) l.segs_u[g] = part;
+      }
+      __syncthreads();
+    }
+    // at most 2^11 weights of at most 2^42 units: exact as a double
+    s = has ? (double)l.segs_u[seg_of] * 0x1p-42 : 0.0;
+    at = block_before<double>(s, l.wave_d, sum);
+  }
+
+  const double target = fmin(fmax((double)a.u[row], 0.0), 1.0) * sum;
+  // the lowest segment whose running mass exceeds the target, else the last that has any
+  if (threadIdx.x == 0) {
+    l.found = kMaxSegs;
+    l.count = 0;
+  }
+  __syncthreads();
+  if (s > 0.0) {
+    if (at + s > target) atomicMin(&l.found, seg_of);
+    atomicMax(&l.count, seg_of);
+  }
+  __syncthreads();
+  const int seg = l.found < kMaxSegs ? l.found : l.count;
+  if (seg_of == seg) l.wave_d[0] = at;
+  __syncthreads();
+  const double rest = target - l.wave_d[0];
+  // its tokens, two a thread
+  const int c = seg * kSeg + 2 * (int)threadIdx.x;
+  float v[2];
+  double e[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int i = 2 * threadIdx.x + j;
-    s[j] = i < a.segs ? ss[i] * st.weight(m[j]) : 0.0;
+    v[j] = c + j < V ? (float)x[c + j] + 0.f : -__builtin_huge_valf();
+    e[j] = st.weight(v[j]);
+    if (st.r.cls != PLAIN)
+      e[j] = c + j < V && place(v[j], c + j) >= cut && e[j] >= st.r.min_p ? (double)units(e[j]) * 0x1p-42 : 0.0;
   }
-  double Z;
-  block_before<double>(s[0] + s[1], l.wave_d, Z);
-
-  const double u = fmin(fmax((double)a.u[row], 0.0), 1.0);
-  uint64_t cut = 0;
-  if (!st.r.filtered) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int i = 2 * threadIdx.x + j;
-      l.segs[i] = s[j];
-    }
-    __syncthreads();
-  } else {
-    if (st.r.k != 0) cut = find_cut<T, false>(x, V, st, 0, (uint64_t)st.r.k, 0.0, l);
-    if (st.r.p != 0.0) {
-      // the mass of what top-k keeps, exactly
-      uint64_t part = 0, zk;
-      for (int c = threadIdx.x * 8; c < V; c += 1024 * 8) {
-        float v[8];
-        load8(x, c, V, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (place(v[j], c + j) >= cut && c + j < V) part += units(st.weight(v[j]));
-      }
-      block_before<uint64_t>(part, l.wave_u, zk);
-      const uint64_t c2 = find_cut<T, true>(x, V, st, cut, 0, st.r.p * (double)zk, l);
-      cut = c2 > cut ? c2 : cut;
-    }
-    // the kept mass of each segment, one wave a segment (whole multiples of 2^-42 below 2^62
-    // of them in all: the doubles of a segment's at most 2^9 + 42 bits are exact)
-    __syncthreads();
-    for (int g = threadIdx.x >> 6; g < kMaxSegs; g += 16) {
-      uint64_t part = 0;
-      if (g < a.segs) {
-        float v[8];
-        const int c = g * kSeg + lane * 8;
-        load8(x, c, V, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (c + j >= V || place(v[j], c + j) < cut) continue;
-          const double e = st.weight(v[j]);
-          if (e >= st.r.min_p) part += units(e);
-        }
-      }
-      part = wave_total(part);
-      if (lane == 0) l.segs[g] = (double)part * 0x1p-42;
-    }
-    __syncthreads();
+  if (threadIdx.x == 0) {
+    l.found = kSeg;
+    l.count = -1;
   }
-  const double s0 = l.segs[2 * threadIdx.x], s1 = l.segs[2 * threadIdx.x + 1];
-  double sum;
-  const double at = block_before<double>(s0 + s1, l.wave_d, sum);
-  const double target = u * sum;
-  // the lowest segment whose running mass exceeds the target, else the last that has any
-  if (threadIdx.x == 0) l.found = kMaxSegs;
-  __syncthreads();
-  if (s0 > 0.0 && at + s0 > target) atomicMin(&l.found, 2 * (int)threadIdx.x);
-  else if (s1 > 0.0 && at + s0 + s1 > target) atomicMin(&l.found, 2 * (int)threadIdx.x + 1);
-  __syncthreads();
-  int seg = l.found;
-  if (seg == kMaxSegs) {
-    __syncthreads();
-    if (threadIdx.x == 0) l.found = 0;
-    __syncthreads();
-    if (s1 > 0.0) atomicMax(&l.found, 2 * (int)threadIdx.x + 1);
-    else if (s0 > 0.0) atomicMax(&l.found, 2 * (int)threadIdx.x);
-    __syncthreads();
-    seg = l.found;
-  }
-  if ((int)threadIdx.x == seg / 2) l.wave_d[0] = seg & 1 ? at + s0 : at;
-  __syncthreads();
-  if (threadIdx.x >= 64) return;
-  // its tokens, 8 a lane
-  double rest = target - l.wave_d[0];
-  float v[8];
-  double e[8], mine = 0.0;
-  const int c = seg * kSeg + lane * 8;
-  load8(x, c, V, v);
-  int last = -1;
+  double run = block_before<double>(e[0] + e[1], l.wave_d, sum);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    e[j] = 0.0;
-    if (c + j < V && place(v[j], c + j) >= cut) e[j] = st.weight(v[j]);
-    if (st.r.filtered) e[j] = e[j] >= st.r.min_p ? (double)units(e[j]) * 0x1p-42 : 0.0;
-    mine += e[j];
-    if (e[j] > 0.0) last = j;
-  }
-  double wt;
-  double run = wave_before(mine, wt);
-  int hit = -1;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 2; ++j) {
     run += e[j];
-    if (hit < 0 && e[j] > 0.0 && run > rest) hit = j;
+    if (e[j] > 0.0) {
+      if (run > rest) atomicMin(&l.found, c + j - seg * kSeg);
+      atomicMax(&l.count, c + j - seg * kSeg);
+    }
   }
-  uint64_t who = __ballot(hit >= 0);
-  if (who == 0) {                       // the target is the mass itself (u = 1, a rounding)
-    hit = last;
-    who = __ballot(hit >= 0);
-    who = who ? 1ull << (63 - __clzll(who)) : 1;
-  }
-  if (lane == __ffsll((unsigned long long)who) - 1) {
-    const int j = hit < 0 ? 0 : hit;
-    float z = v[0];
+  __syncthreads();
+  // (the target is the mass itself if u = 1 or by a rounding: the last token that has any)
+  const int hit = (l.found < kSeg ? l.found : l.count) + seg * kSeg;
 #pragma unroll
-    for (int q = 1; q < 8; ++q)
-      if (q == j) z = v[q];
-    a.token[row] = c + j;
-    a.lp[row] = (float)(((double)z - (double)st.max) * st.r.inv_T - log(Z));
-  }
+  for (int j = 0; j < 2; ++j)
+    if (c + j == hit) {
+      a.token[row] = hit;
+      a.lp[row] = (float)(((double)v[j] - (double)st.max) * st.r.inv_T - log(Z));
+    }
 }
 
 struct SamplePlan {
-  int segs;
-  size_t o_max, o_sum, total;
+  int64_t rows;          // per launch
+  int segs, splits;
+  size_t o_max, o_min, o_sum, o_grp, o_hist, o_z, o_above, o_whole, o_kept, o_listed, o_list, total;
 };
+// Rows go in batches, so that the workspace stays bounded; a row of at most kList tokens needs
+// no histogram.  Splits: about two blocks of 1024 threads per CU, each with at least 4 segments.
 SamplePlan plan_sample(int64_t B, int64_t V) {
   SamplePlan p{};
+  const bool nucleus = V > kList;
+  p.rows = std::min<int64_t>(B, nucleus ? 1024 : 65536);
   p.segs = (int)((V + kSeg - 1) / kSeg);
-  p.o_max = 0;
-  p.o_sum = align_up((size_t)(B * p.segs) * 4);
-  p.total = p.o_sum + align_up((size_t)(B * p.segs) * 8);
+  p.splits = nucleus ? (int)std::max<int64_t>(1, std::min<int64_t>((p.segs + 3) / 4, 512 / p.rows)) : 0;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align_up(off + bytes);
+    return o;
+  };
+  const size_t n = (size_t)(p.rows * p.segs), h = (size_t)(p.rows * p.splits);
+  p.o_max = take(n * 4);
+  p.o_min = take(n * 4);
+  p.o_sum = take(n * 8);
+  p.o_grp = take(n * 256);
+  p.o_hist = take(h * kNucleusBins * 8);
+  p.o_z = take(h * 8);
+  p.o_above = take((size_t)p.rows * 8);
+  p.o_whole = take((size_t)p.rows * 8);
+  p.o_kept = take(nucleus ? n * 8 : 0);
+  p.o_listed = take((size_t)p.rows * 4);
+  p.o_list = take(nucleus ? (size_t)p.rows * kList * 8 : 0);
+  p.total = off;
   return p;
 }
 
@@ -429,17 +798,27 @@ int check_sample(int64_t B, int64_t V, int64_t stride) {
 }
 
 template <typename T>
-hipError_t launch_sample(const SampleArgs& a, int64_t B, hipStream_t s) {
-  const int64_t waves = B * a.segs;
+hipError_t launch_sample(const SampleArgs& a, int64_t rows, hipStream_t s) {
+  hipError_t e;
   {
     ScopedKernelTimer t(KK_SAMPLE_MASS, s);
+    const int64_t waves = rows * a.segs;
     const int64_t blocks = std::min<int64_t>((waves + 3) / 4, 1 << 20);
     k_sample_mass<T><<<(unsigned)blocks, 256, 0, s>>>(a, waves);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  // the two passes of NUCLEUS, where a row may be of that class
+  if (a.V > kList && (a.p_rows != nullptr || (a.p > 0.0 && a.p < 1.0)) &&
+      (a.k_rows != nullptr || a.k == 0 || a.k >= a.V)) {
+    ScopedKernelTimer t(KK_SAMPLE_CUT, s);
+    const dim3 grid((unsigned)a.splits, (unsigned)rows);
+    k_sample_hist<T><<<grid, 1024, 0, s>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    k_sample_gather<T><<<grid, 1024, 0, s>>>(a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   ScopedKernelTimer t(KK_SAMPLE_PICK, s);
-  k_sample_pick<T><<<(unsigned)B, 1024, 0, s>>>(a);
+  k_sample_pick<T><<<(unsigned)rows, 1024, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -479,27 +858,42 @@ int grpo_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row
   if (workspace == nullptr || workspace_bytes < p.total)
     return fail(GRPO_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", p.total,
                 workspace == nullptr ? (size_t)0 : workspace_bytes);
-  grpo::SampleArgs a{};
-  a.logits = logits;
-  a.u = u;
-  a.stride = row_stride;
-  a.V = (int)V;
-  a.segs = p.segs;
-  a.T = o.temperature;
-  a.k = o.top_k;
-  a.p = o.top_p;
-  a.min_p = o.min_p;
-  a.T_rows = o.temperature_rows;
-  a.k_rows = o.top_k_rows;
-  a.p_rows = o.top_p_rows;
-  a.min_p_rows = o.min_p_rows;
-  a.seg_max = (float*)((char*)workspace + p.o_max);
-  a.seg_sum = (double*)((char*)workspace + p.o_sum);
-  a.token = token;
-  a.lp = lp;
+  char* ws = (char*)workspace;
   hipStream_t s = (hipStream_t)stream;
-  GRPO_HIP(dtype == GRPO_BF16 ? grpo::launch_sample<__bf16>(a, B, s)
-                              : grpo::launch_sample<float>(a, B, s));
+  for (int64_t b = 0; b < B; b += p.rows) {
+    const auto off = [b](auto* rows) { return rows == nullptr ? nullptr : rows + b; };
+    grpo::SampleArgs a{};
+    a.logits = (const char*)logits + b * row_stride * (dtype == GRPO_BF16 ? 2 : 4);
+    a.u = u + b;
+    a.stride = row_stride;
+    a.V = (int)V;
+    a.segs = p.segs;
+    a.splits = p.splits;
+    a.T = o.temperature;
+    a.k = o.top_k;
+    a.p = o.top_p;
+    a.min_p = o.min_p;
+    a.T_rows = off(o.temperature_rows);
+    a.k_rows = off(o.top_k_rows);
+    a.p_rows = off(o.top_p_rows);
+    a.min_p_rows = off(o.min_p_rows);
+    a.seg_max = (float*)(ws + p.o_max);
+    a.seg_min = (float*)(ws + p.o_min);
+    a.seg_sum = (double*)(ws + p.o_sum);
+    a.grp_max = (float*)(ws + p.o_grp);
+    a.hist = (uint64_t*)(ws + p.o_hist);
+    a.z_part = (double*)(ws + p.o_z);
+    a.above = (uint64_t*)(ws + p.o_above);
+    a.whole = (uint64_t*)(ws + p.o_whole);
+    a.seg_kept = (uint64_t*)(ws + p.o_kept);
+    a.listed = (int*)(ws + p.o_listed);
+    a.list = (uint64_t*)(ws + p.o_list);
+    a.token = token + b;
+    a.lp = lp + b;
+    const int64_t rows = std::min(p.rows, B - b);
+    GRPO_HIP(dtype == GRPO_BF16 ? grpo::launch_sample<__bf16>(a, rows, s)
+                                : grpo::launch_sample<float>(a, rows, s));
+  }
   return GRPO_OK;
 }
 

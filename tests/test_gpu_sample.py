@@ -154,6 +154,38 @@ def test_largest_vocabulary_and_row_offsets_beyond_32_bits():
 def test_many_rows():
     x, u = logits(3000, 37)
     check(x, u, run(x, u, k=5, p=0.9), k=5, p=0.9)
+    x, u = logits(66000, 9)                 # more than one batch of rows
+    token, lp = (v.cpu() for v in run(x, u, k=4))
+    some = torch.arange(0, 66000, 997)
+    some[-1] = 65999
+    check(x[some], u[some], (token[some], lp[some]), k=4)
+    x, u = logits(1100, 4100)
+    params = dict(p=torch.linspace(0.3, 1.0, 1100), min_p=torch.linspace(0, 1e-3, 1100))
+    token, lp = (v.cpu() for v in run(x, u, **params))
+    some = torch.tensor([0, 1, 511, 1022, 1023, 1024, 1025, 1099])
+    check(x[some], u[some], (token[some], lp[some]), **{k: v[some] for k, v in params.items()})
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("k", [1, 2, 63, 1000, 2047, 2048, 2049])
+def test_every_size_of_the_candidates(k, t):
+    for V in (4095, 4096, 4097, 70001):
+        for p in (1.0, 0.97):
+            x, u = logits(3, V, t, seed=k)
+            x[1] = x[1].sort(descending=True).values     # all candidates side by side
+            check(x, u, run(x, u, k=k, p=p), k=k, p=p)
+
+
+@pytest.mark.parametrize("p", [0.01, 0.5, 0.9, 0.9999999])
+@pytest.mark.parametrize("scale", [0.0, 0.01, 1.0, 8.0])
+def test_nucleus_of_flat_and_peaked_rows(scale, p):
+    for t in (torch.float32, torch.bfloat16):
+        g = torch.Generator().manual_seed(11)
+        x = (torch.randn(5, 50021, generator=g) * scale + 3).to(t)
+        x[1, 100:] = float("-inf")
+        x[2, ::2] = x[2, 0]
+        u = torch.rand(5, generator=g)
+        check(x, u, run(x, u, p=p, min_p=1e-4), p=p, min_p=1e-4)
 
 
 def test_log_probability_is_the_loss_s():
