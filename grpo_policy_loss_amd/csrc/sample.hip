@@ -33,6 +33,7 @@
 namespace grpo {
 namespace {
 
+constexpr int kCUs = 256;
 constexpr int kSeg = 2048;                 // tokens per segment: one wave, 32 a lane
 constexpr int64_t kMaxVocab = 1 << 20;     // 2^20 weights of at most 2^42
 constexpr int kMaxSegs = (int)(kMaxVocab / kSeg);
@@ -53,7 +54,7 @@ struct SampleArgs {
   const float* p_rows;
   const float* min_p_rows;
   float* seg_max;      // [B, segs]; NaN where the segment holds a NaN or +inf
-  float* seg_min;      // [B, segs], of what is above -inf
+  float* seg_min;      // [B, segs], of what is above -inf: NUCLEUS all tokens, LIST the groups' maxima
   double* seg_sum;     // [B, segs], relative to the segment's own maximum (not for NUCLEUS)
   float* grp_max;      // [B, segs, 64]: a lane's 32 tokens (LIST and MIN_P)
   // NUCLEUS
@@ -72,7 +73,7 @@ enum RowClass { PLAIN, LIST, MIN_P, NUCLEUS, GENERAL };
 
 // The parameters of one row, where 0 (or anything out of range in a device array) is off.
 struct RowParams {
-  double T, inv_T, p, min_p;
+  double T, rate, p, min_p;      // rate: log2(e) / T
   int k;
   RowClass cls;
 };
@@ -80,7 +81,7 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row
   RowParams r;
   r.T = a.T_rows != nullptr ? (double)a.T_rows[row] : a.T;
   if (r.T == 0.0) r.T = 1.0;
-  r.inv_T = 1.0 / r.T;
+  r.rate = 1.4426950408889634 / r.T;
   r.k = a.k_rows != nullptr ? a.k_rows[row] : a.k;
   if (r.k <= 0 || r.k >= a.V) r.k = 0;
   r.p = a.p_rows != nullptr ? (double)a.p_rows[row] : a.p;
@@ -95,43 +96,58 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row
   return r;
 }
 
-// exp(t) for t <= 0, 0 below -700: t = n ln 2 + r with |r| <= ln 2 / 2, and the Taylor series
-// of exp(r) to the twelfth power (remainder below 2e-16).  19 instructions.
-__device__ __forceinline__ double exp_down(double t) {
-  const double n = rint(t * 1.4426950408889634);
-  double r = fma(n, -0x1.62e42fefa39efp-1, t);
-  r = fma(n, -0x1.abc9e3b39803fp-56, r);
-  double q = 1.0 / 479001600.0;
-  q = fma(q, r, 1.0 / 39916800.0);
-  q = fma(q, r, 1.0 / 3628800.0);
-  q = fma(q, r, 1.0 / 362880.0);
-  q = fma(q, r, 1.0 / 40320.0);
-  q = fma(q, r, 1.0 / 5040.0);
-  q = fma(q, r, 1.0 / 720.0);
-  q = fma(q, r, 1.0 / 120.0);
-  q = fma(q, r, 1.0 / 24.0);
-  q = fma(q, r, 1.0 / 6.0);
-  q = fma(q, r, 0.5);
-  q = fma(q, r, 1.0);
-  q = fma(q, r, 1.0);
-  return t < -700.0 ? 0.0 : ldexp(q, (int)fmax(n, -1100.0));
+// 2^t for t <= 0: t = n + f with n whole and |f| <= 1/2, and 2^f by its interpolation at the
+// Chebyshev points of degree 10 (relative error below 5e-16).  Below 2^-1000 it stays at
+// 2^-1000: nothing beside the row's maximum, whose weight is 1.
+__device__ __forceinline__ double pow2_down(double t) {
+  t = fmax(t, -1000.0);
+  const double magic = 0x1.8p52, shifted = t + magic;
+  const double f = t - (shifted - magic);
+  double q = 0x1.e6063f7217bc6p-28;
+  q = fma(q, f, 0x1.b675bca4eeebbp-24);
+  q = fma(q, f, 0x1.62bfd47773353p-20);
+  q = fma(q, f, 0x1.ffcb54062e698p-17);
+  q = fma(q, f, 0x1.430913096fd9fp-13);
+  q = fma(q, f, 0x1.5d87fe9d7a584p-10);
+  q = fma(q, f, 0x1.3b2ab6fba1ddap-7);
+  q = fma(q, f, 0x1.c6b08d703ce49p-5);
+  q = fma(q, f, 0x1.ebfbdff82c598p-3);
+  q = fma(q, f, 0x1.62e42fefa3a19p-1);
+  q = fma(q, f, 1.0);
+  // n into the exponent: q is in [0.7, 1.5] and n at least -1000
+  const int n = (int)(uint32_t)__double_as_longlong(shifted);
+  return __hiloint2double(__double2hiint(q) + n * (1 << 20), __double2loint(q));
 }
 
-// 8 consecutive logits from token c on; those at V and behind it read as -inf.  Minus zero
-// becomes zero, its equal, so that the order of the bits is the order of the values.
+// 8 consecutive logits from token c on; those at V and behind it read as -inf.  Loading and
+// unpacking are apart, so that loads can be under way while others are worked on.
+template <typename T> struct Raw8 {
+  typename Vec16<T>::type v[8 / kVec<T>];
+};
 template <typename T>
-__device__ __forceinline__ void load8(const T* row, int c, int V, float (&x)[8]) {
+__device__ __forceinline__ Raw8<T> load8(const T* row, int c, int V) {
+  Raw8<T> r;
   if (c + 8 <= V) {
 #pragma unroll
-    for (int i = 0; i < 8; i += kVec<T>) {
-      const typename Vec16<T>::type v = load_vec(row, c + i, (int64_t)V);
-#pragma unroll
-      for (int j = 0; j < kVec<T>; ++j) x[i + j] = (float)v[j] + 0.f;
-    }
+    for (int i = 0; i < 8; i += kVec<T>) r.v[i / kVec<T>] = *(const typename Vec16<T>::type*)(row + c + i);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = c + j < V ? (float)row[c + j] + 0.f : -__builtin_huge_valf();
+    for (int j = 0; j < 8; ++j) {
+      const T v = row[min(c + j, V - 1)];
+      r.v[j / kVec<T>][j % kVec<T>] = c + j < V ? v : (T)-__builtin_huge_valf();
+    }
   }
+  return r;
+}
+// Minus zero becomes zero, its equal: the order of the bits is then the order of the values.
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw8<T>& r, float (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = (float)r.v[j / kVec<T>][j % kVec<T>] + 0.f;
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int c, int V, float (&x)[8]) {
+  unpack(load8(row, c, V), x);
 }
 
 template <typename V> __device__ __forceinline__ V wave_total(V v) {
@@ -145,6 +161,13 @@ __device__ __forceinline__ float wave_top(float v) {
   return v;
 }
 __device__ __forceinline__ float wave_low(float v) { return -wave_top(-v); }
+// Of values that ascend with the lane: the least `hit` (INT32_MAX: none) and the largest `last`
+// (-1: none) of the wave, in every lane.  (An LDS atomic on one address would run lane by lane.)
+__device__ __forceinline__ void first_and_last(int& hit, int& last) {
+  const uint64_t h = __ballot(hit != INT32_MAX), t = __ballot(last >= 0);
+  hit = h ? __shfl(hit, __ffsll((unsigned long long)h) - 1, 64) : INT32_MAX;
+  last = t ? __shfl(last, 63 - __clzll((unsigned long long)t), 64) : -1;
+}
 // Sums of the lanes below this one, and (total) of all.
 template <typename V> __device__ __forceinline__ V wave_before(V v, V& total) {
   const int lane = threadIdx.x & 63;
@@ -159,38 +182,62 @@ template <typename V> __device__ __forceinline__ V wave_before(V v, V& total) {
 }
 
 // ---------------------------------------------------------------- maxima and sums
-// One wave per segment of one row.
+// One wave per segment of one row; the next segment's loads are under way while this one's
+// weights are summed.  About 20 float64 instructions a token are as many as the loads leave
+// time for.
+template <typename T> struct RawSeg {
+  Raw8<T> q[4];
+};
+template <typename T>
+__device__ __forceinline__ RawSeg<T> load_seg(const SampleArgs& a, int64_t row, int seg) {
+  const int c = seg * kSeg + (threadIdx.x & 63) * 8;
+  RawSeg<T> r;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) r.q[q] = load8((const T*)a.logits + row * a.stride, c + q * 512, a.V);
+  return r;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(256) k_sample_mass(SampleArgs a, int64_t waves) {
   const int lane = threadIdx.x & 63;
-  for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); w < waves; w += (int64_t)gridDim.x * 4) {
-    const int64_t row = w / a.segs;
-    const int seg = (int)(w - row * a.segs);
-    const RowParams r = row_params(a, row);
+  int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (w >= waves) return;
+  const int64_t step = (int64_t)gridDim.x * 4;
+  RawSeg<T> next = load_seg<T>(a, w / a.segs, (int)(w % a.segs));
+  for (;;) {
     float x[4][8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      load8((const T*)a.logits + row * a.stride, seg * kSeg + q * 512 + lane * 8, a.V, x[q]);
-    float m = x[0][0], low = __builtin_huge_valf();
-    bool bad = false;
+    for (int q = 0; q < 4; ++q) unpack(next.q[q], x[q]);
+    const bool more = w + step < waves;
+    if (more) next = load_seg<T>(a, (w + step) / a.segs, (int)((w + step) % a.segs));
+    const RowParams r = row_params(a, w / a.segs);
+    float m = x[0][0], low;
+    bool nan = false;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         m = fmaxf(m, x[q][j]);
-        if (x[q][j] > -__builtin_huge_valf()) low = fminf(low, x[q][j]);
-        bad |= !(x[q][j] < __builtin_huge_valf());
+        nan |= x[q][j] != x[q][j];
       }
+    low = m > -__builtin_huge_valf() ? m : __builtin_huge_valf();
     if (r.cls == LIST || r.cls == MIN_P) a.grp_max[w * 64 + lane] = m;
-    m = wave_top(m);
-    bad = __any(bad);
-    double s = 0.0;
-    if (r.cls == NUCLEUS) low = wave_low(low);
-    else if (!bad && m > -__builtin_huge_valf()) {
+    if (r.cls == NUCLEUS) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s += exp_down(((double)x[q][j] - (double)m) * r.inv_T);
+        for (int j = 0; j < 8; ++j)
+          if (x[q][j] > -__builtin_huge_valf()) low = fminf(low, x[q][j]);
+    }
+    if (r.cls != PLAIN) low = wave_low(low);
+    m = wave_top(m);
+    const bool bad = __any(nan) || m == __builtin_huge_valf();
+    double s = 0.0;
+    if (r.cls != NUCLEUS && m > -__builtin_huge_valf()) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += pow2_down(((double)x[q][j] - (double)m) * r.rate);
       s = wave_total(s);
     }
     if (lane == 0) {
@@ -198,6 +245,8 @@ __global__ void __launch_bounds__(256) k_sample_mass(SampleArgs a, int64_t waves
       a.seg_min[w] = low;
       a.seg_sum[w] = s;
     }
+    if (!more) return;
+    w += step;
   }
 }
 
@@ -227,7 +276,7 @@ struct RowState {
   float max;
   RowParams r;
   __device__ __forceinline__ double weight(float x) const {
-    return exp_down(((double)x - (double)max) * r.inv_T);
+    return pow2_down(((double)x - (double)max) * r.rate);
   }
 };
 
@@ -311,18 +360,21 @@ __global__ void __launch_bounds__(1024) k_sample_hist(SampleArgs a) {
   __shared__ uint64_t bins[kNucleusBins];
   __shared__ float range[3][16];
   __shared__ double zs[16];
+  const int per = (a.segs + a.splits - 1) / a.splits * kSeg;
+  const int from = blockIdx.x * per, to = min(a.V, from + per);
+  const T* x = (const T*)a.logits + row * a.stride;
+  Raw8<T> next = {};
+  if (from + (int)threadIdx.x * 8 < to) next = load8(x, from + threadIdx.x * 8, a.V);
   for (int i = threadIdx.x; i < kNucleusBins; i += 1024) bins[i] = 0;
   const RowRange g = row_range(a, row, range);      // its barrier is also the bins'
   if (!drawable(g, st.r)) return;
   st.max = g.top;
   const Binning bin = nucleus_bins(g, st.r);
-  const int per = (a.segs + a.splits - 1) / a.splits * kSeg;
-  const int from = blockIdx.x * per, to = min(a.V, from + per);
-  const T* x = (const T*)a.logits + row * a.stride;
   double z = 0.0;
   for (int c = from + threadIdx.x * 8; c < to; c += 1024 * 8) {
     float v[8];
-    load8(x, c, a.V, v);
+    unpack(next, v);
+    if (c + 1024 * 8 < to) next = load8(x, c + 1024 * 8, a.V);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const double e = st.weight(v[j]);
@@ -359,6 +411,7 @@ __global__ void __launch_bounds__(1024) k_sample_gather(SampleArgs a) {
   const Binning bin = nucleus_bins(g, st.r);
   // thread t holds bins 4t .. 4t + 3
   uint64_t h[4] = {0, 0, 0, 0}, total;
+#pragma unroll 8
   for (int s = 0; s < a.splits; ++s) {
     const uint64_t* in = a.hist + (row * a.splits + s) * kNucleusBins + 4 * threadIdx.x;
 #pragma unroll
@@ -384,25 +437,42 @@ __global__ void __launch_bounds__(1024) k_sample_gather(SampleArgs a) {
   __syncthreads();
   const int cut_bin = found, lane = threadIdx.x & 63;
   const int per = (a.segs + a.splits - 1) / a.splits;
-  const T* x = (const T*)a.logits + row * a.stride;
   const int end = min(a.segs, (int)(blockIdx.x + 1) * per);
   for (int seg = blockIdx.x * per + (threadIdx.x >> 6); seg < end; seg += 16) {
     uint64_t part = 0;
+    const RawSeg<T> raw = load_seg<T>(a, row, seg);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int c = seg * kSeg + q * 512 + lane * 8;
       float v[8];
-      load8(x, c, a.V, v);
+      unpack(raw.q[q], v);
+      unsigned in_cut = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int b = bin(v[j]);
+        in_cut |= b == cut_bin && c + j < a.V ? 1u << j : 0u;
         if (b < cut_bin) {
           const double e = st.weight(v[j]);
           if (e >= st.r.min_p) part += units(e);
-        } else if (b == cut_bin && c + j < a.V) {
-          const int slot = atomicAdd(&count, 1);
-          if (slot < kList) mine[slot] = place(v[j], c + j);
         }
+      }
+      if (__any(in_cut)) {
+        int all = 0, slot = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint64_t who = __ballot((in_cut >> j) & 1);
+          slot += __popcll(who & ((1ull << lane) - 1));
+          all += __popcll(who);
+        }
+        int first = 0;
+        if (lane == 0) first = atomicAdd(&count, all);
+        slot += __builtin_amdgcn_readfirstlane(first);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if ((in_cut >> j) & 1) {
+            if (slot < kList) mine[slot] = place(v[j], c + j);
+            ++slot;
+          }
       }
     }
     part = wave_total(part);
@@ -433,6 +503,7 @@ struct Lds {
   float range[3][16];
   uint64_t found_sum;
   int found, count;
+  int first[16], last[16];
 };
 
 // The place of the last kept token when tokens are kept in order while fewer than k were
@@ -488,14 +559,33 @@ __device__ uint64_t find_cut(const T* x, int V, const RowState& st, uint64_t flo
   return prefix;
 }
 
-// Sorts list[0, n) downwards (bitonic; the rest up to a power of two is filled with 0).
-__device__ void sort_list(uint64_t* list, int n) {
-  int size = 2;
+// Sorts list[0, n) downwards; places differ.  Up to 512: each thread counts the larger ones.
+// Above: bitonic, filled with 0 up to a power of two.
+__device__ __forceinline__ void sort_list(uint64_t* list, int n) {
+  __syncthreads();
+  if (n <= 512) {
+    const int t = threadIdx.x;
+    uint64_t own = 0;
+    int rank = 0;
+    if (t < n) {
+      own = list[t];
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) rank += list[i] > own;
+    }
+    __syncthreads();
+    if (t < n) list[rank] = own;
+    __syncthreads();
+    return;
+  }
+  int size = 1024;
   while (size < n) size <<= 1;
   for (int i = n + threadIdx.x; i < size; i += 1024) list[i] = 0;
+#pragma unroll 1
   for (int k = 2; k <= size; k <<= 1)
+#pragma unroll 1
     for (int j = k >> 1; j > 0; j >>= 1) {
       __syncthreads();
+#pragma unroll 1
       for (int t = threadIdx.x; t < size / 2; t += 1024) {
         const int lo = ((t & ~(j - 1)) << 1) | (t & (j - 1)), hi = lo | j;
         const uint64_t p = list[lo], q = list[hi];
@@ -509,67 +599,92 @@ __device__ void sort_list(uint64_t* list, int n) {
 }
 
 // The tokens that may be kept, into l.list; their number (over kList: too many).  A group is
-// 32 tokens that one lane of k_sample_mass read; only groups whose maximum may be kept are read.
+// 32 tokens that one lane of k_sample_mass read; only groups whose maximum may be kept are
+// read again.  `low`: the least of the groups' maxima.
 template <typename T>
-__device__ int candidates(const SampleArgs& a, int64_t row, const T* x, const RowState& st, Lds& l) {
+__device__ __forceinline__ int candidates(const SampleArgs& a, int64_t row, const T* x,
+                                          const RowState& st, float low, Lds& l) {
   const int groups = a.segs * 64, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const float* gm = a.grp_max + row * groups;
   const float none = -__builtin_huge_valf();
-  Binning bin(st.max, 0.f, kBins);
-  int last = kBins - 1;
-  if (st.r.cls == LIST && a.V > kList) {
-    // bins over the range of the groups' maxima; the last bin that the k largest reach into
-    float low = __builtin_huge_valf();
-    for (int i = threadIdx.x; i < kBins; i += 1024) l.counts[i] = 0;
-    for (int i = threadIdx.x; i < groups; i += 1024)
-      if (gm[i] > none) low = fminf(low, gm[i]);
-    low = wave_low(low);
-    if (lane == 0) l.range[0][wave] = low;
-    __syncthreads();
+  // 8192 groups at a time, thread t of wave w holding groups 1024 i + 64 w + lane (a segment's)
+  float g[8];
+  auto load = [&](int base) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) low = fminf(low, l.range[0][i]);
-    bin = Binning(st.max, st.max - low, kBins);
-    for (int i = threadIdx.x; i < groups; i += 1024)
-      if (gm[i] > none) atomicAdd(&l.counts[bin(gm[i])], 1u);
+    for (int i = 0; i < 8; ++i) {
+      const int at = base + i * 1024 + (int)threadIdx.x;
+      g[i] = at < groups ? gm[at] : none;
+    }
+  };
+  load(0);
+  Binning bin(st.max, 0.f, kBins);          // all that is above -inf into bin 0
+  int last = kBins - 1;
+  if (threadIdx.x == 0) {
+    l.count = 0;
+    l.found = -1;
+  }
+  if (st.r.cls == LIST && a.V > kList) {
+    // bins over the range of the groups' maxima; the last one that the k largest reach into
+    const Binning fine(st.max, st.max - low, kBins);
+    l.counts[threadIdx.x] = l.counts[threadIdx.x + 1024] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int base = 0; base < groups; base += 8192) {
+      if (base) load(base);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (g[i] > none) atomicAdd(&l.counts[fine(g[i])], 1u);
+    }
     __syncthreads();
     const int b = 2 * threadIdx.x;
     const uint64_t c0 = l.counts[b], c1 = l.counts[b + 1], k = (uint64_t)st.r.k;
     uint64_t total;
-    if (threadIdx.x == 0) l.found = kBins - 1;     // fewer groups than k: all of them
     const uint64_t before = block_before<uint64_t>(c0 + c1, l.wave_u, total);
     if (before < k && before + c0 >= k) l.found = b;
     else if (before + c0 < k && before + c0 + c1 >= k) l.found = b + 1;
     __syncthreads();
-    last = l.found;
-    if (total < k) bin = Binning(st.max, 0.f, kBins);
+    if (l.found >= 0) {                     // otherwise fewer groups than k: all of them
+      last = l.found;
+      bin = fine;
+    }
+    if (groups > 8192) load(0);
+  } else {
+    __syncthreads();
   }
-  // by bins (a scale of 0 puts all that is above -inf into bin 0), or by min_p
+  const bool by_weight = st.r.cls == MIN_P;
   auto wanted = [&](float v) {
     if (!(v > none)) return false;
-    return st.r.cls == MIN_P ? st.weight(v) >= st.r.min_p : bin(v) <= last;
+    return by_weight ? st.weight(v) >= st.r.min_p : bin(v) <= last;
   };
-  if (threadIdx.x == 0) l.count = 0;
-  __syncthreads();
-  // one wave takes 64 groups, and of those the wanted ones two at a time, 32 lanes each
-  for (int g0 = wave * 64; g0 < groups; g0 += 16 * 64) {
-    uint64_t todo = __ballot(wanted(gm[g0 + lane]));
-    while (todo) {
-      const int one = __ffsll((unsigned long long)todo) - 1;
-      todo &= todo - 1;
-      const int two = todo ? __ffsll((unsigned long long)todo) - 1 : -1;
-      todo &= todo - 1;
-      const int gl = lane < 32 ? one : two;
-      // token q * 512 + lane * 8 + j of the segment, for q < 4 and j < 8
-      const int i = lane & 31, c = g0 / 64 * kSeg + (i >> 3) * 512 + gl * 8 + (i & 7);
-      const bool in = gl >= 0 && c < a.V;
-      const float v = in ? (float)x[c] + 0.f : none;
-      const bool take = in && wanted(v);
-      const uint64_t who = __ballot(take);
-      int base = 0;
-      if (lane == 0) base = atomicAdd(&l.count, __popcll(who));
-      base = __builtin_amdgcn_readfirstlane(base);
-      const int slot = base + __popcll(who & ((1ull << lane) - 1));
-      if (take && slot < kList) l.list[slot] = place(v, c);
+#pragma unroll 1
+  for (int base = 0; base < groups; base += 8192) {
+    if (base) load(base);
+    // a bit for each of this lane's groups that is wanted
+    unsigned want = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) want |= wanted(g[i]) ? 1u << i : 0u;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      // of a segment's 64 groups the wanted ones, two at a time, 32 lanes each
+      const int seg = (base + i * 1024) / 64 + wave;
+      uint64_t todo = __ballot((want >> i) & 1u);
+      while (todo) {
+        const int one = __ffsll((unsigned long long)todo) - 1;
+        todo &= todo - 1;
+        const int two = todo ? __ffsll((unsigned long long)todo) - 1 : -1;
+        todo &= todo - 1;
+        const int gl = lane < 32 ? one : two;
+        // tokens q * 512 + gl * 8 + j of the segment, q < 4 and j < 8
+        const int k = lane & 31, c = seg * kSeg + (k >> 3) * 512 + gl * 8 + (k & 7);
+        const bool in = gl >= 0 && c < a.V;
+        const float v = in ? (float)x[c] + 0.f : none;
+        const bool take = in && wanted(v);
+        const uint64_t who = __ballot(take);
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&l.count, __popcll(who));
+        at = __builtin_amdgcn_readfirstlane(at) + __popcll(who & ((1ull << lane) - 1));
+        if (take && at < kList) l.list[at] = place(v, c);
+      }
     }
   }
   __syncthreads();
@@ -579,7 +694,7 @@ __device__ int candidates(const SampleArgs& a, int64_t row, const T* x, const Ro
 // The place of the last kept token (0: all), from a row's sorted list of n places that follow
 // on `above` units of mass; `whole` the mass that top-p is a share of (0: that of the list's
 // first k).  Adds the kept tokens' masses to l.segs_u.
-__device__ uint64_t cut_list(const RowState& st, int n, uint64_t above, uint64_t whole, Lds& l) {
+__device__ __forceinline__ uint64_t cut_list(const RowState& st, int n, uint64_t above, uint64_t whole, Lds& l) {
   sort_list(l.list, n);
   uint64_t m[4], sum = 0, total;
   double e[4];
@@ -612,7 +727,124 @@ __device__ uint64_t cut_list(const RowState& st, int n, uint64_t above, uint64_t
   return cut;
 }
 
-// One block of 1024 threads per row.
+// Rows without filters, in a kernel of its own: one block of 256 threads per row, whose time is
+// that of its four dependent loads.
+template <typename T>
+__global__ void __launch_bounds__(256) k_sample_plain(SampleArgs a) {
+  __shared__ float tops[4];
+  __shared__ int bad[4];
+  __shared__ double mass[2][4];
+  __shared__ int found[2][2][4];
+  const int64_t row = blockIdx.x;
+  const int V = a.V, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const T* x = (const T*)a.logits + row * a.stride;
+  // thread t holds segments 2t and 2t + 1
+  float m[2];
+  double s[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = 2 * threadIdx.x + j;
+    m[j] = i < a.segs ? a.seg_max[row * a.segs + i] : -__builtin_huge_valf();
+    s[j] = i < a.segs ? a.seg_sum[row * a.segs + i] : 0.0;
+  }
+  const double u = fmin(fmax((double)a.u[row], 0.0), 1.0);
+  RowState st;
+  st.r = row_params(a, row);
+  RowRange g;
+  g.bad = __any(m[0] != m[0] || m[1] != m[1]);
+  g.top = wave_top(fmaxf(m[0], m[1]));
+  if (lane == 0) {
+    tops[wave] = g.top;
+    bad[wave] = g.bad;
+  }
+  __syncthreads();
+  g.top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+  g.bad = bad[0] | bad[1] | bad[2] | bad[3];
+  st.max = g.top;
+  if (!drawable(g, st.r)) {
+    if (threadIdx.x == 0) {
+      a.token[row] = -1;
+      a.lp[row] = __builtin_nanf("");
+    }
+    return;
+  }
+  // where the running mass first exceeds u Z: the segment, then its token
+  double Z = 0.0, target = 0.0;
+  int seg = 0;
+  float v[8];
+  double e[8];
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    const int c = pass ? seg * kSeg + (int)threadIdx.x * 8 : 2 * (int)threadIdx.x;
+    double own = 0.0;
+    if (pass) {
+      load8(x, c, V, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        e[j] = v[j] > -__builtin_huge_valf() ? st.weight(v[j]) : 0.0;
+        own += e[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        e[j] = s[j] > 0.0 ? s[j] * st.weight(m[j]) : 0.0;
+        own += e[j];
+      }
+    }
+    double wt, sum = 0.0;
+    double run = wave_before(own, wt);
+    if (lane == 63) mass[pass][wave] = wt;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < wave) run += mass[pass][i];
+      sum += mass[pass][i];
+    }
+    if (!pass) {
+      Z = sum;
+      target = u * Z;
+    }
+    const double first = run;
+    int hit = INT32_MAX, last = -1;
+#pragma unroll
+    for (int j = 0; j < (pass ? 8 : 2); ++j) {
+      run += e[j];
+      if (e[j] > 0.0) {
+        if (run > target) hit = min(hit, c + j);
+        last = c + j;
+      }
+    }
+    first_and_last(hit, last);
+    if (lane == 0) {
+      found[pass][0][wave] = hit;
+      found[pass][1][wave] = last;
+    }
+    __syncthreads();
+    // (the target is the mass itself if u = 1 or by a rounding: the last that has any)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hit = min(i ? hit : INT32_MAX, found[pass][0][i]);
+      last = max(last, found[pass][1][i]);
+    }
+    if (hit == INT32_MAX) hit = last;
+    if (pass) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j == hit) {
+          a.token[row] = hit;
+          a.lp[row] = (float)(((double)v[j] - (double)st.max) / st.r.T - log(Z));
+        }
+    } else {
+      seg = hit;
+      // what lies before the segment comes off the target
+      if (hit / 2 == (int)threadIdx.x) mass[0][0] = hit & 1 ? first + e[0] : first;
+      __syncthreads();
+      target -= mass[0][0];
+    }
+  }
+}
+
+// Rows of any class: one block of 1024 threads per row.
 template <typename T>
 __global__ void __launch_bounds__(1024) k_sample_pick(SampleArgs a) {
   __shared__ Lds l;
@@ -654,11 +886,11 @@ __global__ void __launch_bounds__(1024) k_sample_pick(SampleArgs a) {
         cls = GENERAL;
       }
     } else if (cls == LIST || cls == MIN_P) {
-      const int n = candidates<T>(a, row, x, st, l);
+      const int n = candidates<T>(a, row, x, st, range.low, l);
       if (n <= kList) cut = cut_list(st, n, 0, 0, l);
       else cls = GENERAL;
     }
-    if (cls == GENERAL) {
+    if (__builtin_expect(cls == GENERAL, 0)) {
       if (st.r.k != 0) cut = find_cut<T, false>(x, V, st, 0, (uint64_t)st.r.k, 0.0, l);
       if (st.r.p != 0.0) {
         // the mass of what top-k keeps, exactly
@@ -701,17 +933,22 @@ __global__ void __launch_bounds__(1024) k_sample_pick(SampleArgs a) {
 
   const double target = fmin(fmax((double)a.u[row], 0.0), 1.0) * sum;
   // the lowest segment whose running mass exceeds the target, else the last that has any
-  if (threadIdx.x == 0) {
-    l.found = kMaxSegs;
-    l.count = 0;
+  // (the target is the mass itself if u = 1 or by a rounding)
+  const int wave = threadIdx.x >> 6;
+  int hit = s > 0.0 && at + s > target ? seg_of : INT32_MAX, end = s > 0.0 ? seg_of : -1;
+  first_and_last(hit, end);
+  if (lane == 0) {
+    l.first[wave] = hit;
+    l.last[wave] = end;
   }
   __syncthreads();
-  if (s > 0.0) {
-    if (at + s > target) atomicMin(&l.found, seg_of);
-    atomicMax(&l.count, seg_of);
+  hit = INT32_MAX;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    hit = min(hit, l.first[i]);
+    end = max(end, l.last[i]);
   }
-  __syncthreads();
-  const int seg = l.found < kMaxSegs ? l.found : l.count;
+  const int seg = hit != INT32_MAX ? hit : end;
   if (seg_of == seg) l.wave_d[0] = at;
   __syncthreads();
   const double rest = target - l.wave_d[0];
@@ -722,31 +959,38 @@ __global__ void __launch_bounds__(1024) k_sample_pick(SampleArgs a) {
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     v[j] = c + j < V ? (float)x[c + j] + 0.f : -__builtin_huge_valf();
-    e[j] = st.weight(v[j]);
+    e[j] = v[j] > -__builtin_huge_valf() ? st.weight(v[j]) : 0.0;
     if (st.r.cls != PLAIN)
       e[j] = c + j < V && place(v[j], c + j) >= cut && e[j] >= st.r.min_p ? (double)units(e[j]) * 0x1p-42 : 0.0;
   }
-  if (threadIdx.x == 0) {
-    l.found = kSeg;
-    l.count = -1;
-  }
   double run = block_before<double>(e[0] + e[1], l.wave_d, sum);
+  hit = INT32_MAX, end = -1;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     run += e[j];
     if (e[j] > 0.0) {
-      if (run > rest) atomicMin(&l.found, c + j - seg * kSeg);
-      atomicMax(&l.count, c + j - seg * kSeg);
+      if (run > rest) hit = min(hit, c + j);
+      end = c + j;
     }
   }
+  first_and_last(hit, end);
+  if (lane == 0) {
+    l.first[wave] = hit;
+    l.last[wave] = end;
+  }
   __syncthreads();
-  // (the target is the mass itself if u = 1 or by a rounding: the last token that has any)
-  const int hit = (l.found < kSeg ? l.found : l.count) + seg * kSeg;
+  hit = INT32_MAX;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    hit = min(hit, l.first[i]);
+    end = max(end, l.last[i]);
+  }
+  if (hit == INT32_MAX) hit = end;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
     if (c + j == hit) {
       a.token[row] = hit;
-      a.lp[row] = (float)(((double)v[j] - (double)st.max) * st.r.inv_T - log(Z));
+      a.lp[row] = (float)(((double)v[j] - (double)st.max) / st.r.T - log(Z));
     }
 }
 
@@ -756,13 +1000,14 @@ struct SamplePlan {
   size_t o_max, o_min, o_sum, o_grp, o_hist, o_z, o_above, o_whole, o_kept, o_listed, o_list, total;
 };
 // Rows go in batches, so that the workspace stays bounded; a row of at most kList tokens needs
-// no histogram.  Splits: about two blocks of 1024 threads per CU, each with at least 4 segments.
+// no histogram.  Splits: up to four blocks of 1024 threads per CU (rows of other classes leave theirs
+// at once), each with at least 4 segments.
 SamplePlan plan_sample(int64_t B, int64_t V) {
   SamplePlan p{};
   const bool nucleus = V > kList;
   p.rows = std::min<int64_t>(B, nucleus ? 1024 : 65536);
   p.segs = (int)((V + kSeg - 1) / kSeg);
-  p.splits = nucleus ? (int)std::max<int64_t>(1, std::min<int64_t>((p.segs + 3) / 4, 512 / p.rows)) : 0;
+  p.splits = nucleus ? (int)std::max<int64_t>(1, std::min<int64_t>((p.segs + 3) / 4, 1024 / p.rows)) : 0;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -803,7 +1048,7 @@ hipError_t launch_sample(const SampleArgs& a, int64_t rows, hipStream_t s) {
   {
     ScopedKernelTimer t(KK_SAMPLE_MASS, s);
     const int64_t waves = rows * a.segs;
-    const int64_t blocks = std::min<int64_t>((waves + 3) / 4, 1 << 20);
+    const int64_t blocks = std::min<int64_t>((waves + 3) / 4, 4 * kCUs);
     k_sample_mass<T><<<(unsigned)blocks, 256, 0, s>>>(a, waves);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
@@ -818,7 +1063,10 @@ hipError_t launch_sample(const SampleArgs& a, int64_t rows, hipStream_t s) {
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   ScopedKernelTimer t(KK_SAMPLE_PICK, s);
-  k_sample_pick<T><<<(unsigned)rows, 1024, 0, s>>>(a);
+  const bool plain = a.k_rows == nullptr && a.p_rows == nullptr && a.min_p_rows == nullptr &&
+                     (a.k == 0 || a.k >= a.V) && !(a.p > 0.0 && a.p < 1.0) && !(a.min_p > 0.0);
+  if (plain) k_sample_plain<T><<<(unsigned)rows, 256, 0, s>>>(a);
+  else k_sample_pick<T><<<(unsigned)rows, 1024, 0, s>>>(a);
   return hipGetLastError();
 }
 
