@@ -12,16 +12,17 @@
 // 2^20 tokens are exact in 64 bits: no result depends on an order.
 //
 // Rows by what their filters need, each with the fewest passes over the logits:
-//   PLAIN    no filter: one pass for maxima and sums, then one segment of 2048 tokens.
-//   LIST     top-k up to 2048 (or any filter on a row of at most 4096): the first pass keeps
-//            the maximum of every 32 tokens; at least k of these are at or above the k-th
-//            largest of them, so every kept token is, and only groups whose maximum is get
-//            read again.  The candidates are sorted in LDS, where top-p and min-p are a cut.
-//   MIN_P    the same with the bound max + T log min_p.
-//   NUCLEUS  top-p alone: a histogram of the mass over 4096 bins of x finds the bin that the
-//            cut falls into; one more pass sums what lies above and lists that bin's tokens.
-//   GENERAL  everything else (larger k, lists that overflow as on rows of equal logits): the
-//            cut digit by digit, one pass over the row for each of its 5 digits.
+//   PLAIN   no filter: one pass for maxima and sums, then one segment of 2048 tokens.
+//   LIST    top-k up to 2048, with or without the others, or any filter on a row of at most
+//           4096: the first pass keeps the maximum of every 32 tokens; at least k of these
+//           are at or above the k-th largest of them, so every kept token is, and only the
+//           groups whose maximum is are read again.  The cuts are found among those candidates.
+//   MIN_P   min-p alone: one more pass over the segments whose maximum reaches min_p.
+//   HIST    top-p, alone or with a larger k: histograms of mass and count over 4096 bins of x
+//           tell which bins the cuts fall into; one more pass sums what lies above them and
+//           lists the tokens of those bins, among which the cuts are found.
+// Lists hold up to 4096 tokens; where one overflows (equal logits), the cuts are found among
+// all tokens of the row, by the same search in up to five passes.
 #include <math.h>
 
 #include <algorithm>
@@ -37,10 +38,22 @@ constexpr int kCUs = 256;
 constexpr int kSeg = 2048;                 // tokens per segment: one wave, 32 a lane
 constexpr int64_t kMaxVocab = 1 << 20;     // 2^20 weights of at most 2^42
 constexpr int kMaxSegs = (int)(kMaxVocab / kSeg);
-constexpr int kBins = 2048;                // of one digit, and of the groups' maxima
-constexpr int kNucleusBins = 4096;
-constexpr int kList = 4096;                // candidates that are sorted in LDS
+constexpr int kHistBins = 4096;
+constexpr int kHistThreads = 512;
+constexpr int kBins = 2048;                // of the groups' maxima, and of one pass of a search
+constexpr int kList = 4096;                // listed tokens of a row
 constexpr int kListK = 2048;               // largest top-k that goes by the groups' maxima
+constexpr int kPick = 256;                 // threads of a row's last step
+constexpr float kNone = -__builtin_huge_valf();
+
+// What HIST's gather and pick need to know: tokens in bins below `sure` are kept (but for
+// min-p); those of bins lo .. hi and of bin kbin are listed.  The offsets make ranks and running
+// masses among the listed tokens those among all that matter: see k_sample_cut.
+struct RowCut {
+  int sure, lo, hi, kbin;
+  int k, pad;
+  uint64_t count_off, mass_off, z_off;
+};
 
 struct SampleArgs {
   const void* logits;
@@ -54,22 +67,22 @@ struct SampleArgs {
   const float* p_rows;
   const float* min_p_rows;
   float* seg_max;      // [B, segs]; NaN where the segment holds a NaN or +inf
-  float* seg_min;      // [B, segs], of what is above -inf: NUCLEUS all tokens, LIST the groups' maxima
-  double* seg_sum;     // [B, segs], relative to the segment's own maximum (not for NUCLEUS)
-  float* grp_max;      // [B, segs, 64]: a lane's 32 tokens (LIST and MIN_P)
-  // NUCLEUS
-  uint64_t* hist;      // [B, splits, kNucleusBins]
+  float* seg_min;      // [B, segs], of what is above -inf: HIST all tokens, LIST the groups' maxima
+  double* seg_sum;     // [B, segs], relative to the segment's own maximum (not for HIST)
+  float* grp_max;      // [B, segs, 64]: a lane's 32 tokens (LIST)
+  uint64_t* seg_kept;  // [B, segs]: mass that is surely kept (HIST, MIN_P)
+  int* listed;         // [B]: tokens in the list
+  // HIST
+  uint64_t* hist;      // [B, splits, kHistBins]: masses
+  uint32_t* hist_n;    // [B, splits, kHistBins]: counts
   double* z_part;      // [B, splits]
-  uint64_t* above;     // [B]: mass above the cut's bin
-  uint64_t* whole;     // [B]: mass of the row
-  uint64_t* seg_kept;  // [B, segs]: mass above the cut's bin, by segment
-  int* listed;         // [B]: tokens in the cut's bin
-  uint64_t* list;      // [B, kList]: their places
+  RowCut* cut;         // [B]
+  uint64_t* list;      // [B, kList]: places
   int32_t* token;
   float* lp;
 };
 
-enum RowClass { PLAIN, LIST, MIN_P, NUCLEUS, GENERAL };
+enum RowClass { PLAIN, LIST, MIN_P, HIST };
 
 // The parameters of one row, where 0 (or anything out of range in a device array) is off.
 struct RowParams {
@@ -91,8 +104,7 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row
   if (r.min_p > 1.0) r.min_p = 1.0;
   if (r.k == 0 && r.p == 0.0 && r.min_p == 0.0) r.cls = PLAIN;
   else if (a.V <= kList || (r.k != 0 && r.k <= kListK)) r.cls = LIST;
-  else if (r.k != 0) r.cls = GENERAL;
-  else r.cls = r.p != 0.0 ? NUCLEUS : MIN_P;
+  else r.cls = r.k != 0 || r.p != 0.0 ? HIST : MIN_P;
   return r;
 }
 
@@ -198,7 +210,7 @@ __device__ __forceinline__ RawSeg<T> load_seg(const SampleArgs& a, int64_t row, 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) k_sample_mass(SampleArgs a, int64_t waves) {
+__global__ void __launch_bounds__(256, 4) k_sample_mass(SampleArgs a, int64_t waves) {
   const int lane = threadIdx.x & 63;
   int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (w >= waves) return;
@@ -220,20 +232,20 @@ __global__ void __launch_bounds__(256) k_sample_mass(SampleArgs a, int64_t waves
         m = fmaxf(m, x[q][j]);
         nan |= x[q][j] != x[q][j];
       }
-    low = m > -__builtin_huge_valf() ? m : __builtin_huge_valf();
-    if (r.cls == LIST || r.cls == MIN_P) a.grp_max[w * 64 + lane] = m;
-    if (r.cls == NUCLEUS) {
+    low = m > kNone ? m : __builtin_huge_valf();
+    if (r.cls == LIST) a.grp_max[w * 64 + lane] = m;
+    if (r.cls == HIST) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (x[q][j] > -__builtin_huge_valf()) low = fminf(low, x[q][j]);
+          if (x[q][j] > kNone) low = fminf(low, x[q][j]);
     }
     if (r.cls != PLAIN) low = wave_low(low);
     m = wave_top(m);
     const bool bad = __any(nan) || m == __builtin_huge_valf();
     double s = 0.0;
-    if (r.cls != NUCLEUS && m > -__builtin_huge_valf()) {
+    if (r.cls != HIST && m > kNone) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -244,13 +256,14 @@ __global__ void __launch_bounds__(256) k_sample_mass(SampleArgs a, int64_t waves
       a.seg_max[w] = bad ? __builtin_nanf("") : m;
       a.seg_min[w] = low;
       a.seg_sum[w] = s;
+      if (w % a.segs == 0) a.listed[w / a.segs] = 0;
     }
     if (!more) return;
     w += step;
   }
 }
 
-// ---------------------------------------------------------------- the cut and the token
+// ---------------------------------------------------------------- the order
 // A token's place in the order, larger first: the bits of x in ascending order, then the index
 // reversed.
 __device__ __forceinline__ uint64_t place(float x, int i) {
@@ -294,8 +307,8 @@ struct Binning {
   }
 };
 
-// Sums over the block's 1024 threads of the values before this thread's, and the total.
-template <typename V>
+// Sums over a block of NT threads of the values before this thread's, and the total.
+template <int NT, typename V>
 __device__ __forceinline__ V block_before(V v, V* lds, V& total) {
   V wt;
   const V before = wave_before(v, wt);
@@ -305,461 +318,565 @@ __device__ __forceinline__ V block_before(V v, V* lds, V& total) {
   V off = 0;
   total = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < NT / 64; ++i) {
     if (i < (int)(threadIdx.x >> 6)) off += lds[i];
     total += lds[i];
   }
   return off + before;
 }
 
-// A row's maximum over its segments, whether it holds a NaN or +inf, and its minimum above
-// -inf, for a block of 1024 threads (lds: 16 of each).
+// A row's maximum over its segments, whether it holds a NaN or +inf, and the least of the
+// segments' minima, from each thread's share of them (lds: 3 for each wave).
 struct RowRange {
   float top, low;
   bool bad;
 };
-__device__ __forceinline__ RowRange row_range(const SampleArgs& a, int64_t row, float (*lds)[16]) {
-  const int i = threadIdx.x;
-  RowRange r;
-  r.top = i < a.segs ? a.seg_max[row * a.segs + i] : -__builtin_huge_valf();
-  r.low = i < a.segs ? a.seg_min[row * a.segs + i] : __builtin_huge_valf();
-  r.bad = __any(r.top != r.top);
-  r.top = wave_top(r.top);
-  r.low = wave_low(r.low);
+template <int NT>
+__device__ __forceinline__ RowRange row_range(float top, float low, bool bad, float (*lds)[NT / 64]) {
+  RowRange r{wave_top(top), wave_low(low), (bool)__any(bad)};
   if ((threadIdx.x & 63) == 0) {
-    lds[0][i >> 6] = r.top;
-    lds[1][i >> 6] = r.low;
-    lds[2][i >> 6] = r.bad ? 1.f : 0.f;
+    const int w = threadIdx.x >> 6;
+    lds[0][w] = r.top;
+    lds[1][w] = r.low;
+    lds[2][w] = r.bad ? 1.f : 0.f;
   }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 16; ++w) {
+  for (int w = 0; w < NT / 64; ++w) {
     r.top = fmaxf(r.top, lds[0][w]);
     r.low = fminf(r.low, lds[1][w]);
     r.bad |= lds[2][w] != 0.f;
   }
   return r;
 }
+template <int NT>
+__device__ __forceinline__ RowRange row_range(const SampleArgs& a, int64_t row, float (*lds)[NT / 64]) {
+  float top = kNone, low = -kNone;
+  bool bad = false;
+#pragma unroll
+  for (int i = threadIdx.x; i < kMaxSegs; i += NT)
+    if (i < a.segs) {
+      const float m = a.seg_max[row * a.segs + i];
+      top = fmaxf(top, m);
+      bad |= m != m;
+      low = fminf(low, a.seg_min[row * a.segs + i]);
+    }
+  return row_range<NT>(top, low, bad, lds);
+}
 // Whether there is anything to draw from.
 __device__ __forceinline__ bool drawable(const RowRange& g, const RowParams& r) {
-  return !g.bad && g.top > -__builtin_huge_valf() && r.T > 0.0 && r.T < __builtin_huge_val();
+  return !g.bad && g.top > kNone && r.T > 0.0 && r.T < __builtin_huge_val();
 }
-// Over 30 T below the maximum, 2^20 tokens weigh less than 10^-6 of it.
-__device__ __forceinline__ Binning nucleus_bins(const RowRange& g, const RowParams& r) {
-  return Binning(g.top, fminf(g.top - g.low, (float)(30.0 * r.T)), kNucleusBins);
+// Over 30 T below the maximum, 2^20 tokens weigh less than 10^-6 of it.  With a k, the bins go
+// down to the minimum: tokens without weight count too.
+__device__ __forceinline__ Binning hist_bins(const RowRange& g, const RowParams& r) {
+  const float all = g.top - g.low;
+  return Binning(g.top, r.k != 0 ? all : fminf(all, (float)(30.0 * r.T)), kHistBins);
 }
 
-// ---------------------------------------------------------------- NUCLEUS
-// Block (split, row): the mass of the split's tokens by bin.
+// ---------------------------------------------------------------- HIST
+// Block (split, row): the mass and number of the split's tokens by bin.
 template <typename T>
-__global__ void __launch_bounds__(1024) k_sample_hist(SampleArgs a) {
+__global__ void __launch_bounds__(kHistThreads) k_sample_hist(SampleArgs a) {
+  constexpr int NT = kHistThreads;
   const int64_t row = blockIdx.y;
   RowState st;
   st.r = row_params(a, row);
-  if (st.r.cls != NUCLEUS) return;
-  __shared__ uint64_t bins[kNucleusBins];
-  __shared__ float range[3][16];
-  __shared__ double zs[16];
+  if (st.r.cls != HIST) return;
+  __shared__ uint64_t mass[kHistBins];
+  __shared__ uint32_t number[kHistBins];
+  __shared__ float range[3][NT / 64];
+  __shared__ double zs[NT / 64];
   const int per = (a.segs + a.splits - 1) / a.splits * kSeg;
-  const int from = blockIdx.x * per, to = min(a.V, from + per);
+  const int from = min(a.V, (int)blockIdx.x * per), to = min(a.V, from + per);
   const T* x = (const T*)a.logits + row * a.stride;
   Raw8<T> next = {};
   if (from + (int)threadIdx.x * 8 < to) next = load8(x, from + threadIdx.x * 8, a.V);
-  for (int i = threadIdx.x; i < kNucleusBins; i += 1024) bins[i] = 0;
-  const RowRange g = row_range(a, row, range);      // its barrier is also the bins'
+  for (int i = threadIdx.x; i < kHistBins; i += NT) mass[i] = number[i] = 0;
+  const RowRange g = row_range<NT>(a, row, range);      // its barrier is also the bins'
   if (!drawable(g, st.r)) return;
   st.max = g.top;
-  const Binning bin = nucleus_bins(g, st.r);
+  const Binning bin = hist_bins(g, st.r);
+  const bool counted = st.r.k != 0;
   double z = 0.0;
-  for (int c = from + threadIdx.x * 8; c < to; c += 1024 * 8) {
+  for (int c = from + threadIdx.x * 8; c < to; c += NT * 8) {
     float v[8];
     unpack(next, v);
-    if (c + 1024 * 8 < to) next = load8(x, c + 1024 * 8, a.V);
+    if (c + NT * 8 < to) next = load8(x, c + NT * 8, a.V);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const double e = st.weight(v[j]);
-      z += e;
       const uint64_t n = units(e);
-      if (n) atomicAdd((unsigned long long*)&bins[bin(v[j])], (unsigned long long)n);
+      const int b = bin(v[j]);
+      z += e;
+      if (n) atomicAdd((unsigned long long*)&mass[b], (unsigned long long)n);
+      if (counted && v[j] > kNone) atomicAdd(&number[b], 1u);
     }
   }
   double total;
-  block_before<double>(z, zs, total);
-  uint64_t* out = a.hist + (row * a.splits + blockIdx.x) * kNucleusBins;
-  for (int i = threadIdx.x; i < kNucleusBins; i += 1024) out[i] = bins[i];
-  if (threadIdx.x == 0) {
-    a.z_part[row * a.splits + blockIdx.x] = total;
-    if (blockIdx.x == 0) a.listed[row] = 0;
+  block_before<NT, double>(z, zs, total);
+  const int64_t at = (row * a.splits + blockIdx.x) * kHistBins;
+  for (int i = threadIdx.x; i < kHistBins; i += NT) {
+    a.hist[at + i] = mass[i];
+    if (counted) a.hist_n[at + i] = number[i];
   }
+  if (threadIdx.x == 0) a.z_part[row * a.splits + blockIdx.x] = total;
+
 }
 
-// Block (split, row): the bin that the cut falls into, the mass above it by segment and the
-// places of its tokens.
+// One block per row: adds the splits up and finds the bins of the cuts.  (The last block of a row
+// could do it in k_sample_hist, but its release fence writes back the whole L2: 200 us.)
+//
+// Let kbin be the bin of the k-th token, and lo .. hi the bins in which the share p of the mass
+// may be reached: it is of the mass of the first k, which lies between that above kbin and that
+// with kbin.  Listed are bins lo .. hi and kbin.  Among the listed tokens, in their order:
+//   rank + count_off   is the rank among all for those of kbin, and less for the others;
+//   mass + mass_off    is the mass before among all for those of lo .. hi, and at least the
+//                      share for those of kbin behind them;
+//   z_off + the mass of the listed ones up to rank k is that of the first k of all.
+__global__ void __launch_bounds__(kHistThreads) k_sample_cut(SampleArgs a) {
+  constexpr int NT = kHistThreads, PER = kHistBins / NT;
+  const int64_t row = blockIdx.x;
+  RowState st;
+  st.r = row_params(a, row);
+  if (st.r.cls != HIST) return;
+  __shared__ float range[3][NT / 64];
+  __shared__ uint64_t sums[NT / 64];
+  __shared__ RowCut rc;
+  __shared__ uint64_t above_k, with_k;
+  const bool counted = st.r.k != 0;
+  if (!drawable(row_range<NT>(a, row, range), st.r)) return;
+  // thread t holds bins PER t ..
+  uint64_t h[PER], own = 0, whole;
+  uint32_t n[PER], own_n = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) h[j] = n[j] = 0;
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const int64_t from_s = (row * a.splits + s) * kHistBins + PER * threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) h[j] += a.hist[from_s + j];
+    if (counted) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) n[j] += a.hist_n[from_s + j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    own += h[j];
+    own_n += n[j];
+  }
+  if (threadIdx.x == 0) rc = RowCut{0, 1, 0, -1, 0, 0, 0, 0, 0};
+  const uint64_t first = block_before<NT, uint64_t>(own, sums, whole);
+  uint64_t n_all, n_run = 0, k = (uint64_t)st.r.k;
+  if (counted) {
+    n_run = block_before<NT, uint64_t>(own_n, sums, n_all);
+    uint64_t run = first;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      if (n_run < k && n_run + n[j] >= k) {          // one thread's, if any
+        rc.kbin = rc.sure = PER * threadIdx.x + j;
+        rc.k = st.r.k;
+        rc.count_off = n_run;
+        above_k = run;
+        with_k = run + h[j];
+      }
+      n_run += n[j];
+      run += h[j];
+    }
+    __syncthreads();
+  }
+  const int kbin = rc.kbin;                          // -1: no k, or fewer tokens than k
+  if (st.r.p != 0.0) {
+    const double least = st.r.p * (double)(kbin >= 0 ? above_k : whole);
+    const double most = st.r.p * (double)(kbin >= 0 ? with_k : whole);
+    uint64_t run = first;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      if (h[j] && (double)run < most && (double)(run + h[j]) >= most) rc.hi = PER * threadIdx.x + j;
+      if (h[j] && (double)run < least && (double)(run + h[j]) >= least) {
+        rc.lo = rc.sure = PER * threadIdx.x + j;
+        rc.mass_off = run;
+      }
+      run += h[j];
+    }
+    if (threadIdx.x == 0 && !(least > 0.0)) rc.lo = rc.sure = 0, rc.mass_off = 0;
+    __syncthreads();
+    // what is listed but for kbin
+    uint64_t listed = 0, listed_n = 0, sum, sum_n;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int b = PER * threadIdx.x + j;
+      if (b >= rc.lo && b <= rc.hi && b != kbin) {
+        listed += h[j];
+        listed_n += n[j];
+      }
+    }
+    block_before<NT, uint64_t>(listed, sums, sum);
+    block_before<NT, uint64_t>(listed_n, sums, sum_n);
+    if (threadIdx.x == 0) {
+      rc.z_off = (kbin >= 0 ? above_k : whole) - sum;
+      if (kbin >= 0) rc.count_off -= sum_n;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) a.cut[row] = rc;
+}
+
+// Block (four segments, row) of HIST and MIN_P: the surely kept mass of each segment and the
+// list of what is not sure.  Segments whose maximum is below both are left out.
 template <typename T>
-__global__ void __launch_bounds__(1024) k_sample_gather(SampleArgs a) {
+__global__ void __launch_bounds__(256) k_sample_gather(SampleArgs a) {
   const int64_t row = blockIdx.y;
   RowState st;
   st.r = row_params(a, row);
-  if (st.r.cls != NUCLEUS) return;
-  __shared__ float range[3][16];
-  __shared__ uint64_t sums[16];
-  __shared__ uint64_t mine[kList];
-  __shared__ int found, count, at;
-  const RowRange g = row_range(a, row, range);
-  if (!drawable(g, st.r)) return;
+  if (st.r.cls != HIST && st.r.cls != MIN_P) return;
+  __shared__ float range[3][4];
+  const int seg = min(a.segs - 1, (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
+  const float top = a.seg_max[row * a.segs + seg];
+  RowCut rc{INT32_MAX, 1, 0, -1, 0, 0, 0, 0, 0};
+  if (st.r.cls == HIST) rc = a.cut[row];
+  const RawSeg<T> raw = load_seg<T>(a, row, seg);       // on its way while the row's range is found
+  const RowRange g = row_range<256>(a, row, range);
+  if (!drawable(g, st.r) || blockIdx.x * 4 + (threadIdx.x >> 6) >= (unsigned)a.segs) return;
   st.max = g.top;
-  const Binning bin = nucleus_bins(g, st.r);
-  // thread t holds bins 4t .. 4t + 3
-  uint64_t h[4] = {0, 0, 0, 0}, total;
-#pragma unroll 8
-  for (int s = 0; s < a.splits; ++s) {
-    const uint64_t* in = a.hist + (row * a.splits + s) * kNucleusBins + 4 * threadIdx.x;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) h[j] += in[j];
+  Binning bin(g.top, 0.f, kHistBins);
+  bool read = st.weight(top) >= st.r.min_p;
+  if (st.r.cls == HIST) {
+    bin = hist_bins(g, st.r);
+    const int b = bin(top);
+    read = b < rc.sure || b <= rc.hi || b <= rc.kbin;
   }
-  if (threadIdx.x == 0) {
-    found = kNucleusBins - 1;
-    count = 0;
-  }
-  uint64_t run = block_before<uint64_t>(h[0] + h[1] + h[2] + h[3], sums, total);
-  const double mass = st.r.p * (double)total;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (h[j] && (double)run < mass && (double)(run + h[j]) >= mass) {
-      found = 4 * threadIdx.x + j;       // one thread's: the sums ascend
-      if (blockIdx.x == 0) {
-        a.above[row] = run;
-        a.whole[row] = total;
-      }
-    }
-    run += h[j];
-  }
-  __syncthreads();
-  const int cut_bin = found, lane = threadIdx.x & 63;
-  const int per = (a.segs + a.splits - 1) / a.splits;
-  const int end = min(a.segs, (int)(blockIdx.x + 1) * per);
-  for (int seg = blockIdx.x * per + (threadIdx.x >> 6); seg < end; seg += 16) {
-    uint64_t part = 0;
-    const RawSeg<T> raw = load_seg<T>(a, row, seg);
+  uint64_t part = 0;
+  if (read) {
+    const int c0 = seg * kSeg + lane * 8;
+    unsigned unsure = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int c = seg * kSeg + q * 512 + lane * 8;
       float v[8];
       unpack(raw.q[q], v);
-      unsigned in_cut = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int b = bin(v[j]);
-        in_cut |= b == cut_bin && c + j < a.V ? 1u << j : 0u;
-        if (b < cut_bin) {
+        if (b < rc.sure) {
           const double e = st.weight(v[j]);
           if (e >= st.r.min_p) part += units(e);
         }
+        if (((b >= rc.lo && b <= rc.hi) || b == rc.kbin) && v[j] > kNone) unsure |= 1u << (q * 8 + j);
       }
-      if (__any(in_cut)) {
-        int all = 0, slot = 0;
+    }
+    part = wave_total(part);
+    if (__any(unsure != 0)) {
+      int all, slot = wave_before((int)__popc(unsure), all), first = 0;
+      if (lane == 0) first = atomicAdd(&a.listed[row], all);
+      slot += __builtin_amdgcn_readfirstlane(first);
+      // more than kList in all: the pick sees the number and goes by the row
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint64_t who = __ballot((in_cut >> j) & 1);
-          slot += __popcll(who & ((1ull << lane) - 1));
-          all += __popcll(who);
-        }
-        int first = 0;
-        if (lane == 0) first = atomicAdd(&count, all);
-        slot += __builtin_amdgcn_readfirstlane(first);
+      for (int q = 0; q < 4; ++q) {
+        float v[8];
+        unpack(raw.q[q], v);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if ((in_cut >> j) & 1) {
-            if (slot < kList) mine[slot] = place(v[j], c + j);
+          if ((unsure >> (q * 8 + j)) & 1) {
+            if (slot < kList) a.list[row * kList + slot] = place(v[j], c0 + q * 512 + j);
             ++slot;
           }
       }
     }
-    part = wave_total(part);
-    if (lane == 0) a.seg_kept[row * a.segs + seg] = part;
   }
-  __syncthreads();
-  const int n = count;
-  if (threadIdx.x == 0) at = n ? atomicAdd(&a.listed[row], n) : 0;
-  __syncthreads();
-  // more than kList in all, or in this block: the pick sees the count and goes by digits
-  for (int i = threadIdx.x; i < min(n, kList); i += 1024)
-    if (at + i < kList) a.list[row * kList + at + i] = mine[i];
+  if (lane == 0) a.seg_kept[row * a.segs + seg] = part;
 }
 
 // ---------------------------------------------------------------- the pick
 struct Lds {
+  uint64_t list[kList];
   union {
     uint64_t bins[kBins];
-    uint64_t list[kList];
-    unsigned counts[kBins];
+    uint32_t counts[kBins];
+    int groups[2 * kBins];
   };
-  union {
-    uint64_t segs_u[kMaxSegs];
-    double segs[kMaxSegs];
-  };
-  uint64_t wave_u[16];
-  double wave_d[16];
-  float range[3][16];
-  uint64_t found_sum;
+  uint64_t segs[kMaxSegs];
+  uint64_t wave_u[kPick / 64];
+  uint64_t found_sum, result;
   int found, count;
-  int first[16], last[16];
 };
 
-// The place of the last kept token when tokens are kept in order while fewer than k were
-// before (count), or while the mass before them is below `mass` units; only tokens at `floor`
-// or above are looked at.  0 if all of them are kept.  Digit by digit over the 52 bits of a
-// place: a histogram over the tokens that share the digits so far, and the bin that the border
-// falls into.
-template <typename T, bool MASS>
-__device__ uint64_t find_cut(const T* x, int V, const RowState& st, uint64_t floor, uint64_t k,
-                             double mass, Lds& l) {
-  constexpr int width[5] = {11, 11, 10, 10, 10};
-  uint64_t prefix = 0, above = 0;
-  int shift = 52;
-  for (int d = 0; d < 5; ++d) {
-    const uint64_t top = prefix;             // digits so far
-    const int upper = shift;
-    shift -= width[d];
+// The place, in [lo, hi], of the token with which the running count (or mass, in units) reaches
+// `target`, in order from the top, `base` of it lying above hi; lo if it does not.  each(f) calls
+// f for the place of every token.  Passes over ever smaller ranges, of 2048 bins each, until 256
+// tokens are left, which are compared directly.
+template <bool MASS, typename Each>
+__device__ __forceinline__ uint64_t search(const Each& each, uint64_t lo, uint64_t hi, uint64_t base,
+                                           double target, const RowState& st, Lds& l) {
+  const auto amount = [&](uint64_t p) { return MASS ? units(st.weight(value_at(p))) : (uint64_t)1; };
+  const auto reached = [&](uint64_t sum) { return (double)sum >= target; };
+  for (;;) {
+    const uint64_t span = hi - lo;
+    const int shift = span < kBins ? 0 : 64 - __clzll((long long)span) - 11;
     __syncthreads();
-    for (int i = threadIdx.x; i < kBins; i += 1024) l.bins[i] = 0;
-    __syncthreads();
-    for (int c = threadIdx.x * 8; c < V; c += 1024 * 8) {
-      float v[8];
-      load8(x, c, V, v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint64_t pl = place(v[j], c + j);
-        if (c + j >= V || pl < floor || (pl >> upper) != top) continue;
-        const uint64_t add = MASS ? units(st.weight(v[j])) : 1;
-        if (add) atomicAdd((unsigned long long*)&l.bins[(pl >> shift) & ((1 << width[d]) - 1)], (unsigned long long)add);
+    for (int i = 0; i < kBins / kPick; ++i) l.bins[threadIdx.x + i * kPick] = 0;
+    if (threadIdx.x == 0) {
+      l.found = -1;
+      l.count = 0;
+    }
+    __syncthreads();
+    each([&](uint64_t p) {
+      if (p < lo || p > hi) return;
+      const uint64_t n = amount(p);
+      if (n) atomicAdd((unsigned long long*)&l.bins[(hi - p) >> shift], (unsigned long long)n);
+    });
+    __syncthreads();
+    constexpr int PER = kBins / kPick;
+    uint64_t h[PER], own = 0, total;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      h[j] = l.bins[PER * threadIdx.x + j];
+      own += h[j];
+    }
+    uint64_t run = base + block_before<kPick, uint64_t>(own, l.wave_u, total);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      if (h[j] && !reached(run) && reached(run + h[j])) {
+        l.found = PER * threadIdx.x + j;
+        l.found_sum = run;
       }
+      run += h[j];
     }
     __syncthreads();
-    // from the top bin down: thread t holds bins n - 1 - 2t and n - 2 - 2t
-    const int n = 1 << width[d], b0 = n - 1 - 2 * (int)threadIdx.x;
-    const uint64_t s0 = b0 >= 0 ? l.bins[b0] : 0, s1 = b0 >= 1 ? l.bins[b0 - 1] : 0;
-    uint64_t total;
-    const uint64_t before = above + block_before<uint64_t>(s0 + s1, l.wave_u, total);
-    if (threadIdx.x == 0) l.found = -1;
+    if (l.found < 0) return lo;
+    base = l.found_sum;
+    hi -= (uint64_t)l.found << shift;
+    const uint64_t rest = ((uint64_t)1 << shift) - 1;
+    if (hi - lo > rest) lo = hi - rest;
+    if (lo == hi) return lo;
+    // the bin's tokens, if they are few
+    each([&](uint64_t p) {
+      if (p < lo || p > hi) return;
+      const int slot = atomicAdd(&l.count, 1);
+      if (slot < kPick) l.bins[slot] = p;
+    });
     __syncthreads();
-    auto reaches = [&](uint64_t sum) { return MASS ? (double)sum >= mass : sum >= k; };
-    if (s0 && !reaches(before) && reaches(before + s0)) {
-      l.found = b0;
-      l.found_sum = before;
-    } else if (s1 && !reaches(before + s0) && reaches(before + s0 + s1)) {
-      l.found = b0 - 1;
-      l.found_sum = before + s0;
-    }
-    __syncthreads();
-    if (l.found < 0) return 0;               // the border lies behind the last token
-    above = l.found_sum;
-    prefix = (top << width[d]) | (uint64_t)l.found;
-  }
-  return prefix;
-}
-
-// Sorts list[0, n) downwards; places differ.  Up to 512: each thread counts the larger ones.
-// Above: bitonic, filled with 0 up to a power of two.
-__device__ __forceinline__ void sort_list(uint64_t* list, int n) {
-  __syncthreads();
-  if (n <= 512) {
+    const int n = l.count;
+    if (n > kPick) continue;
     const int t = threadIdx.x;
-    uint64_t own = 0;
-    int rank = 0;
-    if (t < n) {
-      own = list[t];
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) rank += list[i] > own;
-    }
+    const uint64_t p = t < n ? l.bins[t] : 0, mine = t < n ? amount(p) : 0;
+    if (t < n) l.bins[kPick + t] = mine;
     __syncthreads();
-    if (t < n) list[rank] = own;
+    uint64_t before = base;
+    for (int i = 0; i < n; ++i)
+      if (l.bins[i] > p) before += l.bins[kPick + i];
+    if (mine && !reached(before) && reached(before + mine)) l.result = p;
     __syncthreads();
-    return;
+    return l.result;
   }
-  int size = 1024;
-  while (size < n) size <<= 1;
-  for (int i = n + threadIdx.x; i < size; i += 1024) list[i] = 0;
-#pragma unroll 1
-  for (int k = 2; k <= size; k <<= 1)
-#pragma unroll 1
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      __syncthreads();
-#pragma unroll 1
-      for (int t = threadIdx.x; t < size / 2; t += 1024) {
-        const int lo = ((t & ~(j - 1)) << 1) | (t & (j - 1)), hi = lo | j;
-        const uint64_t p = list[lo], q = list[hi];
-        if ((p < q) == ((lo & k) == 0)) {
-          list[lo] = q;
-          list[hi] = p;
-        }
-      }
-    }
-  __syncthreads();
 }
 
-// The tokens that may be kept, into l.list; their number (over kList: too many).  A group is
-// 32 tokens that one lane of k_sample_mass read; only groups whose maximum may be kept are
+// The place of the last kept token among n tokens that each(f) goes through, with the offsets of
+// RowCut.  Up to 256 of them (the usual top-k) are compared directly: each thread ranks one.
+template <typename Each>
+__device__ __forceinline__ uint64_t last_kept(const Each& each, int n, const RowCut& rc, const RowState& st,
+                                              Lds& l) {
+  const int t = threadIdx.x;
+  const uint64_t k = rc.k != 0 ? (uint64_t)rc.k : ~(uint64_t)0;
+  if (n <= kPick) {
+    const uint64_t p = t < n ? l.list[t] : 0, mine = t < n ? units(st.weight(value_at(p))) : 0;
+    if (t < n) l.bins[t] = mine;
+    if (t == 0) l.result = ~(uint64_t)0;
+    __syncthreads();
+    uint64_t rank = rc.count_off, before = rc.mass_off, first_k;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i)
+      if (l.list[i] > p) {
+        ++rank;
+        before += l.bins[i];
+      }
+    bool keep = t < n && rank < k;
+    if (st.r.p != 0.0) {
+      block_before<kPick, uint64_t>(keep ? mine : 0, l.wave_u, first_k);
+      keep = keep && (double)before < st.r.p * (double)(rc.z_off + first_k);
+    }
+    // the least of the kept places: one lane a wave
+    uint64_t least = keep ? p : ~(uint64_t)0;
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+      const uint64_t other = __shfl_xor((unsigned long long)least, o, 64);
+      least = other < least ? other : least;
+    }
+    if ((t & 63) == 0) atomicMin((unsigned long long*)&l.result, (unsigned long long)least);
+    __syncthreads();
+    return l.result;
+  }
+  // the range of the places
+  uint64_t top = 0, cut = 0;
+  each([&](uint64_t p) { top = p > top ? p : top; });
+  if (t == 0) l.result = 0;
+  __syncthreads();
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    const uint64_t other = __shfl_xor((unsigned long long)top, o, 64);
+    top = other > top ? other : top;
+  }
+  if ((t & 63) == 0) atomicMax((unsigned long long*)&l.result, (unsigned long long)top);
+  __syncthreads();
+  top = l.result;
+  if (rc.k != 0) cut = search<false>(each, 0, top, rc.count_off, (double)k, st, l);
+  if (st.r.p != 0.0) {
+    uint64_t sum = 0, first_k;
+    each([&](uint64_t p) {
+      if (p >= cut) sum += units(st.weight(value_at(p)));
+    });
+    block_before<kPick, uint64_t>(sum, l.wave_u, first_k);
+    cut = search<true>(each, cut, top, rc.mass_off, st.r.p * (double)(rc.z_off + first_k), st, l);
+  }
+  return cut;
+}
+
+// LIST: the tokens that may be kept, into l.list; their number (over kList: too many).  A group
+// is 32 tokens that one lane of k_sample_mass read; only groups whose maximum may be kept are
 // read again.  `low`: the least of the groups' maxima.
 template <typename T>
 __device__ __forceinline__ int candidates(const SampleArgs& a, int64_t row, const T* x,
                                           const RowState& st, float low, Lds& l) {
-  const int groups = a.segs * 64, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int groups = a.segs * 64, lane = threadIdx.x & 63;
   const float* gm = a.grp_max + row * groups;
-  const float none = -__builtin_huge_valf();
-  // 8192 groups at a time, thread t of wave w holding groups 1024 i + 64 w + lane (a segment's)
-  float g[8];
+  // 8192 groups at a time, in registers: thread t holds groups 256 i + t
+  constexpr int HELD = 32;
+  float g[HELD];
   auto load = [&](int base) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = base + i * 1024 + (int)threadIdx.x;
-      g[i] = at < groups ? gm[at] : none;
+    for (int i = 0; i < HELD; ++i) {
+      const int at = base + i * kPick + (int)threadIdx.x;
+      g[i] = at < groups ? gm[at] : kNone;
     }
   };
   load(0);
   Binning bin(st.max, 0.f, kBins);          // all that is above -inf into bin 0
   int last = kBins - 1;
-  if (threadIdx.x == 0) {
-    l.count = 0;
-    l.found = -1;
-  }
-  if (st.r.cls == LIST && a.V > kList) {
+  __syncthreads();
+  if (a.V > kList) {
     // bins over the range of the groups' maxima; the last one that the k largest reach into
     const Binning fine(st.max, st.max - low, kBins);
-    l.counts[threadIdx.x] = l.counts[threadIdx.x + 1024] = 0;
+#pragma unroll
+    for (int i = 0; i < kBins / kPick; ++i) l.counts[threadIdx.x + i * kPick] = 0;
+    if (threadIdx.x == 0) l.found = -1;
     __syncthreads();
 #pragma unroll 1
-    for (int base = 0; base < groups; base += 8192) {
+    for (int base = 0; base < groups; base += HELD * kPick) {
       if (base) load(base);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (g[i] > none) atomicAdd(&l.counts[fine(g[i])], 1u);
+      for (int i = 0; i < HELD; ++i)
+        if (g[i] > kNone) atomicAdd(&l.counts[fine(g[i])], 1u);
     }
     __syncthreads();
-    const int b = 2 * threadIdx.x;
-    const uint64_t c0 = l.counts[b], c1 = l.counts[b + 1], k = (uint64_t)st.r.k;
-    uint64_t total;
-    const uint64_t before = block_before<uint64_t>(c0 + c1, l.wave_u, total);
-    if (before < k && before + c0 >= k) l.found = b;
-    else if (before + c0 < k && before + c0 + c1 >= k) l.found = b + 1;
+    constexpr int PER = kBins / kPick;
+    uint64_t c[PER], own = 0, total;
+    const uint64_t k = (uint64_t)st.r.k;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      c[j] = l.counts[PER * threadIdx.x + j];
+      own += c[j];
+    }
+    uint64_t run = block_before<kPick, uint64_t>(own, l.wave_u, total);
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      if (run < k && run + c[j] >= k) l.found = PER * threadIdx.x + j;
+      run += c[j];
+    }
     __syncthreads();
     if (l.found >= 0) {                     // otherwise fewer groups than k: all of them
       last = l.found;
       bin = fine;
     }
-    if (groups > 8192) load(0);
-  } else {
-    __syncthreads();
+    if (groups > HELD * kPick) load(0);
   }
-  const bool by_weight = st.r.cls == MIN_P;
-  auto wanted = [&](float v) {
-    if (!(v > none)) return false;
-    return by_weight ? st.weight(v) >= st.r.min_p : bin(v) <= last;
+  if (threadIdx.x == 0) l.count = l.found_sum = 0;
+  __syncthreads();
+  // the wanted groups: each has a token for the list, so that over kList of them are too many
+  auto wanted = [&](float v) { return v > kNone && bin(v) <= last; };
+  int* n_groups = (int*)&l.found_sum;
+  // one slot for each set bit of every lane's mask: one LDS atomic a wave
+  auto slots = [&](unsigned mask, int* counter) {
+    int all, at = wave_before((int)__popc(mask), all), first = 0;
+    if (all == 0) return 0;
+    if (lane == 0) first = atomicAdd(counter, all);
+    return at + __builtin_amdgcn_readfirstlane(first);
   };
 #pragma unroll 1
-  for (int base = 0; base < groups; base += 8192) {
+  for (int base = 0; base < groups; base += HELD * kPick) {
     if (base) load(base);
-    // a bit for each of this lane's groups that is wanted
     unsigned want = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) want |= wanted(g[i]) ? 1u << i : 0u;
+    for (int i = 0; i < HELD; ++i) want |= wanted(g[i]) ? 1u << i : 0u;
+    int at = slots(want, n_groups);
+    for (; want; want &= want - 1, ++at)
+      if (at < kList) l.groups[at] = base + (__ffs(want) - 1) * kPick + (int)threadIdx.x;
+  }
+  __syncthreads();
+  const int wanted_groups = *n_groups;
+  if (wanted_groups > kList) return kList + 1;
+  // 32 threads to a group, 16 tokens of each thread at a time
+  constexpr int AT_ONCE = 16;
 #pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      // of a segment's 64 groups the wanted ones, two at a time, 32 lanes each
-      const int seg = (base + i * 1024) / 64 + wave;
-      uint64_t todo = __ballot((want >> i) & 1u);
-      while (todo) {
-        const int one = __ffsll((unsigned long long)todo) - 1;
-        todo &= todo - 1;
-        const int two = todo ? __ffsll((unsigned long long)todo) - 1 : -1;
-        todo &= todo - 1;
-        const int gl = lane < 32 ? one : two;
-        // tokens q * 512 + gl * 8 + j of the segment, q < 4 and j < 8
-        const int k = lane & 31, c = seg * kSeg + (k >> 3) * 512 + gl * 8 + (k & 7);
-        const bool in = gl >= 0 && c < a.V;
-        const float v = in ? (float)x[c] + 0.f : none;
-        const bool take = in && wanted(v);
-        const uint64_t who = __ballot(take);
-        int at = 0;
-        if (lane == 0) at = atomicAdd(&l.count, __popcll(who));
-        at = __builtin_amdgcn_readfirstlane(at) + __popcll(who & ((1ull << lane) - 1));
-        if (take && at < kList) l.list[at] = place(v, c);
+  for (int e0 = 0; e0 < wanted_groups * 32; e0 += kPick * AT_ONCE) {
+    T v[AT_ONCE];
+    int c[AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int e = e0 + i * kPick + (int)threadIdx.x, r = e & 31;
+      // tokens q * 512 + lane * 8 + j of the segment, q < 4 and j < 8
+      c[i] = a.V;
+      if (e < wanted_groups * 32) {
+        const int id = l.groups[e >> 5];
+        c[i] = (id >> 6) * kSeg + (r >> 3) * 512 + (id & 63) * 8 + (r & 7);
       }
+      v[i] = c[i] < a.V ? x[c[i]] : (T)kNone;
     }
+    unsigned take = 0;
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) take |= wanted((float)v[i] + 0.f) ? 1u << i : 0u;
+    int at = slots(take, &l.count);
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i)
+      if ((take >> i) & 1) {
+        if (at < kList) l.list[at] = place((float)v[i] + 0.f, c[i]);
+        ++at;
+      }
   }
   __syncthreads();
   return l.count;
 }
 
-// The place of the last kept token (0: all), from a row's sorted list of n places that follow
-// on `above` units of mass; `whole` the mass that top-p is a share of (0: that of the list's
-// first k).  Adds the kept tokens' masses to l.segs_u.
-__device__ __forceinline__ uint64_t cut_list(const RowState& st, int n, uint64_t above, uint64_t whole, Lds& l) {
-  sort_list(l.list, n);
-  uint64_t m[4], sum = 0, total;
-  double e[4];
-  const int first = 4 * threadIdx.x, k = st.r.k != 0 ? min(n, st.r.k) : n;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    e[j] = first + j < k ? st.weight(value_at(l.list[first + j])) : 0.0;
-    m[j] = first + j < k ? units(e[j]) : 0;
-    sum += m[j];
-  }
-  if (threadIdx.x == 0) l.found = k - 1;
-  uint64_t run = above + block_before<uint64_t>(sum, l.wave_u, total);
-  if (st.r.p != 0.0) {
-    const double mass = st.r.p * (double)(whole != 0 ? whole : total);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      // the token with which the mass reaches its share is the last kept one
-      if (m[j] && (double)run < mass && (double)(run + m[j]) >= mass) l.found = first + j;
-      run += m[j];
-    }
-  }
-  __syncthreads();
-  const int last = l.found;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (first + j <= last && m[j] && e[j] >= st.r.min_p)
-      atomicAdd((unsigned long long*)&l.segs_u[index_at(l.list[first + j]) / kSeg], (unsigned long long)m[j]);
-  const uint64_t cut = l.list[last];
-  __syncthreads();
-  return cut;
-}
-
-// Rows without filters, in a kernel of its own: one block of 256 threads per row, whose time is
-// that of its four dependent loads.
-template <typename T>
-__global__ void __launch_bounds__(256) k_sample_plain(SampleArgs a) {
-  __shared__ float tops[4];
-  __shared__ int bad[4];
-  __shared__ double mass[2][4];
-  __shared__ int found[2][2][4];
+// One block of 256 threads per row: what is kept (not for PLAIN), then where the running mass
+// first exceeds u times the kept mass, by segments and in the segment.  Its time is that of a
+// chain of loads and barriers, so it has few waves; a kernel of its own serves calls without
+// filters (4.7 us against 16).
+template <typename T, bool FILTERED>
+__global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
+  struct Small {
+    float range[3][kPick / 64];
+    double mass[2][kPick / 64];
+    int found[2][2][kPick / 64];
+  };
+  __shared__ Small sh;
   const int64_t row = blockIdx.x;
   const int V = a.V, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const T* x = (const T*)a.logits + row * a.stride;
   // thread t holds segments 2t and 2t + 1
-  float m[2];
+  float m[2], low = -kNone;
   double s[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int i = 2 * threadIdx.x + j;
-    m[j] = i < a.segs ? a.seg_max[row * a.segs + i] : -__builtin_huge_valf();
+    m[j] = i < a.segs ? a.seg_max[row * a.segs + i] : kNone;
     s[j] = i < a.segs ? a.seg_sum[row * a.segs + i] : 0.0;
+    if (FILTERED && i < a.segs) low = fminf(low, a.seg_min[row * a.segs + i]);
   }
   const double u = fmin(fmax((double)a.u[row], 0.0), 1.0);
   RowState st;
   st.r = row_params(a, row);
-  RowRange g;
-  g.bad = __any(m[0] != m[0] || m[1] != m[1]);
-  g.top = wave_top(fmaxf(m[0], m[1]));
-  if (lane == 0) {
-    tops[wave] = g.top;
-    bad[wave] = g.bad;
-  }
-  __syncthreads();
-  g.top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-  g.bad = bad[0] | bad[1] | bad[2] | bad[3];
+  const RowRange g = row_range<kPick>(fmaxf(m[0], m[1]), low, m[0] != m[0] || m[1] != m[1], sh.range);
   st.max = g.top;
   if (!drawable(g, st.r)) {
     if (threadIdx.x == 0) {
@@ -768,41 +885,107 @@ __global__ void __launch_bounds__(256) k_sample_plain(SampleArgs a) {
     }
     return;
   }
-  // where the running mass first exceeds u Z: the segment, then its token
-  double Z = 0.0, target = 0.0;
+  double e[8], Z = 0.0, target = 0.0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) e[j] = s[j] > 0.0 ? s[j] * st.weight(m[j]) : 0.0;
+  uint64_t cut = 0;
+  const bool filtered = FILTERED && st.r.cls != PLAIN;
+  if constexpr (FILTERED) {
+    __shared__ Lds l;
+    if (filtered) {
+      // the row's whole mass, for lp
+      if (st.r.cls == HIST)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int i = 2 * threadIdx.x + j;
+          e[j] = i < a.splits ? a.z_part[row * a.splits + i] : 0.0;
+        }
+      block_before<kPick, double>(e[0] + e[1], sh.mass[1], Z);
+      const bool sure = st.r.cls != LIST;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int i = 2 * threadIdx.x + j;
+        l.segs[i] = sure && i < a.segs ? a.seg_kept[row * a.segs + i] : 0;
+      }
+      if (st.r.cls != MIN_P) {
+        RowCut rc{0, 0, 0, 0, st.r.k, 0, 0, 0, 0};
+        int n;
+        if (st.r.cls == LIST) {
+          n = candidates<T>(a, row, x, st, g.low, l);
+        } else {
+          rc = a.cut[row];
+          n = a.listed[row];
+          if (n <= kList)
+            for (int i = threadIdx.x; i < n; i += kPick) l.list[i] = a.list[row * kList + i];
+          __syncthreads();
+        }
+        if (n <= kList) {
+          const auto listed = [&](auto f) {
+            for (int i = threadIdx.x; i < n; i += kPick) f(l.list[i]);
+          };
+          cut = last_kept(listed, n, rc, st, l);
+          listed([&](uint64_t p) {
+            const double w = st.weight(value_at(p));
+            if (p >= cut && w >= st.r.min_p)
+              atomicAdd((unsigned long long*)&l.segs[index_at(p) / kSeg], (unsigned long long)units(w));
+          });
+        } else {
+          const auto all = [&](auto f) {
+            for (int c = threadIdx.x * 8; c < V; c += kPick * 8) {
+              float v[8];
+              load8(x, c, V, v);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (v[j] > kNone) f(place(v[j], c + j));
+            }
+          };
+          cut = last_kept(all, INT32_MAX, RowCut{0, 0, 0, 0, st.r.k, 0, 0, 0, 0}, st, l);
+          __syncthreads();
+#pragma unroll
+          for (int j = 0; j < 2; ++j) l.segs[2 * threadIdx.x + j] = 0;
+          __syncthreads();
+          all([&](uint64_t p) {
+            const double w = st.weight(value_at(p));
+            if (p >= cut && w >= st.r.min_p)
+              atomicAdd((unsigned long long*)&l.segs[index_at(p) / kSeg], (unsigned long long)units(w));
+          });
+        }
+      }
+      __syncthreads();
+      // at most 2^11 weights of at most 2^42 units: exact as a double
+#pragma unroll
+      for (int j = 0; j < 2; ++j) e[j] = (double)l.segs[2 * threadIdx.x + j] * 0x1p-42;
+    }
+  }
   int seg = 0;
   float v[8];
-  double e[8];
 #pragma unroll
   for (int pass = 0; pass < 2; ++pass) {
     const int c = pass ? seg * kSeg + (int)threadIdx.x * 8 : 2 * (int)threadIdx.x;
-    double own = 0.0;
     if (pass) {
       load8(x, c, V, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        e[j] = v[j] > -__builtin_huge_valf() ? st.weight(v[j]) : 0.0;
-        own += e[j];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        e[j] = s[j] > 0.0 ? s[j] * st.weight(m[j]) : 0.0;
-        own += e[j];
+        e[j] = v[j] > kNone ? st.weight(v[j]) : 0.0;
+        if (filtered)
+          e[j] = v[j] > kNone && place(v[j], c + j) >= cut && e[j] >= st.r.min_p ? (double)units(e[j]) * 0x1p-42 : 0.0;
       }
     }
+    double own = 0.0;
+#pragma unroll
+    for (int j = 0; j < (pass ? 8 : 2); ++j) own += e[j];
     double wt, sum = 0.0;
     double run = wave_before(own, wt);
-    if (lane == 63) mass[pass][wave] = wt;
+    if (lane == 63) sh.mass[pass][wave] = wt;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i < wave) run += mass[pass][i];
-      sum += mass[pass][i];
+    for (int i = 0; i < kPick / 64; ++i) {
+      if (i < wave) run += sh.mass[pass][i];
+      sum += sh.mass[pass][i];
     }
     if (!pass) {
-      Z = sum;
-      target = u * Z;
+      target = u * sum;
+      if (!filtered) Z = sum;
     }
     const double first = run;
     int hit = INT32_MAX, last = -1;
@@ -816,15 +999,15 @@ __global__ void __launch_bounds__(256) k_sample_plain(SampleArgs a) {
     }
     first_and_last(hit, last);
     if (lane == 0) {
-      found[pass][0][wave] = hit;
-      found[pass][1][wave] = last;
+      sh.found[pass][0][wave] = hit;
+      sh.found[pass][1][wave] = last;
     }
     __syncthreads();
     // (the target is the mass itself if u = 1 or by a rounding: the last that has any)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      hit = min(i ? hit : INT32_MAX, found[pass][0][i]);
-      last = max(last, found[pass][1][i]);
+    for (int i = 0; i < kPick / 64; ++i) {
+      hit = min(i ? hit : INT32_MAX, sh.found[pass][0][i]);
+      last = max(last, sh.found[pass][1][i]);
     }
     if (hit == INT32_MAX) hit = last;
     if (pass) {
@@ -837,195 +1020,44 @@ __global__ void __launch_bounds__(256) k_sample_plain(SampleArgs a) {
     } else {
       seg = hit;
       // what lies before the segment comes off the target
-      if (hit / 2 == (int)threadIdx.x) mass[0][0] = hit & 1 ? first + e[0] : first;
+      if (hit / 2 == (int)threadIdx.x) sh.mass[0][0] = hit & 1 ? first + e[0] : first;
       __syncthreads();
-      target -= mass[0][0];
+      target -= sh.mass[0][0];
     }
   }
-}
-
-// Rows of any class: one block of 1024 threads per row.
-template <typename T>
-__global__ void __launch_bounds__(1024) k_sample_pick(SampleArgs a) {
-  __shared__ Lds l;
-  const int64_t row = blockIdx.x;
-  const int V = a.V, lane = threadIdx.x & 63, seg_of = threadIdx.x;
-  const T* x = (const T*)a.logits + row * a.stride;
-  RowState st;
-  st.r = row_params(a, row);
-  const RowRange range = row_range(a, row, l.range);
-  st.max = range.top;
-  if (!drawable(range, st.r)) {
-    if (threadIdx.x == 0) {
-      a.token[row] = -1;
-      a.lp[row] = __builtin_nanf("");
-    }
-    return;
-  }
-
-  // the row's whole mass, for lp; segment i belongs to thread i
-  const bool has = seg_of < a.segs;
-  double Z, s = 0.0;
-  if (st.r.cls != NUCLEUS) {
-    const double sum = has ? a.seg_sum[row * a.segs + seg_of] : 0.0;
-    if (sum > 0.0) s = sum * st.weight(a.seg_max[row * a.segs + seg_of]);
-  } else if (seg_of < a.splits) {
-    s = a.z_part[row * a.splits + seg_of];
-  }
-  double at = block_before<double>(s, l.wave_d, Z), sum = Z;
-  uint64_t cut = 0;
-  RowClass cls = st.r.cls;
-  if (cls != PLAIN) {
-    if (seg_of < kMaxSegs) l.segs_u[seg_of] = cls == NUCLEUS && has ? a.seg_kept[row * a.segs + seg_of] : 0;
-    if (cls == NUCLEUS) {
-      const int n = a.listed[row];
-      if (n <= kList) {
-        for (int i = threadIdx.x; i < n; i += 1024) l.list[i] = a.list[row * kList + i];
-        cut = cut_list(st, n, a.above[row], a.whole[row], l);
-      } else {
-        cls = GENERAL;
-      }
-    } else if (cls == LIST || cls == MIN_P) {
-      const int n = candidates<T>(a, row, x, st, range.low, l);
-      if (n <= kList) cut = cut_list(st, n, 0, 0, l);
-      else cls = GENERAL;
-    }
-    if (__builtin_expect(cls == GENERAL, 0)) {
-      if (st.r.k != 0) cut = find_cut<T, false>(x, V, st, 0, (uint64_t)st.r.k, 0.0, l);
-      if (st.r.p != 0.0) {
-        // the mass of what top-k keeps, exactly
-        uint64_t part = 0, zk;
-        for (int c = threadIdx.x * 8; c < V; c += 1024 * 8) {
-          float v[8];
-          load8(x, c, V, v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (c + j < V && place(v[j], c + j) >= cut) part += units(st.weight(v[j]));
-        }
-        block_before<uint64_t>(part, l.wave_u, zk);
-        const uint64_t c2 = find_cut<T, true>(x, V, st, cut, 0, st.r.p * (double)zk, l);
-        cut = c2 > cut ? c2 : cut;
-      }
-      // the kept mass of each segment, one wave a segment
-      for (int g = threadIdx.x >> 6; g < a.segs; g += 16) {
-        uint64_t part = 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = g * kSeg + q * 512 + lane * 8;
-          float v[8];
-          load8(x, c, V, v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (c + j >= V || place(v[j], c + j) < cut) continue;
-            const double e = st.weight(v[j]);
-            if (e >= st.r.min_p) part += units(e);
-          }
-        }
-        part = wave_total(part);
-        if (lane == 0) l.segs_u[g] = part;
-      }
-      __syncthreads();
-    }
-    // at most 2^11 weights of at most 2^42 units: exact as a double
-    s = has ? (double)l.segs_u[seg_of] * 0x1p-42 : 0.0;
-    at = block_before<double>(s, l.wave_d, sum);
-  }
-
-  const double target = fmin(fmax((double)a.u[row], 0.0), 1.0) * sum;
-  // the lowest segment whose running mass exceeds the target, else the last that has any
-  // (the target is the mass itself if u = 1 or by a rounding)
-  const int wave = threadIdx.x >> 6;
-  int hit = s > 0.0 && at + s > target ? seg_of : INT32_MAX, end = s > 0.0 ? seg_of : -1;
-  first_and_last(hit, end);
-  if (lane == 0) {
-    l.first[wave] = hit;
-    l.last[wave] = end;
-  }
-  __syncthreads();
-  hit = INT32_MAX;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    hit = min(hit, l.first[i]);
-    end = max(end, l.last[i]);
-  }
-  const int seg = hit != INT32_MAX ? hit : end;
-  if (seg_of == seg) l.wave_d[0] = at;
-  __syncthreads();
-  const double rest = target - l.wave_d[0];
-  // its tokens, two a thread
-  const int c = seg * kSeg + 2 * (int)threadIdx.x;
-  float v[2];
-  double e[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    v[j] = c + j < V ? (float)x[c + j] + 0.f : -__builtin_huge_valf();
-    e[j] = v[j] > -__builtin_huge_valf() ? st.weight(v[j]) : 0.0;
-    if (st.r.cls != PLAIN)
-      e[j] = c + j < V && place(v[j], c + j) >= cut && e[j] >= st.r.min_p ? (double)units(e[j]) * 0x1p-42 : 0.0;
-  }
-  double run = block_before<double>(e[0] + e[1], l.wave_d, sum);
-  hit = INT32_MAX, end = -1;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    run += e[j];
-    if (e[j] > 0.0) {
-      if (run > rest) hit = min(hit, c + j);
-      end = c + j;
-    }
-  }
-  first_and_last(hit, end);
-  if (lane == 0) {
-    l.first[wave] = hit;
-    l.last[wave] = end;
-  }
-  __syncthreads();
-  hit = INT32_MAX;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    hit = min(hit, l.first[i]);
-    end = max(end, l.last[i]);
-  }
-  if (hit == INT32_MAX) hit = end;
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-    if (c + j == hit) {
-      a.token[row] = hit;
-      a.lp[row] = (float)(((double)v[j] - (double)st.max) / st.r.T - log(Z));
-    }
 }
 
 struct SamplePlan {
   int64_t rows;          // per launch
   int segs, splits;
-  size_t o_max, o_min, o_sum, o_grp, o_hist, o_z, o_above, o_whole, o_kept, o_listed, o_list, total;
+  size_t o_max, o_min, o_sum, o_grp, o_kept, o_listed, o_hist, o_hist_n, o_z, o_cut, o_list, total;
 };
 // Rows go in batches, so that the workspace stays bounded; a row of at most kList tokens needs
-// no histogram.  Splits: up to four blocks of 1024 threads per CU (rows of other classes leave theirs
-// at once), each with at least 4 segments.
+// no histogram.  Splits: about three blocks of 512 threads per CU, each with at least 4 segments.
 SamplePlan plan_sample(int64_t B, int64_t V) {
   SamplePlan p{};
-  const bool nucleus = V > kList;
-  p.rows = std::min<int64_t>(B, nucleus ? 1024 : 65536);
+  const bool hist = V > kList;
+  p.rows = std::min<int64_t>(B, hist ? 1024 : 65536);
   p.segs = (int)((V + kSeg - 1) / kSeg);
-  p.splits = nucleus ? (int)std::max<int64_t>(1, std::min<int64_t>((p.segs + 3) / 4, 1024 / p.rows)) : 0;
+  p.splits = hist ? (int)std::max<int64_t>(1, std::min<int64_t>((p.segs + 3) / 4, 3 * kCUs / p.rows)) : 0;
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
     off = align_up(off + bytes);
     return o;
   };
-  const size_t n = (size_t)(p.rows * p.segs), h = (size_t)(p.rows * p.splits);
+  const size_t rows = (size_t)p.rows, n = rows * (size_t)p.segs, h = rows * (size_t)p.splits;
   p.o_max = take(n * 4);
   p.o_min = take(n * 4);
   p.o_sum = take(n * 8);
   p.o_grp = take(n * 256);
-  p.o_hist = take(h * kNucleusBins * 8);
+  p.o_kept = take(n * 8);
+  p.o_listed = take(rows * 4);
+  p.o_hist = take(h * kHistBins * 8);
+  p.o_hist_n = take(h * kHistBins * 4);
   p.o_z = take(h * 8);
-  p.o_above = take((size_t)p.rows * 8);
-  p.o_whole = take((size_t)p.rows * 8);
-  p.o_kept = take(nucleus ? n * 8 : 0);
-  p.o_listed = take((size_t)p.rows * 4);
-  p.o_list = take(nucleus ? (size_t)p.rows * kList * 8 : 0);
+  p.o_cut = take(hist ? rows * sizeof(RowCut) : 0);
+  p.o_list = take(hist ? rows * kList * 8 : 0);
   p.total = off;
   return p;
 }
@@ -1052,21 +1084,24 @@ hipError_t launch_sample(const SampleArgs& a, int64_t rows, hipStream_t s) {
     k_sample_mass<T><<<(unsigned)blocks, 256, 0, s>>>(a, waves);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  // the two passes of NUCLEUS, where a row may be of that class
-  if (a.V > kList && (a.p_rows != nullptr || (a.p > 0.0 && a.p < 1.0)) &&
-      (a.k_rows != nullptr || a.k == 0 || a.k >= a.V)) {
+  const bool k_on = a.k_rows != nullptr || (a.k > 0 && a.k < a.V);
+  const bool p_on = a.p_rows != nullptr || (a.p > 0.0 && a.p < 1.0);
+  const bool m_on = a.min_p_rows != nullptr || a.min_p > 0.0;
+  const bool all_short = a.k_rows == nullptr && k_on && a.k <= kListK;   // LIST, whatever p
+  if (a.V > kList && (k_on || p_on || m_on) && !all_short) {
     ScopedKernelTimer t(KK_SAMPLE_CUT, s);
-    const dim3 grid((unsigned)a.splits, (unsigned)rows);
-    k_sample_hist<T><<<grid, 1024, 0, s>>>(a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    k_sample_gather<T><<<grid, 1024, 0, s>>>(a);
+    if (k_on || p_on) {
+      k_sample_hist<T><<<dim3((unsigned)a.splits, (unsigned)rows), kHistThreads, 0, s>>>(a);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      k_sample_cut<<<(unsigned)rows, kHistThreads, 0, s>>>(a);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    k_sample_gather<T><<<dim3((unsigned)((a.segs + 3) / 4), (unsigned)rows), 256, 0, s>>>(a);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   ScopedKernelTimer t(KK_SAMPLE_PICK, s);
-  const bool plain = a.k_rows == nullptr && a.p_rows == nullptr && a.min_p_rows == nullptr &&
-                     (a.k == 0 || a.k >= a.V) && !(a.p > 0.0 && a.p < 1.0) && !(a.min_p > 0.0);
-  if (plain) k_sample_plain<T><<<(unsigned)rows, 256, 0, s>>>(a);
-  else k_sample_pick<T><<<(unsigned)rows, 1024, 0, s>>>(a);
+  if (k_on || p_on || m_on) k_sample_pick<T, true><<<(unsigned)rows, kPick, 0, s>>>(a);
+  else k_sample_pick<T, false><<<(unsigned)rows, kPick, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -1129,12 +1164,12 @@ int grpo_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row
     a.seg_min = (float*)(ws + p.o_min);
     a.seg_sum = (double*)(ws + p.o_sum);
     a.grp_max = (float*)(ws + p.o_grp);
-    a.hist = (uint64_t*)(ws + p.o_hist);
-    a.z_part = (double*)(ws + p.o_z);
-    a.above = (uint64_t*)(ws + p.o_above);
-    a.whole = (uint64_t*)(ws + p.o_whole);
     a.seg_kept = (uint64_t*)(ws + p.o_kept);
     a.listed = (int*)(ws + p.o_listed);
+    a.hist = (uint64_t*)(ws + p.o_hist);
+    a.hist_n = (uint32_t*)(ws + p.o_hist_n);
+    a.z_part = (double*)(ws + p.o_z);
+    a.cut = (grpo::RowCut*)(ws + p.o_cut);
     a.list = (uint64_t*)(ws + p.o_list);
     a.token = token + b;
     a.lp = lp + b;
