@@ -18,7 +18,7 @@
 //           are at or above the k-th largest of them, so every kept token is, and only the
 //           groups whose maximum is are read again.  The cuts are found among those candidates.
 //   MIN_P   min-p alone: one more pass over the segments whose maximum reaches min_p.
-//   HIST    top-p, alone or with a larger k: histograms of mass and count over 4096 bins of x
+//   HIST    top-p, alone or with a larger k: histograms of mass and count over 2048 or 4096 bins of x
 //           tell which bins the cuts fall into; one more pass sums what lies above them and
 //           lists the tokens of those bins, among which the cuts are found.
 // Lists hold up to 4096 tokens; where one overflows (equal logits), the cuts are found among
@@ -38,12 +38,16 @@ constexpr int kCUs = 256;
 constexpr int kSeg = 2048;                 // tokens per segment: one wave, 32 a lane
 constexpr int64_t kMaxVocab = 1 << 20;     // 2^20 weights of at most 2^42
 constexpr int kMaxSegs = (int)(kMaxVocab / kSeg);
-constexpr int kHistBins = 4096;
 constexpr int kHistThreads = 512;
+// Bins of HIST: 2048 keep the passes over them short; a flat row of 2^18 tokens then has some 2000
+// in its fullest bin.  4096 for longer rows.
+constexpr int64_t kFewBins = 1 << 18;
+constexpr int hist_bins_for(int64_t V) { return V <= kFewBins ? 2048 : 4096; }
 constexpr int kBins = 2048;                // of the groups' maxima, and of one pass of a search
 constexpr int kList = 4096;                // listed tokens of a row
 constexpr int kListK = 2048;               // largest top-k that goes by the groups' maxima
 constexpr int kPick = 256;                 // threads of a row's last step
+constexpr int kLine = 32;                  // integers of a 128-byte line
 constexpr float kNone = -__builtin_huge_valf();
 
 // What HIST's gather and pick need to know: tokens in bins below `sure` are kept (but for
@@ -71,10 +75,10 @@ struct SampleArgs {
   double* seg_sum;     // [B, segs], relative to the segment's own maximum (not for HIST)
   float* grp_max;      // [B, segs, 64]: a lane's 32 tokens (LIST)
   uint64_t* seg_kept;  // [B, segs]: mass that is surely kept (HIST, MIN_P)
-  int* listed;         // [B]: tokens in the list
+  int* listed;         // [B, kLine]: tokens in the list, each row's number in a cache line of its own
   // HIST
-  uint64_t* hist;      // [B, splits, kHistBins]: masses
-  uint32_t* hist_n;    // [B, splits, kHistBins]: counts
+  uint64_t* hist;      // [B, splits, bins]: masses
+  uint32_t* hist_n;    // [B, splits, bins]: counts
   double* z_part;      // [B, splits]
   RowCut* cut;         // [B]
   uint64_t* list;      // [B, kList]: places
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(256, 4) k_sample_mass(SampleArgs a, int64_t wa
       a.seg_max[w] = bad ? __builtin_nanf("") : m;
       a.seg_min[w] = low;
       a.seg_sum[w] = s;
-      if (w % a.segs == 0) a.listed[w / a.segs] = 0;
+      if (w % a.segs == 0) a.listed[w / a.segs * kLine] = 0;
     }
     if (!more) return;
     w += step;
@@ -369,22 +373,22 @@ __device__ __forceinline__ bool drawable(const RowRange& g, const RowParams& r) 
 }
 // Over 30 T below the maximum, 2^20 tokens weigh less than 10^-6 of it.  With a k, the bins go
 // down to the minimum: tokens without weight count too.
-__device__ __forceinline__ Binning hist_bins(const RowRange& g, const RowParams& r) {
+__device__ __forceinline__ Binning hist_bins(const RowRange& g, const RowParams& r, int bins) {
   const float all = g.top - g.low;
-  return Binning(g.top, r.k != 0 ? all : fminf(all, (float)(30.0 * r.T)), kHistBins);
+  return Binning(g.top, r.k != 0 ? all : fminf(all, (float)(30.0 * r.T)), bins);
 }
 
 // ---------------------------------------------------------------- HIST
 // Block (split, row): the mass and number of the split's tokens by bin.
-template <typename T>
+template <typename T, int BINS>
 __global__ void __launch_bounds__(kHistThreads) k_sample_hist(SampleArgs a) {
   constexpr int NT = kHistThreads;
   const int64_t row = blockIdx.y;
   RowState st;
   st.r = row_params(a, row);
   if (st.r.cls != HIST) return;
-  __shared__ uint64_t mass[kHistBins];
-  __shared__ uint32_t number[kHistBins];
+  __shared__ uint64_t mass[BINS];
+  __shared__ uint32_t number[BINS];
   __shared__ float range[3][NT / 64];
   __shared__ double zs[NT / 64];
   const int per = (a.segs + a.splits - 1) / a.splits * kSeg;
@@ -392,11 +396,11 @@ __global__ void __launch_bounds__(kHistThreads) k_sample_hist(SampleArgs a) {
   const T* x = (const T*)a.logits + row * a.stride;
   Raw8<T> next = {};
   if (from + (int)threadIdx.x * 8 < to) next = load8(x, from + threadIdx.x * 8, a.V);
-  for (int i = threadIdx.x; i < kHistBins; i += NT) mass[i] = number[i] = 0;
+  for (int i = threadIdx.x; i < BINS; i += NT) mass[i] = number[i] = 0;
   const RowRange g = row_range<NT>(a, row, range);      // its barrier is also the bins'
   if (!drawable(g, st.r)) return;
   st.max = g.top;
-  const Binning bin = hist_bins(g, st.r);
+  const Binning bin = hist_bins(g, st.r, BINS);
   const bool counted = st.r.k != 0;
   double z = 0.0;
   for (int c = from + threadIdx.x * 8; c < to; c += NT * 8) {
@@ -415,8 +419,8 @@ __global__ void __launch_bounds__(kHistThreads) k_sample_hist(SampleArgs a) {
   }
   double total;
   block_before<NT, double>(z, zs, total);
-  const int64_t at = (row * a.splits + blockIdx.x) * kHistBins;
-  for (int i = threadIdx.x; i < kHistBins; i += NT) {
+  const int64_t at = (row * a.splits + blockIdx.x) * BINS;
+  for (int i = threadIdx.x; i < BINS; i += NT) {
     a.hist[at + i] = mass[i];
     if (counted) a.hist_n[at + i] = number[i];
   }
@@ -434,8 +438,9 @@ __global__ void __launch_bounds__(kHistThreads) k_sample_hist(SampleArgs a) {
 //   mass + mass_off    is the mass before among all for those of lo .. hi, and at least the
 //                      share for those of kbin behind them;
 //   z_off + the mass of the listed ones up to rank k is that of the first k of all.
+template <int BINS>
 __global__ void __launch_bounds__(kHistThreads) k_sample_cut(SampleArgs a) {
-  constexpr int NT = kHistThreads, PER = kHistBins / NT;
+  constexpr int NT = kHistThreads, PER = BINS / NT;
   const int64_t row = blockIdx.x;
   RowState st;
   st.r = row_params(a, row);
@@ -451,14 +456,32 @@ __global__ void __launch_bounds__(kHistThreads) k_sample_cut(SampleArgs a) {
   uint32_t n[PER], own_n = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) h[j] = n[j] = 0;
-#pragma unroll 4
-  for (int s = 0; s < a.splits; ++s) {
-    const int64_t from_s = (row * a.splits + s) * kHistBins + PER * threadIdx.x;
+  // 8 splits' loads at a time
+  for (int s0 = 0; s0 < a.splits; s0 += 8) {
+    typedef __attribute__((ext_vector_type(2))) uint64_t U2;
+    typedef __attribute__((ext_vector_type(4))) uint32_t U4;
+    U2 in[8][PER / 2];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) h[j] += a.hist[from_s + j];
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < PER / 2; ++j)
+        in[i][j] = s0 + i < a.splits
+                       ? ((const U2*)(a.hist + (row * a.splits + s0 + i) * BINS))[PER / 2 * threadIdx.x + j]
+                       : U2{0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < PER; ++j) h[j] += in[i][j / 2][j % 2];
     if (counted) {
 #pragma unroll
-      for (int j = 0; j < PER; ++j) n[j] += a.hist_n[from_s + j];
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < PER / 4; ++j)
+          if (s0 + i < a.splits) {
+            const U4 in_n = ((const U4*)(a.hist_n + (row * a.splits + s0 + i) * BINS))[PER / 4 * threadIdx.x + j];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) n[4 * j + q] += in_n[q];
+          }
     }
   }
 #pragma unroll
@@ -533,25 +556,28 @@ __global__ void __launch_bounds__(256) k_sample_gather(SampleArgs a) {
   st.r = row_params(a, row);
   if (st.r.cls != HIST && st.r.cls != MIN_P) return;
   __shared__ float range[3][4];
-  const int seg = min(a.segs - 1, (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6)), lane = threadIdx.x & 63;
+  __shared__ int counts[4], first;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int seg = min(a.segs - 1, (int)blockIdx.x * 4 + wave);
   const float top = a.seg_max[row * a.segs + seg];
   RowCut rc{INT32_MAX, 1, 0, -1, 0, 0, 0, 0, 0};
   if (st.r.cls == HIST) rc = a.cut[row];
   const RawSeg<T> raw = load_seg<T>(a, row, seg);       // on its way while the row's range is found
   const RowRange g = row_range<256>(a, row, range);
-  if (!drawable(g, st.r) || blockIdx.x * 4 + (threadIdx.x >> 6) >= (unsigned)a.segs) return;
+  if (!drawable(g, st.r)) return;
   st.max = g.top;
-  Binning bin(g.top, 0.f, kHistBins);
+  const int bins = hist_bins_for(a.V);
+  Binning bin(g.top, 0.f, bins);
   bool read = st.weight(top) >= st.r.min_p;
   if (st.r.cls == HIST) {
-    bin = hist_bins(g, st.r);
+    bin = hist_bins(g, st.r, bins);
     const int b = bin(top);
     read = b < rc.sure || b <= rc.hi || b <= rc.kbin;
   }
+  const bool own = (int)blockIdx.x * 4 + wave < a.segs;
   uint64_t part = 0;
-  if (read) {
-    const int c0 = seg * kSeg + lane * 8;
-    unsigned unsure = 0;
+  unsigned unsure = 0;
+  if (read && own) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       float v[8];
@@ -567,25 +593,36 @@ __global__ void __launch_bounds__(256) k_sample_gather(SampleArgs a) {
       }
     }
     part = wave_total(part);
-    if (__any(unsure != 0)) {
-      int all, slot = wave_before((int)__popc(unsure), all), first = 0;
-      if (lane == 0) first = atomicAdd(&a.listed[row], all);
-      slot += __builtin_amdgcn_readfirstlane(first);
-      // more than kList in all: the pick sees the number and goes by the row
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float v[8];
-        unpack(raw.q[q], v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if ((unsure >> (q * 8 + j)) & 1) {
-            if (slot < kList) a.list[row * kList + slot] = place(v[j], c0 + q * 512 + j);
-            ++slot;
-          }
-      }
-    }
   }
-  if (lane == 0) a.seg_kept[row * a.segs + seg] = part;
+  if (lane == 0 && own) a.seg_kept[row * a.segs + seg] = part;
+  if (st.r.cls != HIST) return;
+  // one addition to the row's number for the block
+  int all, slot = wave_before((int)__popc(unsure), all);
+  if (lane == 0) counts[wave] = all;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int sum = counts[0] + counts[1] + counts[2] + counts[3];
+    first = sum ? atomicAdd(&a.listed[row * kLine], sum) : 0;
+  }
+  __syncthreads();
+  if (all == 0) return;
+  slot += first;
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (i < wave) slot += counts[i];
+  // more than kList in all: the pick sees the number and goes by the row
+  const int c0 = seg * kSeg + lane * 8;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float v[8];
+    unpack(raw.q[q], v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if ((unsure >> (q * 8 + j)) & 1) {
+        if (slot < kList) a.list[row * kList + slot] = place(v[j], c0 + q * 512 + j);
+        ++slot;
+      }
+  }
 }
 
 // ---------------------------------------------------------------- the pick
@@ -665,8 +702,11 @@ __device__ __forceinline__ uint64_t search(const Each& each, uint64_t lo, uint64
     if (t < n) l.bins[kPick + t] = mine;
     __syncthreads();
     uint64_t before = base;
-    for (int i = 0; i < n; ++i)
-      if (l.bins[i] > p) before += l.bins[kPick + i];
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const uint64_t other = l.bins[i], amount = l.bins[kPick + i];
+      before += other > p ? amount : 0;
+    }
     if (mine && !reached(before) && reached(before + mine)) l.result = p;
     __syncthreads();
     return l.result;
@@ -686,12 +726,12 @@ __device__ __forceinline__ uint64_t last_kept(const Each& each, int n, const Row
     if (t == 0) l.result = ~(uint64_t)0;
     __syncthreads();
     uint64_t rank = rc.count_off, before = rc.mass_off, first_k;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i)
-      if (l.list[i] > p) {
-        ++rank;
-        before += l.bins[i];
-      }
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const uint64_t other = l.list[i], amount = l.bins[i];
+      rank += other > p ? 1 : 0;
+      before += other > p ? amount : 0;
+    }
     bool keep = t < n && rank < k;
     if (st.r.p != 0.0) {
       block_before<kPick, uint64_t>(keep ? mine : 0, l.wave_u, first_k);
@@ -709,19 +749,31 @@ __device__ __forceinline__ uint64_t last_kept(const Each& each, int n, const Row
     return l.result;
   }
   // the range of the places
-  uint64_t top = 0, cut = 0;
-  each([&](uint64_t p) { top = p > top ? p : top; });
-  if (t == 0) l.result = 0;
+  uint64_t top = 0, low = ~(uint64_t)0;
+  each([&](uint64_t p) {
+    top = p > top ? p : top;
+    low = p < low ? p : low;
+  });
+  if (t == 0) {
+    l.result = 0;
+    l.found_sum = ~(uint64_t)0;
+  }
   __syncthreads();
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {
-    const uint64_t other = __shfl_xor((unsigned long long)top, o, 64);
-    top = other > top ? other : top;
+    const uint64_t high = __shfl_xor((unsigned long long)top, o, 64), deep = __shfl_xor((unsigned long long)low, o, 64);
+    top = high > top ? high : top;
+    low = deep < low ? deep : low;
   }
-  if ((t & 63) == 0) atomicMax((unsigned long long*)&l.result, (unsigned long long)top);
+  if ((t & 63) == 0) {
+    atomicMax((unsigned long long*)&l.result, (unsigned long long)top);
+    atomicMin((unsigned long long*)&l.found_sum, (unsigned long long)low);
+  }
   __syncthreads();
   top = l.result;
-  if (rc.k != 0) cut = search<false>(each, 0, top, rc.count_off, (double)k, st, l);
+  low = l.found_sum;
+  uint64_t cut = low;
+  if (rc.k != 0) cut = search<false>(each, low, top, rc.count_off, (double)k, st, l);
   if (st.r.p != 0.0) {
     uint64_t sum = 0, first_k;
     each([&](uint64_t p) {
@@ -816,8 +868,8 @@ __device__ __forceinline__ int candidates(const SampleArgs& a, int64_t row, cons
   __syncthreads();
   const int wanted_groups = *n_groups;
   if (wanted_groups > kList) return kList + 1;
-  // 32 threads to a group, 16 tokens of each thread at a time
-  constexpr int AT_ONCE = 16;
+  // 32 threads to a group, 32 tokens of each thread at a time
+  constexpr int AT_ONCE = 32;
 #pragma unroll 1
   for (int e0 = 0; e0 < wanted_groups * 32; e0 += kPick * AT_ONCE) {
     T v[AT_ONCE];
@@ -914,7 +966,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
           n = candidates<T>(a, row, x, st, g.low, l);
         } else {
           rc = a.cut[row];
-          n = a.listed[row];
+          n = a.listed[row * kLine];
           if (n <= kList)
             for (int i = threadIdx.x; i < n; i += kPick) l.list[i] = a.list[row * kList + i];
           __syncthreads();
@@ -1052,9 +1104,9 @@ SamplePlan plan_sample(int64_t B, int64_t V) {
   p.o_sum = take(n * 8);
   p.o_grp = take(n * 256);
   p.o_kept = take(n * 8);
-  p.o_listed = take(rows * 4);
-  p.o_hist = take(h * kHistBins * 8);
-  p.o_hist_n = take(h * kHistBins * 4);
+  p.o_listed = take(rows * kLine * 4);
+  p.o_hist = take(h * hist_bins_for(V) * 8);
+  p.o_hist_n = take(h * hist_bins_for(V) * 4);
   p.o_z = take(h * 8);
   p.o_cut = take(hist ? rows * sizeof(RowCut) : 0);
   p.o_list = take(hist ? rows * kList * 8 : 0);
@@ -1091,9 +1143,13 @@ hipError_t launch_sample(const SampleArgs& a, int64_t rows, hipStream_t s) {
   if (a.V > kList && (k_on || p_on || m_on) && !all_short) {
     ScopedKernelTimer t(KK_SAMPLE_CUT, s);
     if (k_on || p_on) {
-      k_sample_hist<T><<<dim3((unsigned)a.splits, (unsigned)rows), kHistThreads, 0, s>>>(a);
+      const dim3 grid((unsigned)a.splits, (unsigned)rows);
+      const bool few = a.V <= kFewBins;
+      if (few) k_sample_hist<T, 2048><<<grid, kHistThreads, 0, s>>>(a);
+      else k_sample_hist<T, 4096><<<grid, kHistThreads, 0, s>>>(a);
       if ((e = hipGetLastError()) != hipSuccess) return e;
-      k_sample_cut<<<(unsigned)rows, kHistThreads, 0, s>>>(a);
+      if (few) k_sample_cut<2048><<<(unsigned)rows, kHistThreads, 0, s>>>(a);
+      else k_sample_cut<4096><<<(unsigned)rows, kHistThreads, 0, s>>>(a);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     k_sample_gather<T><<<dim3((unsigned)((a.segs + 3) / 4), (unsigned)rows), 256, 0, s>>>(a);
