@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -17,21 +18,30 @@ from ._lib import (AdamWOpts, AdamWTensor, SampleOpts, _arg, _check, _dev, _dt, 
 NORM_LAYER, NORM_RMS = 0, 1
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(*ts, strided=()):
     """The tensors' one GPU made current, and its current stream: (context, stream).
     All of them are contiguous, except those of `strided`."""
-    _dev(*ts)
+    at = ts[0].get_device()
+    for t in ts:
+        if at < 0 or t.get_device() != at or not t.is_contiguous():
+            _refuse(ts + strided, ts)
     for t in strided:
+        if t.get_device() != at:
+            _refuse(ts + strided, ts)
+    ctx = _HERE if at == torch.cuda.current_device() else torch.cuda.device(at)
+    return ctx, torch._C._cuda_getCurrentRawStream(at)
+
+
+def _refuse(ts, contiguous):
+    for t in ts:
         if not t.is_cuda:
             raise ValueError("all tensors must be on the GPU")
-    ts += strided
-    dev = ts[0].device
-    for t in ts:
-        if t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one call runs on one GPU")
-    ctx = contextlib.nullcontext() if dev.index == torch.cuda.current_device() else \
-        torch.cuda.device(dev)
-    return ctx, torch.cuda.current_stream(dev).cuda_stream
+    _dev(*contiguous)
+    raise ValueError("tensors on %s: one call runs on one GPU"
+                     % " and ".join(sorted({str(t.device) for t in ts})))
 
 
 def _workspace(need, device, workspace):
@@ -65,6 +75,14 @@ def grpo_norm_fwd(X, weight, bias=None, eps: float = 1e-5, kind: int = NORM_RMS,
     return Y, mean, rstd
 
 
+@functools.lru_cache(maxsize=256)
+def _norm_bytes(rows, cols, dt):
+    need = int(lib().grpo_norm_workspace_bytes(rows, cols, dt))
+    if need == 0:
+        _check("grpo_norm_workspace_bytes", -1)
+    return need
+
+
 def grpo_norm_bwd(dY, X, weight, mean, rstd, kind: int = NORM_RMS, bias: bool = False, dX=None,
                   dweight=None, dbias=None, workspace=None):
     """(dX, dweight, dbias): dX in X's type; dweight and dbias [cols] float32,
@@ -88,9 +106,7 @@ def grpo_norm_bwd(dY, X, weight, mean, rstd, kind: int = NORM_RMS, bias: bool = 
         _arg(dbias, "dbias", dtype=torch.float32, numel=cols)
     elif bias:
         dbias = torch.zeros(cols, dtype=torch.float32, device=dev)
-    need = int(lib().grpo_norm_workspace_bytes(rows, cols, dt))
-    if need == 0:
-        _check("grpo_norm_workspace_bytes", -1)
+    need = _norm_bytes(rows, cols, dt)
     if workspace is not None:
         workspace = _workspace(need, dev, workspace)
     ctx, stream = _on(*(t for t in (dY, X, weight, mean, rstd, dX, dweight, dbias, workspace)
@@ -157,7 +173,7 @@ class AdamWPlan:
         self.tensors, self.image, self.table = tensors, image, table
         self.versioned = [p for p in params if not p.is_inference()]
         self.device = table.device
-        self.stream = torch.cuda.current_stream(self.device).cuda_stream
+        self.stream = torch._C._cuda_getCurrentRawStream(table.get_device())
 
 
 def adamw_plan(params, grads, exp_avg, exp_avg_sq, master=None) -> AdamWPlan:
@@ -236,6 +252,14 @@ def grpo_adamw(plan: AdamWPlan, step, lr=1e-6, betas=(0.9, 0.999), eps: float = 
 
 
 # ---------------------------------------------------------------- sampling
+@functools.lru_cache(maxsize=256)
+def _sample_bytes(B, V):
+    need = int(lib().grpo_sample_workspace_bytes(B, V))
+    if need == 0:
+        _check("grpo_sample_workspace_bytes", -3)
+    return need
+
+
 def grpo_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None,
                 workspace=None):
     """(token, lp): one token (int32 [B]) for each row of logits [B, V] (float32 or
@@ -252,23 +276,24 @@ def grpo_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=N
         raise ValueError("the logits of a row must be adjacent and rows must not overlap")
     stride = max(V, logits.stride(0))
     _arg(u, "u", dtype=torch.float32, numel=B)
-    opts, rows = SampleOpts(), []
-    for name, x, dtype in (("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
-                           ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+    # numbers, and device arrays in their places
+    numbers, arrays, rows = [], [], []
+    for name, x in (("temperature", temperature), ("top_p", top_p), ("min_p", min_p), ("top_k", top_k)):
         if isinstance(x, torch.Tensor):
-            rows.append(_arg(x, name, dtype=dtype, numel=B))
-            setattr(opts, name + "_rows", x.data_ptr())
+            rows.append(_arg(x, name, dtype=torch.int32 if name == "top_k" else torch.float32, numel=B))
+            numbers.append(0)
+            arrays.append(x.data_ptr())
         else:
-            setattr(opts, name, x)
+            numbers.append(x)
+            arrays.append(None)
+    opts = SampleOpts(*numbers, 0, *arrays)
     token, lp = (None, None) if out is None else out
     dev = logits.device
     token = torch.empty(B, dtype=torch.int32, device=dev) if token is None else \
         _arg(token, "token", dtype=torch.int32, numel=B)
     lp = torch.empty(B, dtype=torch.float32, device=dev) if lp is None else \
         _arg(lp, "lp", dtype=torch.float32, numel=B)
-    need = int(lib().grpo_sample_workspace_bytes(B, V))
-    if need == 0:
-        _check("grpo_sample_workspace_bytes", -3)
+    need = _sample_bytes(B, V)
     if workspace is not None:
         rows.append(_workspace(need, dev, workspace))
     ctx, stream = _on(u, token, lp, *rows, strided=(logits,))
