@@ -66,21 +66,22 @@ template <> struct Vec4<uint8_t> {
   typedef __attribute__((ext_vector_type(4), aligned(1))) uint8_t type;
 };
 
-// Elements [e, e + 4) of n; those at n and behind it read as zero and are not written.
-template <typename T>
-__device__ __forceinline__ typename Vec4<T>::type load4(const T* p, int64_t e, int64_t n) {
+// Elements [e, e + 4) of n; those at n and behind it read as zero and are not written.  FULL:
+// there are none.
+template <bool FULL, typename T>
+__device__ __forceinline__ typename Vec4<T>::type load4(const T* p, int e, int n) {
   typedef typename Vec4<T>::type V;
-  if (e + 4 <= n) return *(const V*)(p + e);
+  if (FULL || e + 4 <= n) return *(const V*)(p + e);
   V v = {};
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (e + j < n) v[j] = p[e + j];
   return v;
 }
-template <typename T>
-__device__ __forceinline__ void store4(T* p, int64_t e, int64_t n, typename Vec4<T>::type v) {
+template <bool FULL, typename T>
+__device__ __forceinline__ void store4(T* p, int e, int n, typename Vec4<T>::type v) {
   typedef typename Vec4<T>::type V;
-  if (e + 4 <= n) {
+  if (FULL || e + 4 <= n) {
     *(V*)(p + e) = v;
     return;
   }
@@ -89,10 +90,17 @@ __device__ __forceinline__ void store4(T* p, int64_t e, int64_t n, typename Vec4
     if (e + j < n) p[e + j] = v[j];
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
+// The wave's largest value, by row shifts and row broadcasts (no LDS).
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define GRPO_STEP(ctrl, rows) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xf, false))
+  GRPO_STEP(0x111, 0xf);   // row_shr:1
+  GRPO_STEP(0x112, 0xf);
+  GRPO_STEP(0x114, 0xf);
+  GRPO_STEP(0x118, 0xf);
+  GRPO_STEP(0x142, 0xa);   // row_bcast:15
+  GRPO_STEP(0x143, 0xc);   // row_bcast:31
+#undef GRPO_STEP
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 // The last tensor whose first chunk is <= chunk: a 64-way search, one load per level.
@@ -111,41 +119,56 @@ __device__ __forceinline__ int owner_of(const int64_t* __restrict__ first, int c
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// The codes of a value q = (|m| / a) 127^2 or (v / a) 255^4, exactly: a candidate from float32
-// roots, moved to the side of the borders (c -+ 1/2)^k that the float64 q is on.  A float32
-// root alone would put one value in about 10^5 on the wrong side.
-__device__ __forceinline__ int code_m(double q) {
-  const float c = rintf(sqrtf((float)q));
+// The codes of a value q = (|m| / a) 127^2 or (v / a) 255^4, exactly: the candidate c from float32
+// roots, moved to the side of the borders (c -+ 1/2)^k that the float64 q is on.
+__device__ __forceinline__ float exact_m(float c, double q) {
   const double up = (double)c + 0.5, dn = (double)c - 0.5;
-  int k = (int)c + (q >= up * up ? 1 : 0) - (c > 0.f && q < dn * dn ? 1 : 0);
-  return min(k, 127);
+  return fminf(c + (q >= up * up ? 1.f : 0.f) - (c > 0.f && q < dn * dn ? 1.f : 0.f), 127.f);
 }
-__device__ __forceinline__ int code_v(double q) {
-  const float c = rintf(sqrtf(sqrtf((float)q)));
+__device__ __forceinline__ float exact_v(float c, double q) {
   const double up = ((double)c + 0.5) * ((double)c + 0.5), dn = ((double)c - 0.5) * ((double)c - 0.5);
-  int k = (int)c + (q >= up * up ? 1 : 0) - (c > 0.f && q < dn * dn ? 1 : 0);
-  return min(max(k, q > 0.0 ? 1 : 0), 255);
+  return fminf(c + (q >= up * up ? 1.f : 0.f) - (c > 0.f && q < dn * dn ? 1.f : 0.f), 255.f);
 }
 
-__device__ __forceinline__ double value_m(int c, double unit) {
-  return (double)(c * abs(c)) * unit;          // unit = a / 127^2
-}
-__device__ __forceinline__ double value_v(unsigned c, double unit) {
-  return (double)(c * c * c * c) * unit;       // unit = a / 255^4; 255^4 < 2^32
+// 1 / a to about 2^-52: the hardware's start and two Newton steps.
+__device__ __forceinline__ double reciprocal(double a) {
+  double r = __builtin_amdgcn_rcp(a);
+  r = fma(r, fma(-a, r, 1.0), r);
+  return fma(r, fma(-a, r, 1.0), r);
 }
 
-template <typename P, typename G, int BITS, bool MASTER>
-__global__ void __launch_bounds__(256)
-    k_adamw(const grpo_adamw_tensor* __restrict__ tensors, const int64_t* __restrict__ first,
-            int count, Hyper h) {
-  const int64_t chunk = blockIdx.x;
-  const int at = owner_of(first, count, chunk);
-  const grpo_adamw_tensor t = tensors[at];
-  const int64_t n = t.n, base = (chunk - first[at]) * kChunk;
-  P* param = (P*)t.param;
-  const G* grad = (const G*)t.grad;
-  float* master = (float*)t.master;
+constexpr double kUnitM = 1.0 / 16129.0, kUnitV = 1.0 / 4228250625.0;   // 127^-2, 255^-4
 
+__device__ __forceinline__ double square_m(int c) { return (double)(c * abs(c)); }
+__device__ __forceinline__ double fourth_v(unsigned c) {
+  const double s = (double)(c * c);
+  return s * s;
+}
+
+// What is the same for every element.
+struct Factors {
+  float scale, decay, step_size, inv_bc2, eps;
+  float b1, b2, a1, a2;
+};
+
+// w after the step.  The root and quotient of the hardware are good to a unit in the last place
+// for normal numbers; a smaller root only matters beside an eps that is smaller still.
+template <bool FAST>
+__device__ __forceinline__ float updated(float w, float m, float v, const Factors& f) {
+  const float vh = v * f.inv_bc2;
+  float u;
+  if (FAST && vh >= 1.17549435e-38f) u = m * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(vh) + f.eps);
+  else u = m / (sqrtf(vh) + f.eps);
+  return (w - f.decay * w) - f.step_size * u;
+}
+
+template <typename P, typename G, int BITS, bool MASTER, bool FULL>
+__device__ __forceinline__ void step_chunk(const grpo_adamw_tensor& t, int64_t base, const Hyper& h,
+                                           const Factors& f) {
+  const int n = FULL ? kChunk : (int)(t.n - base);
+  P* param = (P*)t.param + base;
+  const G* grad = (const G*)t.grad + base;
+  float* master = t.master + (MASTER ? base : 0);
   typename Vec4<P>::type p[kSteps];
   typename Vec4<G>::type g[kSteps];
   typename Vec4<float>::type w[kSteps], m[kSteps], v[kSteps];
@@ -154,55 +177,41 @@ __global__ void __launch_bounds__(256)
   float ma[kSteps], va[kSteps];
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
-    const int64_t e = base + (k * 256 + threadIdx.x) * 4;
-    g[k] = load4(grad, e, n);
-    if constexpr (MASTER) w[k] = load4(master, e, n);
-    else p[k] = load4(param, e, n);
+    const int e = (k * 256 + (int)threadIdx.x) * 4;
+    g[k] = load4<FULL>(grad, e, n);
+    if constexpr (MASTER) w[k] = load4<FULL>(master, e, n);
+    else p[k] = load4<FULL>(param, e, n);
     if constexpr (BITS == 32) {
-      m[k] = load4((const float*)t.exp_avg, e, n);
-      v[k] = load4((const float*)t.exp_avg_sq, e, n);
+      m[k] = load4<FULL>((const float*)t.exp_avg + base, e, n);
+      v[k] = load4<FULL>((const float*)t.exp_avg_sq + base, e, n);
     } else {
-      mc[k] = load4((const int8_t*)t.exp_avg, e, n);
-      vc[k] = load4((const uint8_t*)t.exp_avg_sq, e, n);
-      const int64_t b = e / kQuantBlock;      // one scale per wave and step
-      ma[k] = e < n ? t.exp_avg_scales[b] : 0.f;
-      va[k] = e < n ? t.exp_avg_sq_scales[b] : 0.f;
+      mc[k] = load4<FULL>((const int8_t*)t.exp_avg + base, e, n);
+      vc[k] = load4<FULL>((const uint8_t*)t.exp_avg_sq + base, e, n);
+      const int64_t b = base / kQuantBlock + e / kQuantBlock;      // one scale per wave and step
+      ma[k] = FULL || e < n ? t.exp_avg_scales[b] : 0.f;
+      va[k] = FULL || e < n ? t.exp_avg_sq_scales[b] : 0.f;
     }
   }
-
-  float step_size = h.step_size, inv_bc2 = h.inv_bc2, lr = h.lr;
-  if (h.lr_dev != nullptr) lr = *h.lr_dev;
-  if (h.lr_dev != nullptr || h.step_dev != nullptr) {
-    // 1 - b^t = -expm1(t log b), the product in float64: 1 - b^t loses nothing near b = 1
-    const int64_t s = h.step_dev != nullptr ? *h.step_dev : 0;
-    if (h.step_dev != nullptr) {
-      const double td = (double)(s < 1 ? 1 : s);
-      step_size = lr / -expm1f((float)(td * h.log_b1));
-      inv_bc2 = 1.f / -expm1f((float)(td * h.log_b2));
-    } else {
-      step_size = lr * h.step_size;            // the host passed 1 / (1 - b1^t)
-    }
-  }
-  const float scale = h.grad_scale != nullptr ? *h.grad_scale : 1.f;
-  const float decay = lr * h.wd;
-  const float b1 = (float)h.b1, b2 = (float)h.b2, a1 = (float)(1.0 - h.b1), a2 = (float)(1.0 - h.b2);
-
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
-    const int64_t e = base + (k * 256 + threadIdx.x) * 4;
+    const int e = (k * 256 + (int)threadIdx.x) * 4;
     float nm[4], nv[4];
     double dm[4], dv[4];
+    if constexpr (BITS == 32) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if constexpr (BITS == 32) {
-        const float x = (float)g[k][j] * scale;
-        nm[j] = m[k][j] * b1 + x * a1;
-        nv[j] = v[k][j] * b2 + x * x * a2;
-      } else {
-        // float64, so that the new codes are those of the exact moments
-        const double x = (double)(float)g[k][j] * (double)scale;
-        dm[j] = value_m(mc[k][j], (double)ma[k] * (1.0 / 16129.0)) * h.b1 + x * (1.0 - h.b1);
-        dv[j] = value_v(vc[k][j], (double)va[k] * (1.0 / 4228250625.0)) * h.b2 + x * x * (1.0 - h.b2);
+      for (int j = 0; j < 4; ++j) {
+        const float x = (float)g[k][j] * f.scale;
+        nm[j] = m[k][j] * f.b1 + x * f.a1;
+        nv[j] = v[k][j] * f.b2 + x * x * f.a2;
+      }
+    } else {
+      // float64, so that the new codes are those of the exact moments
+      const double um = (double)ma[k] * (kUnitM * h.b1), uv = (double)va[k] * (kUnitV * h.b2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const double x = (double)(float)g[k][j] * (double)f.scale;
+        dm[j] = fma(square_m(mc[k][j]), um, x * (1.0 - h.b1));
+        dv[j] = fma(fourth_v(vc[k][j]), uv, x * x * (1.0 - h.b2));
         nm[j] = (float)dm[j];
         nv[j] = (float)dv[j];
       }
@@ -214,67 +223,129 @@ __global__ void __launch_bounds__(256)
       float old;
       if constexpr (MASTER) old = w[k][j];
       else old = (float)p[k][j];
-      nw[j] = (old - decay * old) - step_size * (nm[j] / (sqrtf(nv[j] * inv_bc2) + h.eps));
+      nw[j] = updated<BITS == 8>(old, nm[j], nv[j], f);
       np[j] = (P)nw[j];
     }
-    store4(param, e, n, np);
-    if constexpr (MASTER) store4(master, e, n, nw);
+    store4<FULL>(param, e, n, np);
+    if constexpr (MASTER) store4<FULL>(master, e, n, nw);
     if constexpr (BITS == 32) {
-      store4((float*)t.exp_avg, e, n, typename Vec4<float>::type{nm[0], nm[1], nm[2], nm[3]});
-      store4((float*)t.exp_avg_sq, e, n, typename Vec4<float>::type{nv[0], nv[1], nv[2], nv[3]});
+      store4<FULL>((float*)t.exp_avg + base, e, n, typename Vec4<float>::type{nm[0], nm[1], nm[2], nm[3]});
+      store4<FULL>((float*)t.exp_avg_sq + base, e, n, typename Vec4<float>::type{nv[0], nv[1], nv[2], nv[3]});
     } else {
-      // lanes behind n hold zeros and zero codes
-      float top_m = 0.f, top_v = 0.f;
-      bool bad_m = false, bad_v = false;
+      // the block's largest magnitudes, as bits: above those of every finite value lie infinity
+      // and NaN (lanes behind n hold zeros)
+      uint32_t bits_m = 0, bits_v = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        top_m = fmaxf(top_m, fabsf(nm[j]));
-        top_v = fmaxf(top_v, nv[j]);
-        bad_m |= !(fabsf(nm[j]) <= 3.402823466e38f);
-        bad_v |= !(nv[j] <= 3.402823466e38f);
+        bits_m = max(bits_m, __float_as_uint(nm[j]) & 0x7fffffffu);
+        bits_v = max(bits_v, __float_as_uint(nv[j]) & 0x7fffffffu);
       }
-      top_m = wave_max(top_m);
-      top_v = wave_max(top_v);
-      bad_m = __any(bad_m);
-      bad_v = __any(bad_v);
-      const bool on_m = !bad_m && top_m > 0.f, on_v = !bad_v && top_v > 0.f;
-      const double to_m = on_m ? 16129.0 / (double)top_m : 0.0;
-      const double to_v = on_v ? 4228250625.0 / (double)top_v : 0.0;
-      typename Vec4<int8_t>::type cm = {};
-      typename Vec4<uint8_t>::type cv = {};
+      bits_m = wave_max(bits_m);
+      bits_v = wave_max(bits_v);
+      const bool bad_m = bits_m >= 0x7f800000u, bad_v = bits_v >= 0x7f800000u;
+      const float top_m = __uint_as_float(bits_m), top_v = __uint_as_float(bits_v);
+      const double to_m = bad_m || bits_m == 0 ? 0.0 : 16129.0 * reciprocal((double)top_m);
+      const double to_v = bad_v || bits_v == 0 ? 0.0 : 4228250625.0 * reciprocal((double)top_v);
+      float cm[4], cv[4], edge = 0.f;
+      double qm[4], qv[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (on_m) {
-          const int c = code_m(fabs(dm[j]) * to_m);
-          cm[j] = (int8_t)(dm[j] < 0.0 ? -c : c);
+        qm[j] = fabs(dm[j]) * to_m;
+        qv[j] = dv[j] * to_v;
+        const float rm = __builtin_amdgcn_sqrtf((float)qm[j]);
+        const float rv = __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf((float)qv[j]));
+        cm[j] = rintf(rm);
+        cv[j] = rintf(rv);
+        edge = fmaxf(edge, fmaxf(fabsf(rm - cm[j]), fabsf(rv - cv[j])));
+      }
+      // the roots are off by less than 10^-4, so only those that near a border need float64 (one
+      // step of a wave in ten has one); a scale below the normal numbers may be rounded so far
+      // that a root passes the last code
+      if (edge > 0.4999f || bits_m < 0x800000u || bits_v < 0x800000u) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          cm[j] = exact_m(cm[j], qm[j]);
+          cv[j] = exact_v(cv[j], qv[j]);
         }
-        if (on_v) cv[j] = (uint8_t)code_v(dv[j] * to_v);
       }
-      store4((int8_t*)t.exp_avg, e, n, cm);
-      store4((uint8_t*)t.exp_avg_sq, e, n, cv);
-      if ((threadIdx.x & 63) == 0 && e < n) {
-        t.exp_avg_scales[e / kQuantBlock] = bad_m ? __builtin_nanf("") : top_m;
-        t.exp_avg_sq_scales[e / kQuantBlock] = bad_v ? __builtin_nanf("") : top_v;
+      typename Vec4<int8_t>::type om;
+      typename Vec4<uint8_t>::type ov;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        om[j] = (int8_t)(int)__builtin_copysignf(cm[j], nm[j]);
+        ov[j] = (uint8_t)max((unsigned)cv[j], qv[j] > 0.0 ? 1u : 0u);
+      }
+      if (bad_m) om = typename Vec4<int8_t>::type{};
+      if (bad_v) ov = typename Vec4<uint8_t>::type{};
+      store4<FULL>((int8_t*)t.exp_avg + base, e, n, om);
+      store4<FULL>((uint8_t*)t.exp_avg_sq + base, e, n, ov);
+      if ((threadIdx.x & 63) == 0 && (FULL || e < n)) {
+        const int64_t b = base / kQuantBlock + e / kQuantBlock;
+        t.exp_avg_scales[b] = bad_m ? __builtin_nanf("") : top_m;
+        t.exp_avg_sq_scales[b] = bad_v ? __builtin_nanf("") : top_v;
       }
     }
   }
 }
 
-// The float32 values of 8-bit moments.
+template <typename P, typename G, int BITS, bool MASTER>
+__global__ void __launch_bounds__(256)
+    k_adamw(const grpo_adamw_tensor* __restrict__ tensors, const int64_t* __restrict__ first,
+            int count, Hyper h) {
+  const int64_t chunk = blockIdx.x;
+  const int at = owner_of(first, count, chunk);
+  const grpo_adamw_tensor t = tensors[at];
+  const int64_t base = (chunk - first[at]) * kChunk;
+
+  Factors f;
+  float lr = h.lr;
+  f.step_size = h.step_size;
+  f.inv_bc2 = h.inv_bc2;
+  f.eps = h.eps;
+  if (h.lr_dev != nullptr) lr = *h.lr_dev;
+  if (h.step_dev != nullptr) {
+    // 1 - b^t = -expm1(t log b), the product in float64: 1 - b^t loses nothing near b = 1
+    const int64_t s = *h.step_dev;
+    const double td = (double)(s < 1 ? 1 : s);
+    f.step_size = lr / -expm1f((float)(td * h.log_b1));
+    f.inv_bc2 = 1.f / -expm1f((float)(td * h.log_b2));
+  } else if (h.lr_dev != nullptr) {
+    f.step_size = lr * h.step_size;            // the host passed 1 / (1 - b1^t)
+  }
+  f.scale = h.grad_scale != nullptr ? *h.grad_scale : 1.f;
+  f.decay = lr * h.wd;
+  f.b1 = (float)h.b1;
+  f.b2 = (float)h.b2;
+  f.a1 = (float)(1.0 - h.b1);
+  f.a2 = (float)(1.0 - h.b2);
+  if (base + kChunk <= t.n) step_chunk<P, G, BITS, MASTER, true>(t, base, h, f);
+  else step_chunk<P, G, BITS, MASTER, false>(t, base, h, f);
+}
+
+// The float32 values of 8-bit moments: a block takes 4096 of them.
 template <typename C>
 __global__ void __launch_bounds__(256)
     k_moment_values(const C* __restrict__ codes, const float* __restrict__ scales, int64_t n,
                     float* __restrict__ out) {
-  const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (e >= n) return;
-  const typename Vec4<C>::type c = load4(codes, e, n);
-  const double a = (double)scales[e / kQuantBlock];
-  typename Vec4<float>::type o;
+  const int64_t base = (int64_t)blockIdx.x * kChunk;
+  const int left = (int)min<int64_t>(kChunk, n - base);
+  typename Vec4<C>::type c[kSteps];
+  float a[kSteps];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    o[j] = sizeof(C) == 1 && (C)-1 < (C)0 ? (float)value_m((int)c[j], a * (1.0 / 16129.0))
-                                          : (float)value_v((unsigned)c[j], a * (1.0 / 4228250625.0));
-  store4(out, e, n, o);
+  for (int k = 0; k < kSteps; ++k) {
+    const int e = (k * 256 + (int)threadIdx.x) * 4;
+    c[k] = load4<false>(codes + base, e, left);
+    a[k] = e < left ? scales[base / kQuantBlock + e / kQuantBlock] : 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < kSteps; ++k) {
+    typename Vec4<float>::type o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = (C)-1 < (C)0 ? (float)(square_m((int)c[k][j]) * ((double)a[k] * kUnitM))
+                          : (float)(fourth_v((unsigned)c[k][j]) * ((double)a[k] * kUnitV));
+    store4<false>(out + base, (k * 256 + (int)threadIdx.x) * 4, left, o);
+  }
 }
 
 template <typename P, typename G, bool MASTER>
@@ -465,7 +536,7 @@ int grpo_moment_values(const void* codes, const float* scales, int64_t n, int sq
   GRPO_CHECK_PTR(codes);
   GRPO_CHECK_PTR(scales);
   GRPO_CHECK_PTR(out);
-  const int64_t blocks = (n + 1023) / 1024;
+  const int64_t blocks = (n + grpo::kChunk - 1) / grpo::kChunk;
   if (blocks > grpo::kMaxBlocks) return fail(GRPO_ERR_UNSUPPORTED, "n is too large");
   hipStream_t s = (hipStream_t)stream;
   grpo::ScopedKernelTimer timer(grpo::KK_MOMENT_VALUES, s);
