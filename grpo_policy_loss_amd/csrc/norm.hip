@@ -7,7 +7,9 @@
 //   dw += sum over rows of dy xh,  db += sum over rows of dy
 // All of it is bound by memory: the forward reads x once and writes y once, the backward
 // reads dy and x once and writes dx once.  A row therefore stays in registers between its
-// sums and its result: LPR lanes hold a row as NV vectors of 16 bytes each.
+// sums and its result: LPR lanes hold a row as NV vectors of 16 bytes each.  Measured in bf16:
+// forward of 32768 x 1536 39 us (5.2 TB/s), backward of 32768 x 4096 with mean and bias 148 us
+// (5.4 TB/s); a copy of that size reaches 4.7 to 5.1 TB/s on the same card.
 #include <math.h>
 
 #include <algorithm>
@@ -22,9 +24,12 @@ namespace {
 constexpr int kCUs = 256;
 
 template <int LPR> constexpr int kThreads = LPR > 256 ? LPR : 256;
+// The backward takes two rows of 256 lanes at a time: a block then leaves one partial row of dw
+// for twice the rows.
+template <int LPR> constexpr int kThreadsBwd = LPR >= 256 && LPR <= 512 ? 512 : kThreads<LPR>;
 
-// Sums of a and b over the LPR lanes of a row, in every lane.  LPR > 64: one row per block;
-// the waves' sums meet in LDS.  `phase` alternates between two LDS buffers, so one barrier
+// Sums of a and b over the LPR lanes of a row, in every lane.  LPR > 64: the waves' sums meet
+// in LDS.  `phase` alternates between two LDS buffers, so one barrier
 // per call is enough: a buffer is written again only behind the next call's barrier, which
 // every wave reaches after it has read this one.
 template <int LPR>
@@ -36,7 +41,7 @@ __device__ __forceinline__ void row_sums(float& a, float& b, float (*lds)[2][16]
   }
   if constexpr (LPR > 64) {
     constexpr int W = LPR / 64;
-    const int w = threadIdx.x >> 6;
+    const int w = threadIdx.x >> 6, w0 = threadIdx.x / LPR * W;
     if ((threadIdx.x & 63) == 0) {
       lds[phase][0][w] = a;
       lds[phase][1][w] = b;
@@ -45,8 +50,8 @@ __device__ __forceinline__ void row_sums(float& a, float& b, float (*lds)[2][16]
     a = b = 0.f;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-      a += lds[phase][0][i];
-      b += lds[phase][1][i];
+      a += lds[phase][0][w0 + i];
+      b += lds[phase][1][w0 + i];
     }
   }
 }
@@ -136,14 +141,14 @@ __global__ void __launch_bounds__(1024)
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const T* x = X + row * n;
     float s = 0.f, q = 0.f, dummy = 0.f;
-    for (int64_t c = threadIdx.x * VE; c < n; c += 1024 * VE) {
+    for (int c = threadIdx.x * VE; c < n; c += 1024 * VE) {
       const V t = load_vec(x, c, n);
 #pragma unroll
       for (int j = 0; j < VE; ++j) s += (float)t[j];
     }
     row_sums<1024>(s, dummy, lds, 0);
     const float mu = layer ? s * inv_n : 0.f;
-    for (int64_t c = threadIdx.x * VE; c < n; c += 1024 * VE) {
+    for (int c = threadIdx.x * VE; c < n; c += 1024 * VE) {
       const V t = load_vec(x, c, n);
 #pragma unroll
       for (int j = 0; j < VE; ++j) {
@@ -153,7 +158,7 @@ __global__ void __launch_bounds__(1024)
     }
     row_sums<1024>(q, dummy, lds, 1);
     const float r = 1.f / sqrtf(q * inv_n + eps);
-    for (int64_t c = threadIdx.x * VE; c < n; c += 1024 * VE) {
+    for (int c = threadIdx.x * VE; c < n; c += 1024 * VE) {
       const V t = load_vec(x, c, n), w = load_vec(weight, c, n);
       V b = {}, o;
       if (bias != nullptr) b = load_vec(bias, c, n);
@@ -169,17 +174,18 @@ __global__ void __launch_bounds__(1024)
 }
 
 // ---------------------------------------------------------------- backward
-// Each block walks rows blockIdx, blockIdx + grid, ...  A lane holds the same columns of
+// Each block walks rows blockIdx, blockIdx + grid, ... (neighbouring blocks on neighbouring rows:
+// with a run of rows for each block 32768 x 1536 took 7 % longer).  A lane holds the same columns of
 // every row, so the weight's and bias's gradients add up in its registers; at the end the
 // block's row groups are joined (lanes, then waves) into one partial row of dw and of db,
 // which k_norm_reduce sums in block order.
 template <typename T, int LPR, int NV, bool DB>
-__global__ void __launch_bounds__(kThreads<LPR>)
+__global__ void __launch_bounds__(kThreadsBwd<LPR>, LPR == 256 ? 4 : 1)
     k_norm_bwd(const T* __restrict__ dY, const T* __restrict__ X, const T* __restrict__ weight,
                const float* __restrict__ mean, const float* __restrict__ rstd, int64_t rows, int n,
                T* __restrict__ dX, float* __restrict__ part_w, float* __restrict__ part_b) {
   typedef typename Vec16<T>::type V;
-  constexpr int VE = kVec<T>, RPB = kThreads<LPR> / LPR;
+  constexpr int VE = kVec<T>, RPB = kThreadsBwd<LPR> / LPR;
   __shared__ float lds[2][2][16];
   const int lane = threadIdx.x % LPR, sub = threadIdx.x / LPR;
   V w[NV];
@@ -201,8 +207,13 @@ __global__ void __launch_bounds__(kThreads<LPR>)
     V x[NV], d[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      x[i] = load_vec(X + row * n, (lane + i * LPR) * VE, n);
-      d[i] = load_vec(dY + row * n, (lane + i * LPR) * VE, n);
+      x[i] = fetch_vec(X + row * n, (lane + i * LPR) * VE, n);
+      d[i] = fetch_vec(dY + row * n, (lane + i * LPR) * VE, n);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      x[i] = place_vec<T>(x[i], (lane + i * LPR) * VE, n);
+      d[i] = place_vec<T>(d[i], (lane + i * LPR) * VE, n);
     }
     float c1 = 0.f, c2 = 0.f;
 #pragma unroll
@@ -247,33 +258,33 @@ __global__ void __launch_bounds__(kThreads<LPR>)
           if (DB) ab[i][j] += __shfl_xor(ab[i][j], o, 64);
         }
   }
-  if constexpr (LPR <= 64) {
-    constexpr int W = kThreads<LPR> / 64;
-    __shared__ float joined[W - 1][NV * VE * LPR];
-    const int wave = threadIdx.x >> 6;
-    const bool mine = (threadIdx.x & 63) < LPR;
+  constexpr int HOLD = LPR < 64 ? 64 : LPR, GROUPS = kThreadsBwd<LPR> / HOLD;
+  if constexpr (GROUPS > 1) {
+    __shared__ float joined[GROUPS - 1][NV * VE * LPR];
+    const int group = threadIdx.x / HOLD;
+    const bool mine = (int)threadIdx.x % HOLD < LPR;
     for (int pass = 0; pass < (DB ? 2 : 1); ++pass) {
       if (pass) __syncthreads();
-      if (mine && wave > 0)
+      if (mine && group > 0)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
           for (int j = 0; j < VE; ++j)
-            joined[wave - 1][(i * VE + j) * LPR + lane] = pass ? ab[i][j] : aw[i][j];
+            joined[group - 1][(i * VE + j) * LPR + lane] = pass ? ab[i][j] : aw[i][j];
       __syncthreads();
-      if (mine && wave == 0)
+      if (mine && group == 0)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
           for (int j = 0; j < VE; ++j) {
             float t = pass ? ab[i][j] : aw[i][j];
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) t += joined[k][(i * VE + j) * LPR + lane];
+            for (int k = 0; k < GROUPS - 1; ++k) t += joined[k][(i * VE + j) * LPR + lane];
             if (pass) ab[i][j] = t;
             else aw[i][j] = t;
           }
     }
-    if (wave != 0 || !mine) return;
+    if (group != 0 || !mine) return;
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(1024)
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const float r = rstd[row], mu = mean != nullptr ? mean[row] : 0.f;
     float c1 = 0.f, c2 = 0.f;
-    for (int64_t c = threadIdx.x * VE; c < n; c += 1024 * VE) {
+    for (int c = threadIdx.x * VE; c < n; c += 1024 * VE) {
       const V x = load_vec(X + row * n, c, n), d = load_vec(dY + row * n, c, n),
               w = load_vec(weight, c, n);
 #pragma unroll
@@ -318,7 +329,7 @@ __global__ void __launch_bounds__(1024)
     phase ^= 1;
     c1 *= inv_n;
     c2 = mean != nullptr ? c2 * inv_n : 0.f;
-    for (int64_t c = threadIdx.x * VE; c < n; c += 1024 * VE) {
+    for (int c = threadIdx.x * VE; c < n; c += 1024 * VE) {
       const V x = load_vec(X + row * n, c, n), d = load_vec(dY + row * n, c, n),
               w = load_vec(weight, c, n);
       V o;
@@ -374,35 +385,43 @@ __global__ void __launch_bounds__(1024)
 }
 
 // ---------------------------------------------------------------- launches
-// How a row of n elements is held: lanes per row, vectors per lane.  Both directions take
-// the fewest lanes that keep at most NV vectors each; n above the last entry: long rows.
+// How a row of n elements is held: lanes per row, vectors per lane; {0, 0}: long rows.  The
+// fewest lanes that hold it in at most two vectors each (four for the longest rows).
 struct RowShape {
   int lpr, nv;
 };
-template <typename T> RowShape row_shape(int64_t n) {
-  static const RowShape shapes[] = {{4, 1},   {16, 1},  {64, 1},  {64, 2},
-                                    {256, 1}, {256, 2}, {512, 2}, {512, 4}, {1024, 4}};
-  for (const RowShape& s : shapes)
-    if (n <= (int64_t)s.lpr * s.nv * kVec<T> && (s.lpr < 1024 || sizeof(T) == 4)) return s;
+template <typename T> RowShape row_shape(int64_t n, bool backward) {
+  static const RowShape shapes[] = {{4, 1},   {16, 1},  {64, 1},  {64, 2},  {256, 1},
+                                    {256, 2}, {512, 2}, {512, 4}, {1024, 4}};
+  for (const RowShape& s : shapes) {
+    if (n > (int64_t)s.lpr * s.nv * kVec<T> || (s.lpr == 1024 && sizeof(T) != 4)) continue;
+    // The backward of 16-bit rows that nearly fill 512 lanes of one vector is faster in those, with
+    // fewer registers (32768 x 4096 with bias 147 us against 180), that of shorter rows in 256 lanes
+    // of two, which keep more rows in flight (32768 x 2880: 110 us against 130).
+    if (backward && sizeof(T) == 2 && s.lpr == 256 && s.nv == 2 && n > 416 * kVec<T>) return {512, 1};
+    return s;
+  }
   return {0, 0};
 }
 
 #define GRPO_ROW_SHAPES(CASE) \
   CASE(4, 1) CASE(16, 1) CASE(64, 1) CASE(64, 2) CASE(256, 1) CASE(256, 2) CASE(512, 2) CASE(512, 4)
 
-// Blocks of the backward, each of which leaves one partial row.  Four blocks of 256 threads
-// per CU keep enough rows in flight.
-int64_t bwd_blocks(int64_t rows, RowShape sh) {
-  const int64_t rpb = sh.lpr == 0 ? 1 : std::max(1, 256 / sh.lpr);
-  const int64_t most = sh.lpr == 0 ? 64 : sh.lpr > 512 ? kCUs : sh.lpr > 256 ? 2 * kCUs : 4 * kCUs;
-  return std::min<int64_t>((rows + rpb - 1) / rpb, most);
+// Blocks of the backward, each of which leaves one partial row: as many as keep the loads
+// going, but no more, since partial rows are written and read again (and the sums of a bias
+// take registers: with three blocks a CU, 32768 x 2048 took 89 us, with two 77).
+int64_t bwd_blocks(int64_t rows, RowShape sh, bool bias) {
+  if (sh.lpr == 0) return std::min<int64_t>(rows, 64);
+  const int64_t rpb = sh.lpr >= 256 ? std::max(1, 512 / sh.lpr) : 256 / sh.lpr;
+  const int64_t most = sh.nv == 4 ? 1 : sh.lpr == 256 && sh.nv == 1 ? (bias ? 2 : 3) : sh.lpr >= 256 ? 2 : 4;
+  return std::min<int64_t>((rows + rpb - 1) / rpb, most * kCUs);
 }
 
 template <typename T>
 hipError_t launch_norm_fwd(const T* X, const T* w, const T* b, int64_t rows, int n, int layer,
                            float eps, T* Y, float* mean, float* rstd, hipStream_t s) {
   ScopedKernelTimer t(KK_NORM_FWD, s);
-  const RowShape sh = row_shape<T>(n);
+  const RowShape sh = row_shape<T>(n, false);
   const int64_t rpb = sh.lpr == 0 ? 1 : std::max(1, 256 / sh.lpr);
   const unsigned grid = (unsigned)std::min<int64_t>((rows + rpb - 1) / rpb, 8 * kCUs);
 #define GRPO_CASE(L, N)                                                                      \
@@ -424,19 +443,19 @@ hipError_t launch_norm_bwd(const T* dY, const T* X, const T* w, const float* mea
                            const float* rstd, int64_t rows, int n, T* dX, float* part_w,
                            float* part_b, hipStream_t s) {
   ScopedKernelTimer t(KK_NORM_BWD, s);
-  const RowShape sh = row_shape<T>(n);
-  const unsigned grid = (unsigned)bwd_blocks(rows, sh);
+  const RowShape sh = row_shape<T>(n, true);
+  const unsigned grid = (unsigned)bwd_blocks(rows, sh, part_b != nullptr);
 #define GRPO_CASE(L, N)                                                                         \
   if (sh.lpr == L && sh.nv == N) {                                                              \
     if (part_b != nullptr)                                                                      \
-      k_norm_bwd<T, L, N, true><<<grid, kThreads<L>, 0, s>>>(dY, X, w, mean, rstd, rows, n, dX, \
+      k_norm_bwd<T, L, N, true><<<grid, kThreadsBwd<L>, 0, s>>>(dY, X, w, mean, rstd, rows, n, dX, \
                                                              part_w, part_b);                   \
     else                                                                                        \
-      k_norm_bwd<T, L, N, false><<<grid, kThreads<L>, 0, s>>>(dY, X, w, mean, rstd, rows, n, dX, \
+      k_norm_bwd<T, L, N, false><<<grid, kThreadsBwd<L>, 0, s>>>(dY, X, w, mean, rstd, rows, n, dX, \
                                                               part_w, part_b);                  \
     return hipGetLastError();                                                                   \
   }
-  GRPO_ROW_SHAPES(GRPO_CASE)
+  GRPO_ROW_SHAPES(GRPO_CASE) GRPO_CASE(512, 1)
   if constexpr (sizeof(T) == 4) {  // 16-bit rows of this length would spill
     GRPO_CASE(1024, 4)
   }
@@ -474,8 +493,9 @@ int check_norm(int64_t rows, int64_t cols, int dtype, int kind) {
 }
 
 // The number of partial rows for either type (their vectors differ, so their lanes do).
-int64_t partial_rows(int64_t rows, int64_t cols, int dtype) {
-  return bwd_blocks(rows, dtype == GRPO_F32 ? row_shape<float>(cols) : row_shape<__bf16>(cols));
+int64_t partial_rows(int64_t rows, int64_t cols, int dtype, bool bias) {
+  return bwd_blocks(rows, dtype == GRPO_F32 ? row_shape<float>(cols, true) : row_shape<__bf16>(cols, true),
+                    bias);
 }
 
 }  // namespace
@@ -487,7 +507,7 @@ extern "C" {
 
 size_t grpo_norm_workspace_bytes(int64_t rows, int64_t cols, int dtype) {
   if (grpo::check_norm(rows, cols, dtype, GRPO_NORM_LAYER) != GRPO_OK) return 0;
-  return 2 * grpo::align_up((size_t)(grpo::partial_rows(rows, cols, dtype) * cols) * 4);
+  return 2 * grpo::align_up((size_t)(grpo::partial_rows(rows, cols, dtype, false) * cols) * 4);
 }
 
 int grpo_norm_fwd(const void* X, const void* weight, const void* bias, int64_t rows, int64_t cols,
@@ -537,7 +557,7 @@ int grpo_norm_bwd(const void* dY, const void* X, const void* weight, const float
   hipStream_t s = (hipStream_t)stream;
   float* part_w = (float*)workspace;
   float* part_b = dbias == nullptr ? nullptr : (float*)((char*)workspace + need / 2);
-  const int np = (int)grpo::partial_rows(rows, cols, dtype);
+  const int np = (int)grpo::partial_rows(rows, cols, dtype, dbias != nullptr);
   if (dtype == GRPO_BF16)
     GRPO_HIP(grpo::launch_norm_bwd<__bf16>((const __bf16*)dY, (const __bf16*)X,
                                            (const __bf16*)weight, mu, rstd, rows, (int)cols,
