@@ -92,8 +92,8 @@ SIGNATURES = {
                                  _i64, _i64, _f32, _f32, _i64, _OPTS_P, _vp, _vp, _vp, _sz, _vp]),
     "grpo_norm_workspace_bytes": (_sz, [_i64, _i64, _int]),
     "grpo_norm_fwd": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _int, _f32, _vp, _vp, _vp, _vp]),
-    "grpo_norm_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _vp, _vp, _vp, _vp,
-                             _sz, _vp]),
+    "grpo_norm_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _int, _vp, _vp, _vp,
+                             _vp, _sz, _vp]),
     "grpo_adamw_plan_bytes": (_sz, [_i64]),
     "grpo_adamw_plan": (_int, [ctypes.POINTER(AdamWTensor), _i64, _int, _int, _int, _vp, _sz]),
     "grpo_adamw": (_int, [_vp, _vp, ctypes.POINTER(AdamWOpts), _vp]),

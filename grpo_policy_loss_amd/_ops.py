@@ -86,7 +86,7 @@ def _norm_bytes(rows, cols, dt):
 def grpo_norm_bwd(dY, X, weight, mean, rstd, kind: int = NORM_RMS, bias: bool = False, dX=None,
                   dweight=None, dbias=None, workspace=None):
     """(dX, dweight, dbias): dX in X's type; dweight and dbias [cols] float32,
-    accumulated into when given (zeros are allocated otherwise).  dbias is formed
+    accumulated into when given.  dbias is formed
     if `bias` is true or dbias is given, and None otherwise.  mean and rstd are
     grpo_norm_fwd's (mean None for NORM_RMS)."""
     rows, cols = _matrix(X, "X")
@@ -100,12 +100,17 @@ def grpo_norm_bwd(dY, X, weight, mean, rstd, kind: int = NORM_RMS, bias: bool = 
         mean = None
     dev = X.device
     dX = torch.empty_like(X) if dX is None else _arg(dX, "dX", dtype=X.dtype, shape=(rows, cols))
-    dweight = torch.zeros(cols, dtype=torch.float32, device=dev) if dweight is None else \
+    # into the caller's accumulators, or new tensors that the call fills
+    accumulate = dweight is not None or dbias is not None
+    new = torch.zeros if accumulate else torch.empty
+    if dweight is not None:
         _arg(dweight, "dweight", dtype=torch.float32, numel=cols)
+    else:
+        dweight = new(cols, dtype=torch.float32, device=dev)
     if dbias is not None:
         _arg(dbias, "dbias", dtype=torch.float32, numel=cols)
     elif bias:
-        dbias = torch.zeros(cols, dtype=torch.float32, device=dev)
+        dbias = new(cols, dtype=torch.float32, device=dev)
     need = _norm_bytes(rows, cols, dt)
     if workspace is not None:
         workspace = _workspace(need, dev, workspace)
@@ -115,7 +120,7 @@ def grpo_norm_bwd(dY, X, weight, mean, rstd, kind: int = NORM_RMS, bias: bool = 
         ws = _workspace(need, dev, workspace)
         _check("grpo_norm_bwd", lib().grpo_norm_bwd(
             _ptr(dY), _ptr(X), _ptr(weight), _ptr(mean), _ptr(rstd), rows, cols, dt, kind,
-            _ptr(dX), _ptr(dweight), _ptr(dbias), _ptr(ws), ws.numel(), stream))
+            int(accumulate), _ptr(dX), _ptr(dweight), _ptr(dbias), _ptr(ws), ws.numel(), stream))
     return dX, dweight, dbias
 
 

@@ -541,8 +541,8 @@ int grpo_moment_values(const void* codes, const float* scales, int64_t n, int sq
   GRPO_CHECK_PTR(codes);
   GRPO_CHECK_PTR(scales);
   GRPO_CHECK_PTR(out);
+  if (n > grpo::kMaxBlocks * grpo::kChunk) return fail(GRPO_ERR_UNSUPPORTED, "n is too large");
   const int64_t blocks = (n + grpo::kChunk - 1) / grpo::kChunk;
-  if (blocks > grpo::kMaxBlocks) return fail(GRPO_ERR_UNSUPPORTED, "n is too large");
   hipStream_t s = (hipStream_t)stream;
   grpo::ScopedKernelTimer timer(grpo::KK_MOMENT_VALUES, s);
   if (squared)

@@ -360,11 +360,11 @@ __global__ void __launch_bounds__(256)
   if (part_b != nullptr) part_b[(int64_t)blockIdx.y * n + c] = ab;
 }
 
-// out[c] += sum over the np partial rows, in a fixed order: 16 row lanes of 64 columns each.
-// blockIdx.y picks dw or db.
+// out[c] = (or +=) the sum over the np partial rows, in a fixed order: 16 row lanes of 64 columns
+// each.  blockIdx.y picks dw or db.
 __global__ void __launch_bounds__(1024)
     k_norm_reduce(const float* __restrict__ part_w, const float* __restrict__ part_b, int np, int n,
-                  float* __restrict__ dw, float* __restrict__ db) {
+                  int accumulate, float* __restrict__ dw, float* __restrict__ db) {
   __shared__ float lds[16][64];
   const float* part = blockIdx.y ? part_b : part_w;
   float* out = blockIdx.y ? db : dw;
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(1024)
   if (rl == 0 && c < n) {
 #pragma unroll
     for (int i = 1; i < 16; ++i) s += lds[i][threadIdx.x];
-    out[c] += s;
+    out[c] = accumulate ? out[c] + s : s;
   }
 }
 
@@ -469,11 +469,11 @@ hipError_t launch_norm_bwd(const T* dY, const T* X, const T* w, const float* mea
   return hipGetLastError();
 }
 
-hipError_t launch_norm_reduce(const float* part_w, const float* part_b, int np, int n, float* dw,
-                              float* db, hipStream_t s) {
+hipError_t launch_norm_reduce(const float* part_w, const float* part_b, int np, int n,
+                              int accumulate, float* dw, float* db, hipStream_t s) {
   ScopedKernelTimer t(KK_NORM_REDUCE, s);
   k_norm_reduce<<<dim3((unsigned)((n + 63) / 64), db != nullptr ? 2 : 1), 1024, 0, s>>>(
-      part_w, part_b, np, n, dw, db);
+      part_w, part_b, np, n, accumulate, dw, db);
   return hipGetLastError();
 }
 
@@ -536,9 +536,9 @@ int grpo_norm_fwd(const void* X, const void* weight, const void* bias, int64_t r
 }
 
 int grpo_norm_bwd(const void* dY, const void* X, const void* weight, const float* mean,
-                  const float* rstd, int64_t rows, int64_t cols, int dtype, int kind, void* dX,
-                  float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
-                  void* stream) {
+                  const float* rstd, int64_t rows, int64_t cols, int dtype, int kind,
+                  int accumulate, void* dX, float* dweight, float* dbias, void* workspace,
+                  size_t workspace_bytes, void* stream) {
   grpo::clear_error();
   GRPO_CHECK_PTR(dY);
   GRPO_CHECK_PTR(X);
@@ -550,6 +550,8 @@ int grpo_norm_bwd(const void* dY, const void* X, const void* weight, const float
   if (st != GRPO_OK) return st;
   const float* mu = kind == GRPO_NORM_LAYER ? mean : nullptr;
   if (kind == GRPO_NORM_LAYER) GRPO_CHECK_PTR(mean);
+  if (accumulate != 0 && accumulate != 1)
+    return fail(GRPO_ERR_INVALID_ARG, "accumulate must be 0 or 1");
   const size_t need = grpo_norm_workspace_bytes(rows, cols, dtype);
   if (workspace == nullptr || workspace_bytes < need)
     return fail(GRPO_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
@@ -566,7 +568,7 @@ int grpo_norm_bwd(const void* dY, const void* X, const void* weight, const float
     GRPO_HIP(grpo::launch_norm_bwd<float>((const float*)dY, (const float*)X, (const float*)weight,
                                           mu, rstd, rows, (int)cols, (float*)dX, part_w, part_b,
                                           s));
-  GRPO_HIP(grpo::launch_norm_reduce(part_w, part_b, np, (int)cols, dweight, dbias, s));
+  GRPO_HIP(grpo::launch_norm_reduce(part_w, part_b, np, (int)cols, accumulate, dweight, dbias, s));
   return GRPO_OK;
 }
 

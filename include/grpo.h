@@ -339,8 +339,8 @@ int grpo_loss_fwd_noalloc(const void* H, const void* W, const int32_t* y, const 
  *   and >= 0.
  * grpo_norm_bwd: dY [rows, cols] the gradient of Y; X, weight, mean and rstd
  *   as in the forward.  dX [rows, cols] dtype, OVERWRITTEN; dweight [cols] and
- *   dbias [cols] (NULL: not formed) float32, ACCUMULATED (+=) as dW is in
- *   grpo_loss_bwd.  workspace: grpo_norm_workspace_bytes(rows, cols, dtype),
+ *   dbias [cols] (NULL: not formed) float32, ACCUMULATED (+=, as dW is in
+ *   grpo_loss_bwd) if accumulate is 1, OVERWRITTEN if it is 0.  workspace: grpo_norm_workspace_bytes(rows, cols, dtype),
  *   256-byte aligned.
  * Any cols from 1 to 2^24 and any element alignment.  Sums are float32, in a
  * fixed order: results are bitwise reproducible.
@@ -351,9 +351,9 @@ size_t grpo_norm_workspace_bytes(int64_t rows, int64_t cols, int dtype);
 int grpo_norm_fwd(const void* X, const void* weight, const void* bias, int64_t rows, int64_t cols,
                   int dtype, int kind, float eps, void* Y, float* mean, float* rstd, void* stream);
 int grpo_norm_bwd(const void* dY, const void* X, const void* weight, const float* mean,
-                  const float* rstd, int64_t rows, int64_t cols, int dtype, int kind, void* dX,
-                  float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
-                  void* stream);
+                  const float* rstd, int64_t rows, int64_t cols, int dtype, int kind,
+                  int accumulate, void* dX, float* dweight, float* dbias, void* workspace,
+                  size_t workspace_bytes, void* stream);
 
 /*
  * One AdamW step over many tensors in one launch; the consumer of

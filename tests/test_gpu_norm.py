@@ -120,6 +120,10 @@ def test_gradients_are_accumulated_and_bitwise_repeatable():
     assert out[0] is dx and out[1] is dw and out[2] is db
     assert torch.equal(dx, runs[0][0])
     assert torch.equal(dw, 3.0 + runs[0][1]) and torch.equal(db, -2.0 + runs[0][2])
+    # one accumulator given: the other starts at zero
+    dw = torch.full((1537,), 3.0, device="cuda")
+    out = gp.grpo_norm_bwd(i["dy"], i["x"], i["w"], mean, rstd, gp.NORM_LAYER, bias=True, dweight=dw)
+    assert torch.equal(dw, 3.0 + runs[0][1]) and torch.equal(out[2], runs[0][2])
 
 
 def test_nan_and_infinite_values_stay_in_their_row():

@@ -24,7 +24,7 @@ def fwd(**kw):
 
 
 def bwd(**kw):
-    a = dict(dY=FAKE, X=FAKE, w=FAKE, mean=FAKE, rstd=FAKE, rows=4, cols=8, dt=0, kind=0, dX=FAKE,
+    a = dict(dY=FAKE, X=FAKE, w=FAKE, mean=FAKE, rstd=FAKE, rows=4, cols=8, dt=0, kind=0, acc=0, dX=FAKE,
              dw=FAKE, db=None, ws=FAKE, wsb=1 << 30)
     a.update(kw)
     return L.grpo_norm_bwd(*a.values(), None)
@@ -43,7 +43,7 @@ def test_forward_argument_errors(kw, code):
 @pytest.mark.parametrize("kw,code", [
     ({"dY": None}, -1), ({"X": None}, -1), ({"w": None}, -1), ({"mean": None}, -1),
     ({"rstd": None}, -1), ({"dX": None}, -1), ({"dw": None}, -1), ({"rows": -3}, -1),
-    ({"dt": 7}, -1), ({"kind": -1}, -1), ({"ws": None}, -2), ({"wsb": 16}, -2),
+    ({"dt": 7}, -1), ({"kind": -1}, -1), ({"acc": 2}, -1), ({"ws": None}, -2), ({"wsb": 16}, -2),
     ({"cols": 1 << 25}, -3)])
 def test_backward_argument_errors(kw, code):
     assert bwd(**kw) == code
