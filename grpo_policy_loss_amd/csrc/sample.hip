@@ -223,7 +223,9 @@ __global__ void __launch_bounds__(256, 4) k_sample_mass(SampleArgs a, int64_t wa
   for (;;) {
     float x[4][8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) unpack(next.q[q], x[q]);
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[q][j] = (float)next.q[q].v[j / kVec<T>][j % kVec<T>];
     const bool more = w + step < waves;
     if (more) next = load_seg<T>(a, (w + step) / a.segs, (int)((w + step) % a.segs));
     const RowParams r = row_params(a, w / a.segs);
@@ -357,14 +359,15 @@ template <int NT>
 __device__ __forceinline__ RowRange row_range(const SampleArgs& a, int64_t row, float (*lds)[NT / 64]) {
   float top = kNone, low = -kNone;
   bool bad = false;
+  // a thread past the last segment looks at the last one again
 #pragma unroll
-  for (int i = threadIdx.x; i < kMaxSegs; i += NT)
-    if (i < a.segs) {
-      const float m = a.seg_max[row * a.segs + i];
-      top = fmaxf(top, m);
-      bad |= m != m;
-      low = fminf(low, a.seg_min[row * a.segs + i]);
-    }
+  for (int i = 0; i < kMaxSegs; i += NT) {
+    const int64_t at = row * a.segs + min(i + (int)threadIdx.x, a.segs - 1);
+    const float m = a.seg_max[at];
+    top = fmaxf(top, m);
+    bad |= m != m;
+    low = fminf(low, a.seg_min[at]);
+  }
   return row_range<NT>(top, low, bad, lds);
 }
 // Whether there is anything to draw from.
@@ -800,8 +803,11 @@ __device__ __forceinline__ int candidates(const SampleArgs& a, int64_t row, cons
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
       const int at = base + i * kPick + (int)threadIdx.x;
-      g[i] = at < groups ? gm[at] : kNone;
+      g[i] = gm[min(at, groups - 1)];
     }
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (base + i * kPick + (int)threadIdx.x >= groups) g[i] = kNone;
   };
   load(0);
   Binning bin(st.max, 0.f, kBins);          // all that is above -inf into bin 0
@@ -868,8 +874,9 @@ __device__ __forceinline__ int candidates(const SampleArgs& a, int64_t row, cons
   __syncthreads();
   const int wanted_groups = *n_groups;
   if (wanted_groups > kList) return kList + 1;
-  // 32 threads to a group, 32 tokens of each thread at a time
-  constexpr int AT_ONCE = 32;
+  // 32 threads to a group, 16 tokens of each thread at a time
+  // (their loads are not under a condition: a branch for each would wait for it)
+  constexpr int AT_ONCE = 16;
 #pragma unroll 1
   for (int e0 = 0; e0 < wanted_groups * 32; e0 += kPick * AT_ONCE) {
     T v[AT_ONCE];
@@ -878,16 +885,16 @@ __device__ __forceinline__ int candidates(const SampleArgs& a, int64_t row, cons
     for (int i = 0; i < AT_ONCE; ++i) {
       const int e = e0 + i * kPick + (int)threadIdx.x, r = e & 31;
       // tokens q * 512 + lane * 8 + j of the segment, q < 4 and j < 8
-      c[i] = a.V;
-      if (e < wanted_groups * 32) {
-        const int id = l.groups[e >> 5];
-        c[i] = (id >> 6) * kSeg + (r >> 3) * 512 + (id & 63) * 8 + (r & 7);
-      }
-      v[i] = c[i] < a.V ? x[c[i]] : (T)kNone;
+      const int id = l.groups[min(e >> 5, wanted_groups - 1)];
+      c[i] = (id >> 6) * kSeg + (r >> 3) * 512 + (id & 63) * 8 + (r & 7);
+      v[i] = x[min(c[i], a.V - 1)];
     }
     unsigned take = 0;
 #pragma unroll
-    for (int i = 0; i < AT_ONCE; ++i) take |= wanted((float)v[i] + 0.f) ? 1u << i : 0u;
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const bool in = e0 + i * kPick + (int)threadIdx.x < wanted_groups * 32 && c[i] < a.V;
+      take |= in && wanted((float)v[i] + 0.f) ? 1u << i : 0u;
+    }
     int at = slots(take, &l.count);
 #pragma unroll
     for (int i = 0; i < AT_ONCE; ++i)
@@ -920,11 +927,17 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
   double s[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    const int i = 2 * threadIdx.x + j;
-    m[j] = i < a.segs ? a.seg_max[row * a.segs + i] : kNone;
-    s[j] = i < a.segs ? a.seg_sum[row * a.segs + i] : 0.0;
-    if (FILTERED && i < a.segs) low = fminf(low, a.seg_min[row * a.segs + i]);
+    const int64_t i = row * a.segs + min(2 * (int)threadIdx.x + j, a.segs - 1);
+    m[j] = a.seg_max[i];
+    s[j] = a.seg_sum[i];
+    if (FILTERED) low = fminf(low, a.seg_min[i]);
   }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (2 * (int)threadIdx.x + j >= a.segs) {
+      m[j] = kNone;
+      s[j] = 0.0;
+    }
   const double u = fmin(fmax((double)a.u[row], 0.0), 1.0);
   RowState st;
   st.r = row_params(a, row);
