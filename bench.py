@@ -48,13 +48,16 @@ PROFILES = os.path.join(ROOT, "profiles")
 COPY_BYTES = 1 << 30      # calibration copy for the HBM byte counters
 
 
+LOSS_SOURCES = ("api.hpp", "grpo_api.hip", "kernels.hip", "kernels.hpp", "tile_mma.hpp",
+                "timing.hip", "timing.hpp")
+
+
 def kernel_source_hash():
-    """sha256 of the HIP sources: a traffic measurement is valid only for these."""
+    """sha256 of the loss's HIP sources: a traffic measurement is valid only for these."""
     h = hashlib.sha256()
-    for name in sorted(os.listdir(CSRC)):
-        if name.endswith((".hip", ".hpp")):
-            with open(os.path.join(CSRC, name), "rb") as f:
-                h.update(name.encode() + b"\0" + f.read())
+    for name in LOSS_SOURCES:
+        with open(os.path.join(CSRC, name), "rb") as f:
+            h.update(name.encode() + b"\0" + f.read())
     return h.hexdigest()[:16]
 
 

@@ -59,6 +59,7 @@ class _GrpoNorm(torch.autograd.Function):
         Y, mean, rstd = grpo_norm_fwd(X, weight, bias, eps, kind)
         ctx.save_for_backward(X, weight, rstd, *([mean] if kind == NORM_LAYER else []))
         ctx.kind = kind
+        ctx.shapes = weight.shape, None if bias is None else bias.shape
         return Y
 
     @staticmethod
@@ -69,8 +70,9 @@ class _GrpoNorm(torch.autograd.Function):
         # an upstream gradient may be a broadcast view (that of a sum is)
         dX, dw, db = grpo_norm_bwd(dY.contiguous(), X, weight, mean[0] if mean else None, rstd,
                                    ctx.kind, bias=need_b)
-        return (dX if need_x else None, dw.to(weight.dtype) if need_w else None,
-                db.to(weight.dtype) if need_b else None, None, None)
+        w_shape, b_shape = ctx.shapes
+        return (dX if need_x else None, dw.to(weight.dtype).view(w_shape) if need_w else None,
+                db.to(weight.dtype).view(b_shape) if need_b else None, None, None)
 
 
 def grpo_norm(X, weight, bias=None, eps: float = 1e-5, kind: int = NORM_RMS):

@@ -248,6 +248,10 @@ __device__ __forceinline__ void step_chunk(const grpo_adamw_tensor& t, int64_t b
       bits_m = wave_max(bits_m);
       bits_v = wave_max(bits_v);
       const bool bad_m = bits_m >= 0x7f800000u, bad_v = bits_v >= 0x7f800000u;
+      if (bad_m)
+        for (int j = 0; j < 4; ++j) dm[j] = nm[j] = 0.f;
+      if (bad_v)
+        for (int j = 0; j < 4; ++j) dv[j] = nv[j] = 0.f;
       const float top_m = __uint_as_float(bits_m), top_v = __uint_as_float(bits_v);
       const double to_m = bad_m || bits_m == 0 ? 0.0 : 16129.0 * reciprocal((double)top_m);
       const double to_v = bad_v || bits_v == 0 ? 0.0 : 4228250625.0 * reciprocal((double)top_v);
@@ -280,8 +284,6 @@ __device__ __forceinline__ void step_chunk(const grpo_adamw_tensor& t, int64_t b
         om[j] = (int8_t)(int)__builtin_copysignf(cm[j], nm[j]);
         ov[j] = (uint8_t)max((unsigned)cv[j], qv[j] > 0.0 ? 1u : 0u);
       }
-      if (bad_m) om = typename Vec4<int8_t>::type{};
-      if (bad_v) ov = typename Vec4<uint8_t>::type{};
       store4<FULL>((int8_t*)t.exp_avg + base, e, n, om);
       store4<FULL>((uint8_t*)t.exp_avg_sq + base, e, n, ov);
       if ((threadIdx.x & 63) == 0 && (FULL || e < n)) {
@@ -498,6 +500,8 @@ int grpo_adamw(const void* image, const void* plan, const grpo_adamw_opts* opts,
     return fail(GRPO_ERR_INVALID_ARG, "step %lld: the first step is 1", (long long)o.step);
   if (hd.chunks == 0) return GRPO_OK;
   GRPO_CHECK_PTR(plan);
+  if ((uintptr_t)plan % 8 != 0)
+    return fail(GRPO_ERR_INVALID_ARG, "the plan's device copy is not 8-byte aligned");
   grpo::Hyper h{};
   h.b1 = o.beta1;
   h.b2 = o.beta2;

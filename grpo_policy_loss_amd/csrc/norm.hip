@@ -409,9 +409,10 @@ template <typename T> RowShape row_shape(int64_t n, bool backward) {
 
 // Blocks of the backward, each of which leaves one partial row: as many as keep the loads
 // going, but no more, since partial rows are written and read again (and the sums of a bias
-// take registers: with three blocks a CU, 32768 x 2048 took 89 us, with two 77).
-int64_t bwd_blocks(int64_t rows, RowShape sh, bool bias) {
-  if (sh.lpr == 0) return std::min<int64_t>(rows, 64);
+// take registers: with three blocks a CU, 32768 x 2048 took 89 us, with two 77).  Long rows: as
+// many as make 64 MB at most.
+int64_t bwd_blocks(int64_t rows, int64_t n, RowShape sh, bool bias) {
+  if (sh.lpr == 0) return std::min<int64_t>(rows, std::max<int64_t>(1, std::min<int64_t>(64, (1 << 24) / n)));
   const int64_t rpb = sh.lpr >= 256 ? std::max(1, 512 / sh.lpr) : 256 / sh.lpr;
   const int64_t most = sh.nv == 4 ? 1 : sh.lpr == 256 && sh.nv == 1 ? (bias ? 2 : 3) : sh.lpr >= 256 ? 2 : 4;
   return std::min<int64_t>((rows + rpb - 1) / rpb, most * kCUs);
@@ -444,7 +445,7 @@ hipError_t launch_norm_bwd(const T* dY, const T* X, const T* w, const float* mea
                            float* part_b, hipStream_t s) {
   ScopedKernelTimer t(KK_NORM_BWD, s);
   const RowShape sh = row_shape<T>(n, true);
-  const unsigned grid = (unsigned)bwd_blocks(rows, sh, part_b != nullptr);
+  const unsigned grid = (unsigned)bwd_blocks(rows, n, sh, part_b != nullptr);
 #define GRPO_CASE(L, N)                                                                         \
   if (sh.lpr == L && sh.nv == N) {                                                              \
     if (part_b != nullptr)                                                                      \
@@ -494,7 +495,7 @@ int check_norm(int64_t rows, int64_t cols, int dtype, int kind) {
 
 // The number of partial rows for either type (their vectors differ, so their lanes do).
 int64_t partial_rows(int64_t rows, int64_t cols, int dtype, bool bias) {
-  return bwd_blocks(rows, dtype == GRPO_F32 ? row_shape<float>(cols, true) : row_shape<__bf16>(cols, true),
+  return bwd_blocks(rows, cols, dtype == GRPO_F32 ? row_shape<float>(cols, true) : row_shape<__bf16>(cols, true),
                     bias);
 }
 
@@ -556,6 +557,8 @@ int grpo_norm_bwd(const void* dY, const void* X, const void* weight, const float
   if (workspace == nullptr || workspace_bytes < need)
     return fail(GRPO_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
                 workspace == nullptr ? (size_t)0 : workspace_bytes);
+  if ((uintptr_t)workspace % grpo::kAlign != 0)
+    return fail(GRPO_ERR_WORKSPACE, "workspace is not 256-byte aligned");
   hipStream_t s = (hipStream_t)stream;
   float* part_w = (float*)workspace;
   float* part_b = dbias == nullptr ? nullptr : (float*)((char*)workspace + need / 2);

@@ -1210,6 +1210,8 @@ int grpo_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row
   if (workspace == nullptr || workspace_bytes < p.total)
     return fail(GRPO_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", p.total,
                 workspace == nullptr ? (size_t)0 : workspace_bytes);
+  if ((uintptr_t)workspace % grpo::kAlign != 0)
+    return fail(GRPO_ERR_WORKSPACE, "workspace is not 256-byte aligned");
   char* ws = (char*)workspace;
   hipStream_t s = (hipStream_t)stream;
   for (int64_t b = 0; b < B; b += p.rows) {

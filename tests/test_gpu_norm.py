@@ -188,6 +188,9 @@ def test_autograd_takes_broadcast_gradients_and_skips_what_is_not_needed():
     assert torch.equal(x.grad, dx) and torch.equal(w.grad, dw.bfloat16())
     y = gp.grpo_norm(i["x"], w.detach().requires_grad_(), i["b"], EPS, gp.NORM_LAYER)
     y.backward(i["dy"])
+    w2 = i["w"].clone().view(1, -1).requires_grad_()     # a weight of another shape
+    gp.grpo_norm(i["x"], w2, None, EPS).backward(i["dy"])
+    assert w2.grad.shape == (1, 513)
     x = i["x"].clone().requires_grad_()
     gp.grpo_norm(x.t().contiguous().t().contiguous(), i["w"], None, EPS).backward(i["dy"].t().contiguous().t())
     assert x.grad.isfinite().all()

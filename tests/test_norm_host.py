@@ -43,7 +43,7 @@ def test_forward_argument_errors(kw, code):
 @pytest.mark.parametrize("kw,code", [
     ({"dY": None}, -1), ({"X": None}, -1), ({"w": None}, -1), ({"mean": None}, -1),
     ({"rstd": None}, -1), ({"dX": None}, -1), ({"dw": None}, -1), ({"rows": -3}, -1),
-    ({"dt": 7}, -1), ({"kind": -1}, -1), ({"acc": 2}, -1), ({"ws": None}, -2), ({"wsb": 16}, -2),
+    ({"dt": 7}, -1), ({"kind": -1}, -1), ({"acc": 2}, -1), ({"ws": None}, -2), ({"wsb": 16}, -2), ({"ws": ctypes.c_void_p(0x1010)}, -2),
     ({"cols": 1 << 25}, -3)])
 def test_backward_argument_errors(kw, code):
     assert bwd(**kw) == code
@@ -60,6 +60,9 @@ def test_workspace_is_bounded():
                 ws = L.grpo_norm_workspace_bytes(rows, cols, dt)
                 # at most 1024 partial rows of dw and of db, and no more than there are rows
                 assert 8 * cols <= ws <= 8 * cols * min(rows, 1024) + 512
+        # long rows: 128 MB at most, or one partial row of each
+        assert L.grpo_norm_workspace_bytes(1 << 20, 1 << 20, dt) <= 1 << 27
+        assert L.grpo_norm_workspace_bytes(1 << 20, 1 << 24, dt) == 1 << 27
 
 
 def _args(t=torch.bfloat16):

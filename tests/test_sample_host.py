@@ -28,7 +28,7 @@ def call(opts=None, **kw):
     ({"logits": None}, -1), ({"u": None}, -1), ({"token": None}, -1), ({"lp": None}, -1),
     ({"dt": 2}, -1), ({"B": 0}, -1), ({"V": 0}, -1), ({"stride": 99}, -1),
     ({"V": (1 << 20) + 1, "stride": 1 << 21}, -3), ({"B": (1 << 20) + 1}, -3),
-    ({"ws": None}, -2), ({"wsb": 8}, -2)])
+    ({"ws": None}, -2), ({"wsb": 8}, -2), ({"ws": ctypes.c_void_p(0x1008)}, -2)])
 def test_argument_errors(kw, code):
     assert call(**kw) == code
     assert L.grpo_last_error()
