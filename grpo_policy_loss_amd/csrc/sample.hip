@@ -55,7 +55,9 @@ constexpr float kNone = -__builtin_huge_valf();
 // masses among the listed tokens those among all that matter: see k_sample_cut.
 struct RowCut {
   int sure, lo, hi, kbin;
-  int k, pad;
+  int k;                 // 0: no k, or fewer tokens than k
+  float top, low;        // the row's range; NaN: nothing to draw from
+  int pad;
   uint64_t count_off, mass_off, z_off;
 };
 
@@ -113,22 +115,22 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row
 }
 
 // 2^t for t <= 0: t = n + f with n whole and |f| <= 1/2, and 2^f by its interpolation at the
-// Chebyshev points of degree 10 (relative error below 5e-16).  Below 2^-1000 it stays at
-// 2^-1000: nothing beside the row's maximum, whose weight is 1.
+// Chebyshev points of degree 9 (relative error below 2e-14: with 10^5 borders in a row, one row in
+// 10^8 has u that near one).  Below 2^-1000 it stays at 2^-1000: nothing beside the row's maximum,
+// whose weight is 1.
 __device__ __forceinline__ double pow2_down(double t) {
   t = fmax(t, -1000.0);
   const double magic = 0x1.8p52, shifted = t + magic;
   const double f = t - (shifted - magic);
-  double q = 0x1.e6063f7217bc6p-28;
-  q = fma(q, f, 0x1.b675bca4eeebbp-24);
-  q = fma(q, f, 0x1.62bfd47773353p-20);
-  q = fma(q, f, 0x1.ffcb54062e698p-17);
-  q = fma(q, f, 0x1.430913096fd9fp-13);
-  q = fma(q, f, 0x1.5d87fe9d7a584p-10);
-  q = fma(q, f, 0x1.3b2ab6fba1ddap-7);
-  q = fma(q, f, 0x1.c6b08d703ce49p-5);
-  q = fma(q, f, 0x1.ebfbdff82c598p-3);
-  q = fma(q, f, 0x1.62e42fefa3a19p-1);
+  double q = 0x1.b6571de2f2351p-24;
+  q = fma(q, f, 0x1.63ef969a64d3cp-20);
+  q = fma(q, f, 0x1.ffcb76789860fp-17);
+  q = fma(q, f, 0x1.43088e257f341p-13);
+  q = fma(q, f, 0x1.5d87fe908f88ap-10);
+  q = fma(q, f, 0x1.3b2ab72b175eep-7);
+  q = fma(q, f, 0x1.c6b08d7044119p-5);
+  q = fma(q, f, 0x1.ebfbdff8149f2p-3);
+  q = fma(q, f, 0x1.62e42fefa39f7p-1);
   q = fma(q, f, 1.0);
   // n into the exponent: q is in [0.7, 1.5] and n at least -1000
   const int n = (int)(uint32_t)__double_as_longlong(shifted);
@@ -198,9 +200,9 @@ template <typename V> __device__ __forceinline__ V wave_before(V v, V& total) {
 }
 
 // ---------------------------------------------------------------- maxima and sums
-// One wave per segment of one row; the next segment's loads are under way while this one's
-// weights are summed.  About 20 float64 instructions a token are as many as the loads leave
-// time for.
+// One wave per segment of one row: 28 instructions a token, most of them float64, against
+// 4 bytes: 256 x 128256 in float32 take 34 us, of which the loads alone need 27.  (Waves that walk
+// over segments and load the next one ahead took 37: more of them at once hide more.)
 template <typename T> struct RawSeg {
   Raw8<T> q[4];
 };
@@ -214,20 +216,15 @@ __device__ __forceinline__ RawSeg<T> load_seg(const SampleArgs& a, int64_t row, 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256, 4) k_sample_mass(SampleArgs a, int64_t waves) {
+__global__ void __launch_bounds__(256) k_sample_mass(SampleArgs a, int64_t waves) {
   const int lane = threadIdx.x & 63;
-  int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (w >= waves) return;
-  const int64_t step = (int64_t)gridDim.x * 4;
-  RawSeg<T> next = load_seg<T>(a, w / a.segs, (int)(w % a.segs));
-  for (;;) {
+  for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); w < waves; w += (int64_t)gridDim.x * 4) {
+    const RawSeg<T> raw = load_seg<T>(a, w / a.segs, (int)(w % a.segs));
     float x[4][8];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[q][j] = (float)next.q[q].v[j / kVec<T>][j % kVec<T>];
-    const bool more = w + step < waves;
-    if (more) next = load_seg<T>(a, (w + step) / a.segs, (int)((w + step) % a.segs));
+      for (int j = 0; j < 8; ++j) x[q][j] = (float)raw.q[q].v[j / kVec<T>][j % kVec<T>];
     const RowParams r = row_params(a, w / a.segs);
     float m = x[0][0], low;
     bool nan = false;
@@ -264,8 +261,6 @@ __global__ void __launch_bounds__(256, 4) k_sample_mass(SampleArgs a, int64_t wa
       a.seg_sum[w] = s;
       if (w % a.segs == 0) a.listed[w / a.segs * kLine] = 0;
     }
-    if (!more) return;
-    w += step;
   }
 }
 
@@ -453,7 +448,11 @@ __global__ void __launch_bounds__(kHistThreads) k_sample_cut(SampleArgs a) {
   __shared__ RowCut rc;
   __shared__ uint64_t above_k, with_k;
   const bool counted = st.r.k != 0;
-  if (!drawable(row_range<NT>(a, row, range), st.r)) return;
+  const RowRange g = row_range<NT>(a, row, range);
+  if (!drawable(g, st.r)) {
+    if (threadIdx.x == 0) a.cut[row].top = __builtin_nanf("");
+    return;
+  }
   // thread t holds bins PER t ..
   uint64_t h[PER], own = 0, whole;
   uint32_t n[PER], own_n = 0;
@@ -492,7 +491,7 @@ __global__ void __launch_bounds__(kHistThreads) k_sample_cut(SampleArgs a) {
     own += h[j];
     own_n += n[j];
   }
-  if (threadIdx.x == 0) rc = RowCut{0, 1, 0, -1, 0, 0, 0, 0, 0};
+  if (threadIdx.x == 0) rc = RowCut{0, 1, 0, -1, 0, g.top, g.low, 0, 0, 0, 0};
   const uint64_t first = block_before<NT, uint64_t>(own, sums, whole);
   uint64_t n_all, n_run = 0, k = (uint64_t)st.r.k;
   if (counted) {
@@ -563,10 +562,11 @@ __global__ void __launch_bounds__(256) k_sample_gather(SampleArgs a) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int seg = min(a.segs - 1, (int)blockIdx.x * 4 + wave);
   const float top = a.seg_max[row * a.segs + seg];
-  RowCut rc{INT32_MAX, 1, 0, -1, 0, 0, 0, 0, 0};
+  RowCut rc{INT32_MAX, 1, 0, -1, 0, 0.f, 0.f, 0, 0, 0, 0};
   if (st.r.cls == HIST) rc = a.cut[row];
   const RawSeg<T> raw = load_seg<T>(a, row, seg);       // on its way while the row's range is found
-  const RowRange g = row_range<256>(a, row, range);
+  RowRange g{rc.top, rc.low, rc.top != rc.top};
+  if (st.r.cls == MIN_P) g = row_range<256>(a, row, range);
   if (!drawable(g, st.r)) return;
   st.max = g.top;
   const int bins = hist_bins_for(a.V);
@@ -973,7 +973,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
         l.segs[i] = sure && i < a.segs ? a.seg_kept[row * a.segs + i] : 0;
       }
       if (st.r.cls != MIN_P) {
-        RowCut rc{0, 0, 0, 0, st.r.k, 0, 0, 0, 0};
+        RowCut rc{0, 0, 0, 0, st.r.k, 0.f, 0.f, 0, 0, 0, 0};
         int n;
         if (st.r.cls == LIST) {
           n = candidates<T>(a, row, x, st, g.low, l);
@@ -1004,7 +1004,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
                 if (v[j] > kNone) f(place(v[j], c + j));
             }
           };
-          cut = last_kept(all, INT32_MAX, RowCut{0, 0, 0, 0, st.r.k, 0, 0, 0, 0}, st, l);
+          cut = last_kept(all, INT32_MAX, RowCut{0, 0, 0, 0, st.r.k, 0.f, 0.f, 0, 0, 0, 0}, st, l);
           __syncthreads();
 #pragma unroll
           for (int j = 0; j < 2; ++j) l.segs[2 * threadIdx.x + j] = 0;
@@ -1145,7 +1145,7 @@ hipError_t launch_sample(const SampleArgs& a, int64_t rows, hipStream_t s) {
   {
     ScopedKernelTimer t(KK_SAMPLE_MASS, s);
     const int64_t waves = rows * a.segs;
-    const int64_t blocks = std::min<int64_t>((waves + 3) / 4, 4 * kCUs);
+    const int64_t blocks = std::min<int64_t>((waves + 3) / 4, 1 << 20);
     k_sample_mass<T><<<(unsigned)blocks, 256, 0, s>>>(a, waves);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
