@@ -910,7 +910,7 @@ __device__ __forceinline__ int candidates(const SampleArgs& a, int64_t row, cons
 // One block of 256 threads per row: what is kept (not for PLAIN), then where the running mass
 // first exceeds u times the kept mass, by segments and in the segment.  Its time is that of a
 // chain of loads and barriers, so it has few waves; a kernel of its own serves calls without
-// filters (4.7 us against 16).
+// filters (4.9 us for a row of 151936 tokens; with top-k 50 and top-p 16).
 template <typename T, bool FILTERED>
 __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
   struct Small {
