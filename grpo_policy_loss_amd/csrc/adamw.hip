@@ -15,8 +15,8 @@
 //
 // With float32 moments the step is bound by memory: 20 to 30 bytes an element against some 20
 // instructions (233M bf16 weights with masters: 1.09 ms, 6.4 TB/s).  With 8-bit moments 10 bytes
-// stand against some 60, and both count (67M bf16 weights: 158 us, 4.3 TB/s; 316 us with every
-// code decided in float64).  One block takes a chunk of 4096 elements of one tensor, 4 elements a
+// stand against some 65, and both count (67M bf16 weights: some 160 us, 4.2 TB/s; 316 us with every
+// code decided in float64).  One block takes a chunk of 2048 elements of one tensor, 4 elements a
 // lane and load, all loads of the chunk issued before its first use.
 #include <math.h>
 #include <string.h>
@@ -32,7 +32,7 @@
 namespace grpo {
 namespace {
 
-constexpr int kChunk = 4096;        // elements per block of 256 threads
+constexpr int kChunk = 2048;        // elements per block of 256 threads
 constexpr int kSteps = kChunk / 1024;
 constexpr int kQuantBlock = 256;    // elements per scale: one wave's load
 
@@ -146,10 +146,26 @@ __device__ __forceinline__ double reciprocal(double a) {
 
 constexpr double kUnitM = 1.0 / 16129.0, kUnitV = 1.0 / 4228250625.0;   // 127^-2, 255^-4
 
-__device__ __forceinline__ double square_m(int c) { return (double)(c * abs(c)); }
-__device__ __forceinline__ double fourth_v(unsigned c) {
+// What a code stands for.  The last codes, 127 and 255, stand for a itself: their products with
+// the constants round to 1.
+__device__ __forceinline__ double value_m(int c, double a) {
+  return (double)(c * abs(c)) * kUnitM * a;
+}
+__device__ __forceinline__ double value_v(unsigned c, double a) {
   const double s = (double)(c * c);
-  return s * s;
+  return s * s * kUnitV * a;
+}
+
+// The moments after the step in float64, each product and sum rounded (none fused): a block's
+// largest one is often a former a, and b1 a + (1 - b1) g then often lies just between two float32
+// scales (one block in ten of those with b1 = 0.9), where the last bit of float64 decides.
+__device__ __forceinline__ double next_m(double m, double x, double b1) {
+#pragma clang fp contract(off)
+  return m * b1 + x * (1.0 - b1);
+}
+__device__ __forceinline__ double next_v(double v, double x, double b2) {
+#pragma clang fp contract(off)
+  return v * b2 + x * x * (1.0 - b2);
 }
 
 // What is the same for every element.
@@ -213,12 +229,11 @@ __device__ __forceinline__ void step_chunk(const grpo_adamw_tensor& t, int64_t b
       }
     } else {
       // float64, so that the new codes are those of the exact moments
-      const double um = (double)ma[k] * (kUnitM * h.b1), uv = (double)va[k] * (kUnitV * h.b2);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const double x = (double)(float)g[k][j] * (double)f.scale;
-        dm[j] = fma(square_m(mc[k][j]), um, x * (1.0 - h.b1));
-        dv[j] = fma(fourth_v(vc[k][j]), uv, x * x * (1.0 - h.b2));
+        dm[j] = next_m(value_m(mc[k][j], (double)ma[k]), x, h.b1);
+        dv[j] = next_v(value_v(vc[k][j], (double)va[k]), x, h.b2);
         nm[j] = (float)dm[j];
         nv[j] = (float)dv[j];
       }
@@ -331,7 +346,7 @@ __global__ void __launch_bounds__(256)
   else step_chunk<P, G, BITS, MASTER, false>(t, base, h, f);
 }
 
-// The float32 values of 8-bit moments: a block takes 4096 of them.
+// The float32 values of 8-bit moments: a block takes 2048 of them.
 template <typename C>
 __global__ void __launch_bounds__(256)
     k_moment_values(const C* __restrict__ codes, const float* __restrict__ scales, int64_t n,
@@ -351,8 +366,8 @@ __global__ void __launch_bounds__(256)
     typename Vec4<float>::type o;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      o[j] = (C)-1 < (C)0 ? (float)(square_m((int)c[k][j]) * ((double)a[k] * kUnitM))
-                          : (float)(fourth_v((unsigned)c[k][j]) * ((double)a[k] * kUnitV));
+      o[j] = (C)-1 < (C)0 ? (float)value_m((int)c[k][j], (double)a[k])
+                          : (float)value_v((unsigned)c[k][j], (double)a[k]);
     store4<false>(out + base, (k * 256 + (int)threadIdx.x) * 4, left, o);
   }
 }

@@ -370,7 +370,8 @@ int grpo_norm_bwd(const void* dY, const void* X, const void* weight, const float
  *   both to every grpo_adamw: image is read on the host during the call, plan
  *   (the device copy) by the kernel.  Both hold the tensors' addresses: a tensor that
  *   moves needs a new plan.  Tensors that share memory (one twice) are
- *   refused; n = 0 is allowed.
+ *   refused; n = 0 is allowed.  At most 2^24 tensors, and 2^24 - 1 chunks of
+ *   2048 elements (3.4e10 elements).
  *   param_dtype, grad_dtype: GRPO_F32 or GRPO_BF16, the same for all tensors;
  *   a master goes with bfloat16 parameters only.
  *   state_bits 32: exp_avg and exp_avg_sq are float32 [n] (scales unused).
@@ -381,8 +382,8 @@ int grpo_norm_bwd(const void* dY, const void* X, const void* weight, const float
  *     exp_avg_sq = (c / 255)^4 a,          c rounded from 255 (v / a)^(1/4),
  *                                          at least 1 where v > 0
  *   All zeros is the state before the first step.  The new codes are those of
- *   the moments in float64; the weights use the moments before their rounding to
- *   codes.
+ *   the moments in float64, beta m + (1 - beta) g with each product and sum
+ *   rounded; the weights use the moments before their rounding to codes.
  * grpo_adamw: betas in [0, 1); lr, eps and weight_decay finite and >= 0; step
  *   the number of this step, from 1.  Device-side values, each read when the
  *   kernel runs if non-NULL (for a step under graph capture): step_dev [1] int64

@@ -124,6 +124,29 @@ def test_first_step_from_zero_moments(bits):
     assert all(x.isfinite().all() for x in p)
 
 
+@pytest.mark.parametrize("betas", [(0.9, 0.999), (0.9, 0.95), (0.95, 0.98)])
+def test_scales_that_lie_between_two_float32_values(betas):
+    """Bfloat16 gradients and old moments at their blocks' scales: the new scale is often an exact
+    tie of float32, which the last bit of the float64 sum decides.  Scales and codes are those
+    of the formula's own order of operations, bit for bit, step after step."""
+    n = 1 << 20
+    gen = torch.Generator().manual_seed(2)
+    p = [torch.randn(n, generator=gen).cuda()]
+    g = [(1e-3 * torch.randn(n, generator=gen)).bfloat16().cuda()]
+    m, v = gp.adamw_moments(p, 8)
+    hyper = dict(lr=1e-4, betas=betas, eps=1e-8, weight_decay=0.0)
+    plan = gp.adamw_plan(p, g, m, v)
+    for step in (1, 2, 3, 4):
+        g[0].mul_(torch.randn(n, generator=gen).cuda().sign())
+        before = [plain_ops.moment_values(q.codes.cpu(), q.scales.cpu()) for q in (m[0], v[0])]
+        gp.grpo_adamw(plan, step, **hyper)
+        x = g[0].cpu().double()
+        for q, old, new, b in ((m[0], before[0], x, betas[0]), (v[0], before[1], x * x, betas[1])):
+            codes, scales = plain_ops.moment_codes(old * b + new * (1 - b), q.codes.dtype == torch.uint8)
+            assert torch.equal(q.scales.cpu(), scales)
+            assert torch.equal(q.codes.cpu(), codes)
+
+
 def test_values_that_are_not_finite_stay_where_they_are():
     for bits in (32, 8):
         s = make([2000], torch.float32, torch.float32, False, bits, False)
