@@ -10,14 +10,16 @@
 //   v = (c / 255)^4 a,          c = floor(255 (v / a)^(1/4) + 1/2), at least 1 where v > 0
 // The powers spend the codes on the small values of a block: m spans 16129 : 1 and sqrt(v),
 // which is what divides, 65025 : 1.  A positive v never reads back as 0, so the quotient
-// never sees a zero under a live m (unless a is below float32's range).  A block with a value that is not finite has the scale
-// NaN, so all of it reads back as NaN.
+// never sees a zero under a live m (unless a is below float32's range).  A block with a value
+// that is not finite has the scale NaN, so all of it reads back as NaN.
 //
 // With float32 moments the step is bound by memory: 20 to 30 bytes an element against some 20
 // instructions (233M bf16 weights with masters: 1.09 ms, 6.4 TB/s).  With 8-bit moments 10 bytes
-// stand against some 65, and both count (67M bf16 weights: some 160 us, 4.2 TB/s; 316 us with every
-// code decided in float64).  One block takes a chunk of 2048 elements of one tensor, 4 elements a
-// lane and load, all loads of the chunk issued before its first use.
+// stand against some 80, a third of them in float64, and both count (67M bf16 weights: 175 us,
+// 3.8 TB/s; 245 us with the definition of the codes worked out in every wave that has a root near a
+// border).  One block takes a chunk of 2048 elements of one tensor, 4 elements a lane and load, all
+// loads of the chunk issued before its first use.  Chunks of 4096 make the large steps 1 to 3 %
+// faster and 160 small tensors 11 % slower (10.1 against 11.2 us).
 #include <math.h>
 #include <string.h>
 
@@ -74,12 +76,12 @@ template <> struct Vec4<uint8_t> {
 // faster with the caches' help (8-bit step 294 us against 279).
 template <bool FULL, typename T>
 __device__ __forceinline__ typename Vec4<T>::type load4(const T* p, int e, int n) {
-  typedef typename Vec4<T>::type V;
+  typedef const __attribute__((address_space(1))) typename Vec4<T>::type V;
   if (FULL || e + 4 <= n) {
-    if constexpr (sizeof(T) == 4) return __builtin_nontemporal_load((const V*)(p + e));
-    else return *(const V*)(p + e);
+    if constexpr (sizeof(T) == 4) return __builtin_nontemporal_load((V*)(p + e));
+    else return *(V*)(p + e);
   }
-  V v = {};
+  typename Vec4<T>::type v = {};
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (e + j < n) v[j] = p[e + j];
@@ -87,7 +89,7 @@ __device__ __forceinline__ typename Vec4<T>::type load4(const T* p, int e, int n
 }
 template <bool FULL, typename T>
 __device__ __forceinline__ void store4(T* p, int e, int n, typename Vec4<T>::type v) {
-  typedef typename Vec4<T>::type V;
+  typedef __attribute__((address_space(1))) typename Vec4<T>::type V;
   if (FULL || e + 4 <= n) {
     __builtin_nontemporal_store(v, (V*)(p + e));
     return;
@@ -126,15 +128,25 @@ __device__ __forceinline__ int owner_of(const int64_t* __restrict__ first, int c
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// The codes of a value q = (|m| / a) 127^2 or (v / a) 255^4, exactly: the candidate c from float32
-// roots, moved to the side of the borders (c -+ 1/2)^k that the float64 q is on.
-__device__ __forceinline__ float exact_m(float c, double q) {
-  const double up = (double)c + 0.5, dn = (double)c - 0.5;
-  return fminf(c + (q >= up * up ? 1.f : 0.f) - (c > 0.f && q < dn * dn ? 1.f : 0.f), 127.f);
+// The codes from their definition, each operation rounded to float64 (none fused).
+__device__ __forceinline__ float exact_m(double m, double a) {
+#pragma clang fp contract(off)
+  return fminf((float)floor(127.0 * sqrt(m / a) + 0.5), 127.f);
 }
-__device__ __forceinline__ float exact_v(float c, double q) {
-  const double up = ((double)c + 0.5) * ((double)c + 0.5), dn = ((double)c - 0.5) * ((double)c - 0.5);
-  return fminf(c + (q >= up * up ? 1.f : 0.f) - (c > 0.f && q < dn * dn ? 1.f : 0.f), 255.f);
+__device__ __forceinline__ float exact_v(double v, double a) {
+#pragma clang fp contract(off)
+  return fminf((float)floor(255.0 * sqrt(sqrt(v / a)) + 0.5), 255.f);
+}
+
+// The side of the nearer border b = c -+ 1/2 that the root r (of q, to 4 10^-5) is on, from
+// q >= b^POWER in float64.  Within 10^-13 of it the definition's own roundings decide: `tie`.
+template <int POWER>
+__device__ __forceinline__ float side(float r, float c, double q, bool& tie) {
+  const double b = (double)(r < c ? c - 0.5f : c + 0.5f);
+  double t = b * b;
+  if (POWER == 4) t *= t;
+  tie |= fabs(q - t) <= 1e-13 * t;
+  return (float)(q >= t ? b + 0.5 : b - 0.5);
 }
 
 // 1 / a to about 2^-52: the hardware's start and two Newton steps.
@@ -174,15 +186,17 @@ struct Factors {
   float b1, b2, a1, a2;
 };
 
-// w after the step.  The root and quotient of the hardware are good to a unit in the last place
-// for normal numbers; a smaller root only matters beside an eps that is smaller still.
-template <bool FAST>
-__device__ __forceinline__ float updated(float w, float m, float v, const Factors& f) {
+// m / (sqrt(v / (1 - b2^t)) + eps)
+__device__ __forceinline__ float quotient(float m, float v, const Factors& f) {
+  return m / (sqrtf(v * f.inv_bc2) + f.eps);
+}
+
+// The same with the hardware's root and reciprocal, good to a unit in the last place for normal
+// numbers; a smaller root only matters beside an eps that is smaller still: `tiny`.
+__device__ __forceinline__ float quick_quotient(float m, float v, const Factors& f, bool& tiny) {
   const float vh = v * f.inv_bc2;
-  float u;
-  if (FAST && vh >= 1.17549435e-38f) u = m * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(vh) + f.eps);
-  else u = m / (sqrtf(vh) + f.eps);
-  return (w - f.decay * w) - f.step_size * u;
+  tiny |= !(vh >= 1.17549435e-38f);
+  return m * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(vh) + f.eps);
 }
 
 template <typename P, typename G, int BITS, bool MASTER, bool FULL>
@@ -238,6 +252,17 @@ __device__ __forceinline__ void step_chunk(const grpo_adamw_tensor& t, int64_t b
         nv[j] = (float)dv[j];
       }
     }
+    float u[4];
+    bool tiny = BITS == 32;
+    if constexpr (BITS == 8) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = quick_quotient(nm[j], nv[j], f, tiny);
+    }
+    if (tiny) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (BITS == 32 || !(nv[j] * f.inv_bc2 >= 1.17549435e-38f)) u[j] = quotient(nm[j], nv[j], f);
+    }
     typename Vec4<P>::type np;
     typename Vec4<float>::type nw;
 #pragma unroll
@@ -245,7 +270,7 @@ __device__ __forceinline__ void step_chunk(const grpo_adamw_tensor& t, int64_t b
       float old;
       if constexpr (MASTER) old = w[k][j];
       else old = (float)p[k][j];
-      nw[j] = updated<BITS == 8>(old, nm[j], nv[j], f);
+      nw[j] = (old - f.decay * old) - f.step_size * u[j];
       np[j] = (P)nw[j];
     }
     store4<FULL>(param, e, n, np);
@@ -272,26 +297,43 @@ __device__ __forceinline__ void step_chunk(const grpo_adamw_tensor& t, int64_t b
       const float top_m = __uint_as_float(bits_m), top_v = __uint_as_float(bits_v);
       const double to_m = bad_m || bits_m == 0 ? 0.0 : 16129.0 * reciprocal((double)top_m);
       const double to_v = bad_v || bits_v == 0 ? 0.0 : 4228250625.0 * reciprocal((double)top_v);
-      float cm[4], cv[4], edge = 0.f;
+      float cm[4], cv[4], rm[4], rv[4], edge = 0.f;
       double qm[4], qv[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         qm[j] = fabs(dm[j]) * to_m;
         qv[j] = dv[j] * to_v;
-        const float rm = __builtin_amdgcn_sqrtf((float)qm[j]);
-        const float rv = __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf((float)qv[j]));
-        cm[j] = rintf(rm);
-        cv[j] = rintf(rv);
-        edge = fmaxf(edge, fmaxf(fabsf(rm - cm[j]), fabsf(rv - cv[j])));
+        rm[j] = __builtin_amdgcn_sqrtf((float)qm[j]);
+        rv[j] = __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf((float)qv[j]));
+        cm[j] = rintf(rm[j]);
+        cv[j] = rintf(rv[j]);
+        edge = fmaxf(edge, fmaxf(fabsf(rm[j] - cm[j]), fabsf(rv[j] - cv[j])));
       }
-      // the roots are off by less than 10^-4, so only those that near a border need float64 (one
-      // step of a wave in ten has one); a scale below the normal numbers may be rounded so far
-      // that a root passes the last code
-      if (edge > 0.4999f || bits_m < 0x800000u || bits_v < 0x800000u) {
+      // the roots are off by less than 4 10^-5 (two square roots of 1 ulp and the narrowing, up to
+      // 255), so only those that near a border c + 1/2 need float64 (one step of a wave in twenty
+      // has one), and only those on it the definition.  Exact halves are not rare: m / a is 1/4 where
+      // the first step meets a gradient of a quarter of its block's largest.  A scale below the
+      // normal numbers may be rounded so far that a root passes the last code.
+      bool tie = bits_m - 1u < 0x7fffffu || bits_v - 1u < 0x7fffffu;   // a tiny scale, not 0
+      if (edge > 0.49995f) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          cm[j] = exact_m(cm[j], qm[j]);
-          cv[j] = exact_v(cv[j], qv[j]);
+          cm[j] = side<2>(rm[j], cm[j], qm[j], tie);
+          cv[j] = side<4>(rv[j], cv[j], qv[j], tie);
+        }
+      }
+      if (tie) {
+#pragma unroll 1   // one copy of the divisions: the kernel stays in the instruction cache
+        for (int i = 0; i < 4; ++i) {
+          double x = dm[0], y = dv[0];
+#pragma unroll
+          for (int j = 1; j < 4; ++j) x = i == j ? dm[j] : x, y = i == j ? dv[j] : y;
+          const float em = exact_m(fabs(x), (double)top_m), ev = exact_v(y, (double)top_v);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (i == j && bits_m != 0 && !bad_m) cm[j] = em;
+            if (i == j && bits_v != 0 && !bad_v) cv[j] = ev;
+          }
         }
       }
       typename Vec4<int8_t>::type om;

@@ -1,6 +1,13 @@
 """The operators around the loss in plain float64 torch on the CPU, from their
 formulas (the tests' oracle for them; nothing here is shared with the library)."""
+import numpy as np
 import torch
+
+
+def _sqrt(x):
+    """Correctly rounded, which torch's own on the CPU is not everywhere (some hosts give 1/2 for the
+    root of the float64 below 1/4)."""
+    return torch.from_numpy(np.sqrt(x.numpy()))
 
 
 def norm_fwd(x, w, b, eps, layer):
@@ -31,11 +38,11 @@ def moment_codes(x, squared):
     bad = ~b.isfinite().all(1)
     q = torch.where((a > 0)[:, None], b.abs() / a.double()[:, None], 0.0)
     if squared:
-        c = (255 * q ** 0.25 + 0.5).floor().clamp(max=255)
+        c = (255 * _sqrt(_sqrt(q)) + 0.5).floor().clamp(max=255)
         c = torch.where(b > 0, c.clamp(min=1), c)
         c = torch.where(a[:, None] == 0, 0.0, c)
     else:
-        c = (127 * q.sqrt() + 0.5).floor().clamp(max=127) * b.sign()
+        c = (127 * _sqrt(q) + 0.5).floor().clamp(max=127) * b.sign()
     c[bad] = 0
     a = torch.where(bad, float("nan"), a)
     return c.flatten()[:n].to(torch.uint8 if squared else torch.int8), a

@@ -127,8 +127,9 @@ def test_first_step_from_zero_moments(bits):
 @pytest.mark.parametrize("betas", [(0.9, 0.999), (0.9, 0.95), (0.95, 0.98)])
 def test_scales_that_lie_between_two_float32_values(betas):
     """Bfloat16 gradients and old moments at their blocks' scales: the new scale is often an exact
-    tie of float32, which the last bit of the float64 sum decides.  Scales and codes are those
-    of the formula's own order of operations, bit for bit, step after step."""
+    tie of float32, which the last bit of the float64 sum decides, and after the first step many
+    moments are a quarter of their block's largest, a root of exactly 63 and a half.  Scales and
+    codes are those of the formula's own order of operations, bit for bit, step after step."""
     n = 1 << 20
     gen = torch.Generator().manual_seed(2)
     p = [torch.randn(n, generator=gen).cuda()]
@@ -161,6 +162,7 @@ def test_values_that_are_not_finite_stay_where_they_are():
                 lost = gp.dequantize_moment(q).isnan()
                 blocks = torch.arange(2000, device="cuda") // 256
                 assert torch.equal(lost, (blocks == 700 // 256) | (blocks == 1500 // 256))
+                assert (q.codes[lost] == 0).all()
 
 
 def test_betas_of_zero_and_no_decay():
