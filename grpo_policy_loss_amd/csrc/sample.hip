@@ -512,6 +512,7 @@ __global__ void __launch_bounds__(kHistThreads) k_sample_cut(SampleArgs a) {
     __syncthreads();
   }
   const int kbin = rc.kbin;                          // -1: no k, or fewer tokens than k
+  if (kbin < 0 && st.r.p == 0.0 && threadIdx.x == 0) rc.sure = BINS;    // then all are kept
   if (st.r.p != 0.0) {
     const double least = st.r.p * (double)(kbin >= 0 ? above_k : whole);
     const double most = st.r.p * (double)(kbin >= 0 ? with_k : whole);
@@ -717,12 +718,14 @@ __device__ __forceinline__ uint64_t search(const Each& each, uint64_t lo, uint64
 }
 
 // The place of the last kept token among n tokens that each(f) goes through, with the offsets of
-// RowCut.  Up to 256 of them (the usual top-k) are compared directly: each thread ranks one.
+// RowCut; 0 for none (a row with fewer tokens than k: no cut).  Up to 256 of them (the usual top-k)
+// are compared directly: each thread ranks one.
 template <typename Each>
 __device__ __forceinline__ uint64_t last_kept(const Each& each, int n, const RowCut& rc, const RowState& st,
                                               Lds& l) {
   const int t = threadIdx.x;
   const uint64_t k = rc.k != 0 ? (uint64_t)rc.k : ~(uint64_t)0;
+  if (n == 0) return 0;
   if (n <= kPick) {
     const uint64_t p = t < n ? l.list[t] : 0, mine = t < n ? units(st.weight(value_at(p))) : 0;
     if (t < n) l.bins[t] = mine;

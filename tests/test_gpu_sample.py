@@ -176,6 +176,19 @@ def test_every_size_of_the_candidates(k, t):
             check(x, u, run(x, u, k=k, p=p), k=k, p=p)
 
 
+@pytest.mark.parametrize("V", [5003, 40000, 270000])
+@pytest.mark.parametrize("params", [dict(k=4000), dict(k=4000, min_p=0.01), dict(k=4000, p=0.9), dict(k=1500), dict(k=2049, T=3.0)], ids=str)
+def test_rows_with_fewer_tokens_than_k(V, params):
+    x, u = logits(5, V)
+    for b, left in enumerate((1, 2, 300, 1400, 2040)):
+        off = torch.ones(V, dtype=torch.bool)
+        off[torch.randperm(V, generator=torch.Generator().manual_seed(b))[:left]] = False
+        x[b, off] = float("-inf")
+    check(x, u, run(x, u, **params), **params)
+    rows = dict(params, k=torch.full((5,), params["k"], dtype=torch.int32))
+    check(x, u, run(x, u, **rows), **rows)
+
+
 @pytest.mark.parametrize("p", [0.01, 0.5, 0.9, 0.9999999])
 @pytest.mark.parametrize("scale", [0.0, 0.01, 1.0, 8.0])
 def test_nucleus_of_flat_and_peaked_rows(scale, p):
