@@ -289,7 +289,8 @@ def grpo_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=N
             numbers.append(0)
             arrays.append(x.data_ptr())
         else:
-            numbers.append(x)
+            # ctypes drops what does not fit 32 bits
+            numbers.append(min(max(x, -1), 2**31 - 1) if name == "top_k" else x)
             arrays.append(None)
     opts = SampleOpts(*numbers, 0, *arrays)
     token, lp = (None, None) if out is None else out

@@ -1086,7 +1086,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
           a.lp[row] = (float)(((double)v[j] - (double)st.max) / st.r.T - log(Z));
         }
     } else {
-      seg = hit;
+      seg = max(hit, 0);   // -1 only if another call writes the workspace meanwhile
       // what lies before the segment comes off the target
       if (hit / 2 == (int)threadIdx.x) sh.mass[0][0] = hit & 1 ? first + e[0] : first;
       __syncthreads();
@@ -1226,7 +1226,8 @@ int grpo_sample(const void* logits, int dtype, int64_t B, int64_t V, int64_t row
     a.V = (int)V;
     a.segs = p.segs;
     a.splits = p.splits;
-    a.T = o.temperature;
+    // 1 / T has to be finite: infinity times a difference of 0 is NaN
+    a.T = o.temperature > 0.0 ? std::max(o.temperature, 1e-300) : 0.0;
     a.k = o.top_k;
     a.p = o.top_p;
     a.min_p = o.min_p;

@@ -104,6 +104,16 @@ def test_device_temperatures_out_of_range():
     check(x, u, run(x, u, T=T), T=T)
 
 
+def test_temperatures_near_zero_and_large_top_k():
+    x, u = logits(3, 900)
+    for T in (1e-300, 1e-310, 5e-324):
+        token, lp = run(x, u, T=T)
+        assert token.tolist() == x.argmax(1).tolist() and not lp.any()
+    check(x, u, run(x, u, k=2**32 + 5))
+    with pytest.raises(gp.GrpoError, match="top_k"):
+        run(x, u, k=-2**32 + 5)
+
+
 def test_bounds_of_u():
     x, _ = logits(6, 2000, masked=0.5)
     x[:, :5] = x[:, -5:] = float("-inf")
