@@ -384,9 +384,10 @@ int grpo_norm_bwd(const void* dY, const void* X, const void* weight, const float
  *   All zeros is the state before the first step.  The new codes are those of
  *   the moments in float64, beta m + (1 - beta) g with each product and sum
  *   rounded; the weights use the moments before their rounding to codes.
- * grpo_adamw: betas in [0, 1); lr, eps and weight_decay finite and >= 0; step
- *   the number of this step, from 1.  Device-side values, each read when the
- *   kernel runs if non-NULL (for a step under graph capture): step_dev [1] int64
+ * grpo_adamw: betas in [0, 1); lr, eps and weight_decay finite in
+ *   float32 and >= 0; step the number of this step, from 1.  Device-side values,
+ *   each read when the kernel runs if non-NULL (for a step under graph capture):
+ *   step_dev [1] int64
  *   in place of step (below 1 counts as 1), lr_dev [1] float32 in place of lr,
  *   grad_scale [1] float32 (NULL: 1).
  * grpo_moment_values: the float32 values of 8-bit codes (squared = 0: exp_avg's

@@ -103,7 +103,7 @@ def step(image, **kw):
 @pytest.mark.parametrize("kw", [
     {"lr": -1.0}, {"lr": float("nan")}, {"beta1": 1.0}, {"beta1": -0.1}, {"beta2": 1.5},
     {"beta2": float("nan")}, {"eps": -1e-8}, {"eps": float("inf")}, {"weight_decay": -1.0},
-    {"step": 0}, {"step": -5}])
+    {"lr": 1e39}, {"eps": 1e39}, {"weight_decay": 1e39}, {"step": 0}, {"step": -5}])
 def test_bad_hyperparameters_are_refused(kw):
     assert step(plan([tensor(1 << 24)])[1], **kw) == -1
     assert L.grpo_last_error()

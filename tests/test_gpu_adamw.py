@@ -174,6 +174,17 @@ def test_betas_of_zero_and_no_decay():
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_an_eps_below_float32_keeps_what_has_no_gradient(bits):
+    p = torch.full((600,), 2.0, device="cuda")
+    g = torch.zeros_like(p)
+    g[::2] = 3.0
+    m, v = gp.adamw_moments([p], bits)
+    gp.grpo_adamw(gp.adamw_plan([p], [g], m, v), step=1, lr=0.5, eps=1e-50, weight_decay=0.0)
+    want = torch.where(g > 0, 1.5, 2.0)                  # m / sqrt(v) is 1 at the first step
+    assert ((p - want).abs() <= 32 * U).all() and (p[1::2] == 2).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 def test_captured_step_follows_its_device_scalars(bits):
     a = make([5000, 300], torch.bfloat16, torch.float32, True, bits, False)
     b = make([5000, 300], torch.bfloat16, torch.float32, True, bits, False)
