@@ -65,6 +65,10 @@ class _GrpoNorm(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
+        if torch.cuda.is_current_stream_capturing():
+            # an eager graph of the same leaves that is still alive would draw its own stream into
+            # the capture, which ends the process
+            raise RuntimeError("grpo_norm's backward cannot be captured: call grpo_norm_bwd, which can")
         X, weight, rstd, *mean = ctx.saved_tensors
         need_x, need_w, need_b = ctx.needs_input_grad[:3]
         # an upstream gradient may be a broadcast view (that of a sum is)
@@ -79,5 +83,6 @@ def grpo_norm(X, weight, bias=None, eps: float = 1e-5, kind: int = NORM_RMS):
     """The norm of the rows of X [rows, cols], differentiable (once) with respect to X,
     weight and bias.  Arguments as for grpo_norm_fwd.  The gradients of weight and bias
     are formed in float32 and returned in the weight's type (grpo_norm_bwd with float32
-    accumulators keeps them in float32)."""
+    accumulators keeps them in float32).  The backward cannot be captured into a graph;
+    grpo_norm_fwd and grpo_norm_bwd can."""
     return _GrpoNorm.apply(X, weight, bias, eps, kind)

@@ -524,6 +524,7 @@ int grpo_norm_fwd(const void* X, const void* weight, const void* bias, int64_t r
   if (layer) GRPO_CHECK_PTR(mean);
   if (!isfinite(eps) || eps < 0.f)
     return fail(GRPO_ERR_INVALID_ARG, "eps must be finite and >= 0, not %g", (double)eps);
+  if (Y == X) return fail(GRPO_ERR_INVALID_ARG, "Y may not be X");
   hipStream_t s = (hipStream_t)stream;
   if (dtype == GRPO_BF16)
     GRPO_HIP(grpo::launch_norm_fwd<__bf16>((const __bf16*)X, (const __bf16*)weight,
@@ -559,6 +560,8 @@ int grpo_norm_bwd(const void* dY, const void* X, const void* weight, const float
                 workspace == nullptr ? (size_t)0 : workspace_bytes);
   if ((uintptr_t)workspace % grpo::kAlign != 0)
     return fail(GRPO_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+  // long rows are read again, for dweight, after dX is written
+  if (dX == dY || dX == X) return fail(GRPO_ERR_INVALID_ARG, "dX may not be dY or X");
   hipStream_t s = (hipStream_t)stream;
   float* part_w = (float*)workspace;
   float* part_b = dbias == nullptr ? nullptr : (float*)((char*)workspace + need / 2);

@@ -340,8 +340,9 @@ int grpo_loss_fwd_noalloc(const void* H, const void* W, const int32_t* y, const 
  * grpo_norm_bwd: dY [rows, cols] the gradient of Y; X, weight, mean and rstd
  *   as in the forward.  dX [rows, cols] dtype, OVERWRITTEN; dweight [cols] and
  *   dbias [cols] (NULL: not formed) float32, ACCUMULATED (+=, as dW is in
- *   grpo_loss_bwd) if accumulate is 1, OVERWRITTEN if it is 0.  workspace: grpo_norm_workspace_bytes(rows, cols, dtype),
- *   256-byte aligned.
+ *   grpo_loss_bwd) if accumulate is 1, OVERWRITTEN if it is 0.  workspace:
+ *   grpo_norm_workspace_bytes(rows, cols, dtype), 256-byte aligned.
+ * Y is not X, nor dX dY or X (refused), and outputs overlap no input.
  * Any cols from 1 to 2^24 and any element alignment.  Sums are float32, in a
  * fixed order: results are bitwise reproducible.
  */

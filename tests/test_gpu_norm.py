@@ -221,6 +221,18 @@ def test_another_stream_and_a_captured_graph():
         assert torch.equal(y, ey) and all(torch.equal(a, b) for a, b in zip(out, eager))
 
 
+def test_a_captured_backward_of_autograd_is_refused(monkeypatch):
+    i = inputs(8, 64, torch.float32)
+    x = i["x"].clone().requires_grad_()
+    y = gp.grpo_norm(x, i["w"], None, EPS)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="grpo_norm_bwd"):
+        y.backward(i["dy"])
+    monkeypatch.undo()
+    gp.grpo_norm(x, i["w"], None, EPS).backward(i["dy"])
+    assert x.grad.isfinite().all()
+
+
 def test_refusals_on_the_gpu():
     i = inputs(8, 64, torch.float32)
     with pytest.raises(ValueError, match="contiguous"):

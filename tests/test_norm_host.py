@@ -13,18 +13,18 @@ if not os.path.exists(_lib.LIB_PATH):
     pytest.skip("libgrpo.so not built", allow_module_level=True)
 
 L = _lib.lib()
-FAKE = ctypes.c_void_p(0x1000)
+FAKE, OUT = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x2000)
 
 
 def fwd(**kw):
-    a = dict(X=FAKE, w=FAKE, b=None, rows=4, cols=8, dt=0, kind=0, eps=1e-5, Y=FAKE, mean=FAKE,
+    a = dict(X=FAKE, w=FAKE, b=None, rows=4, cols=8, dt=0, kind=0, eps=1e-5, Y=OUT, mean=FAKE,
              rstd=FAKE)
     a.update(kw)
     return L.grpo_norm_fwd(*a.values(), None)
 
 
 def bwd(**kw):
-    a = dict(dY=FAKE, X=FAKE, w=FAKE, mean=FAKE, rstd=FAKE, rows=4, cols=8, dt=0, kind=0, acc=0, dX=FAKE,
+    a = dict(dY=FAKE, X=FAKE, w=FAKE, mean=FAKE, rstd=FAKE, rows=4, cols=8, dt=0, kind=0, acc=0, dX=OUT,
              dw=FAKE, db=None, ws=FAKE, wsb=1 << 30)
     a.update(kw)
     return L.grpo_norm_bwd(*a.values(), None)
@@ -34,7 +34,7 @@ def bwd(**kw):
     ({"X": None}, -1), ({"w": None}, -1), ({"Y": None}, -1), ({"rstd": None}, -1),
     ({"mean": None}, -1), ({"rows": 0}, -1), ({"cols": -1}, -1), ({"dt": 2}, -1), ({"dt": -1}, -1),
     ({"kind": 2}, -1), ({"eps": -1e-5}, -1), ({"eps": float("nan")}, -1),
-    ({"eps": float("inf")}, -1), ({"rows": 1 << 31}, -3), ({"cols": (1 << 24) + 1}, -3)])
+    ({"eps": float("inf")}, -1), ({"Y": FAKE}, -1), ({"rows": 1 << 31}, -3), ({"cols": (1 << 24) + 1}, -3)])
 def test_forward_argument_errors(kw, code):
     assert fwd(**kw) == code
     assert L.grpo_last_error()
@@ -43,7 +43,8 @@ def test_forward_argument_errors(kw, code):
 @pytest.mark.parametrize("kw,code", [
     ({"dY": None}, -1), ({"X": None}, -1), ({"w": None}, -1), ({"mean": None}, -1),
     ({"rstd": None}, -1), ({"dX": None}, -1), ({"dw": None}, -1), ({"rows": -3}, -1),
-    ({"dt": 7}, -1), ({"kind": -1}, -1), ({"acc": 2}, -1), ({"ws": None}, -2), ({"wsb": 16}, -2), ({"ws": ctypes.c_void_p(0x1010)}, -2),
+    ({"dt": 7}, -1), ({"kind": -1}, -1), ({"acc": 2}, -1), ({"dX": FAKE}, -1), ({"X": OUT}, -1), ({"dY": OUT}, -1),
+    ({"ws": None}, -2), ({"wsb": 16}, -2), ({"ws": ctypes.c_void_p(0x1010)}, -2),
     ({"cols": 1 << 25}, -3)])
 def test_backward_argument_errors(kw, code):
     assert bwd(**kw) == code
