@@ -17,9 +17,8 @@
 // instructions (233M bf16 weights with masters: 1.09 ms, 6.4 TB/s).  With 8-bit moments 10 bytes
 // stand against some 80, a third of them in float64, and both count (67M bf16 weights: 175 us,
 // 3.8 TB/s; 245 us with the definition of the codes worked out in every wave that has a root near a
-// border).  One block takes a chunk of 2048 elements of one tensor, 4 elements a lane and load, all
-// loads of the chunk issued before its first use.  Chunks of 4096 make the large steps 1 to 3 %
-// faster and 160 small tensors 11 % slower (10.1 against 11.2 us).
+// border).  One block takes a chunk of one tensor, 4 elements a lane and load, all loads of the
+// chunk issued before its first use.
 #include <float.h>
 #include <math.h>
 #include <string.h>
@@ -35,8 +34,12 @@
 namespace grpo {
 namespace {
 
-constexpr int kChunk = 2048;        // elements per block of 256 threads
-constexpr int kSteps = kChunk / 1024;
+// A block of 256 threads takes a chunk of STEPS * 1024 elements: 2048, or 4096 in plans of at least
+// 2^26 elements with float32 moments.  With masters, 2048 against 4096 against 8192: 2^27 elements 712,
+// 689 and 723 us, 2^24 83.3, 83.5 and 85.2 us, 160 small tensors 10.1 and 11.2; moments in 8 bits
+// are 5 % slower with 4096 at any size.
+constexpr int kStep = 1024, kChunk = 2 * kStep, kLongChunk = 4 * kStep;
+constexpr int64_t kMany = (int64_t)1 << 26;
 constexpr int kQuantBlock = 256;    // elements per scale: one wave's load
 
 // The image of a plan: this header, the tensors, then the first chunk of each tensor.
@@ -44,6 +47,7 @@ struct PlanHeader {
   uint64_t magic;
   int64_t count, chunks;
   int32_t param_dtype, grad_dtype, bits, master;
+  int64_t chunk;               // elements
   int64_t o_tensors, o_first;
 };
 constexpr uint64_t kMagic = 0x314e414c50574441ull;
@@ -200,21 +204,21 @@ __device__ __forceinline__ float quick_quotient(float m, float v, const Factors&
   return m * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(vh) + f.eps);
 }
 
-template <typename P, typename G, int BITS, bool MASTER, bool FULL>
+template <typename P, typename G, int BITS, bool MASTER, int STEPS, bool FULL>
 __device__ __forceinline__ void step_chunk(const grpo_adamw_tensor& t, int64_t base, const Hyper& h,
                                            const Factors& f) {
-  const int n = FULL ? kChunk : (int)(t.n - base);
+  const int n = FULL ? STEPS * kStep : (int)(t.n - base);
   P* param = (P*)t.param + base;
   const G* grad = (const G*)t.grad + base;
   float* master = t.master + (MASTER ? base : 0);
-  typename Vec4<P>::type p[kSteps];
-  typename Vec4<G>::type g[kSteps];
-  typename Vec4<float>::type w[kSteps], m[kSteps], v[kSteps];
-  typename Vec4<int8_t>::type mc[kSteps];
-  typename Vec4<uint8_t>::type vc[kSteps];
-  float ma[kSteps], va[kSteps];
+  typename Vec4<P>::type p[STEPS];
+  typename Vec4<G>::type g[STEPS];
+  typename Vec4<float>::type w[STEPS], m[STEPS], v[STEPS];
+  typename Vec4<int8_t>::type mc[STEPS];
+  typename Vec4<uint8_t>::type vc[STEPS];
+  float ma[STEPS], va[STEPS];
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
+  for (int k = 0; k < STEPS; ++k) {
     const int e = (k * 256 + (int)threadIdx.x) * 4;
     g[k] = load4<FULL>(grad, e, n);
     if constexpr (MASTER) w[k] = load4<FULL>(master, e, n);
@@ -231,7 +235,7 @@ __device__ __forceinline__ void step_chunk(const grpo_adamw_tensor& t, int64_t b
     }
   }
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
+  for (int k = 0; k < STEPS; ++k) {
     const int e = (k * 256 + (int)threadIdx.x) * 4;
     float nm[4], nv[4];
     double dm[4], dv[4];
@@ -239,8 +243,10 @@ __device__ __forceinline__ void step_chunk(const grpo_adamw_tensor& t, int64_t b
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float x = (float)g[k][j] * f.scale;
-        nm[j] = m[k][j] * f.b1 + x * f.a1;
-        nv[j] = v[k][j] * f.b2 + x * x * f.a2;
+        // fused by hand here and below: left to the compiler, which product is fused could differ
+        // between whole and last chunks, and results then go by where a tensor ends
+        nm[j] = fmaf(m[k][j], f.b1, x * f.a1);
+        nv[j] = fmaf(v[k][j], f.b2, x * x * f.a2);
       }
     } else {
       // float64, so that the new codes are those of the exact moments
@@ -271,7 +277,7 @@ __device__ __forceinline__ void step_chunk(const grpo_adamw_tensor& t, int64_t b
       float old;
       if constexpr (MASTER) old = w[k][j];
       else old = (float)p[k][j];
-      nw[j] = (old - f.decay * old) - f.step_size * u[j];
+      nw[j] = fmaf(-f.step_size, u[j], fmaf(-f.decay, old, old));
       np[j] = (P)nw[j];
     }
     store4<FULL>(param, e, n, np);
@@ -355,14 +361,14 @@ __device__ __forceinline__ void step_chunk(const grpo_adamw_tensor& t, int64_t b
   }
 }
 
-template <typename P, typename G, int BITS, bool MASTER>
+template <typename P, typename G, int BITS, bool MASTER, int STEPS>
 __global__ void __launch_bounds__(256)
     k_adamw(const grpo_adamw_tensor* __restrict__ tensors, const int64_t* __restrict__ first,
             int count, Hyper h) {
   const int64_t chunk = blockIdx.x;
   const int at = owner_of(first, count, chunk);
   const grpo_adamw_tensor t = tensors[at];
-  const int64_t base = (chunk - first[at]) * kChunk;
+  const int64_t base = (chunk - first[at]) * (STEPS * kStep);
 
   Factors f;
   float lr = h.lr;
@@ -385,8 +391,8 @@ __global__ void __launch_bounds__(256)
   f.b2 = (float)h.b2;
   f.a1 = (float)(1.0 - h.b1);
   f.a2 = (float)(1.0 - h.b2);
-  if (base + kChunk <= t.n) step_chunk<P, G, BITS, MASTER, true>(t, base, h, f);
-  else step_chunk<P, G, BITS, MASTER, false>(t, base, h, f);
+  if (base + STEPS * kStep <= t.n) step_chunk<P, G, BITS, MASTER, STEPS, true>(t, base, h, f);
+  else step_chunk<P, G, BITS, MASTER, STEPS, false>(t, base, h, f);
 }
 
 // The float32 values of 8-bit moments: a block takes 2048 of them.
@@ -396,16 +402,17 @@ __global__ void __launch_bounds__(256)
                     float* __restrict__ out) {
   const int64_t base = (int64_t)blockIdx.x * kChunk;
   const int left = (int)min<int64_t>(kChunk, n - base);
-  typename Vec4<C>::type c[kSteps];
-  float a[kSteps];
+  constexpr int STEPS = kChunk / kStep;
+  typename Vec4<C>::type c[STEPS];
+  float a[STEPS];
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
+  for (int k = 0; k < STEPS; ++k) {
     const int e = (k * 256 + (int)threadIdx.x) * 4;
     c[k] = load4<false>(codes + base, e, left);
     a[k] = e < left ? scales[base / kQuantBlock + e / kQuantBlock] : 0.f;
   }
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k) {
+  for (int k = 0; k < STEPS; ++k) {
     typename Vec4<float>::type o;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -419,10 +426,10 @@ template <typename P, typename G, bool MASTER>
 void launch_adamw(const PlanHeader& hd, const char* plan, const Hyper& h, hipStream_t s) {
   const auto* tensors = (const grpo_adamw_tensor*)(plan + hd.o_tensors);
   const auto* first = (const int64_t*)(plan + hd.o_first);
-  if (hd.bits == 32)
-    k_adamw<P, G, 32, MASTER><<<(unsigned)hd.chunks, 256, 0, s>>>(tensors, first, (int)hd.count, h);
-  else
-    k_adamw<P, G, 8, MASTER><<<(unsigned)hd.chunks, 256, 0, s>>>(tensors, first, (int)hd.count, h);
+  const auto kernel = hd.bits == 8                ? k_adamw<P, G, 8, MASTER, 2>
+                      : hd.chunk == kLongChunk ? k_adamw<P, G, 32, MASTER, 4>
+                                               : k_adamw<P, G, 32, MASTER, 2>;
+  kernel<<<(unsigned)hd.chunks, 256, 0, s>>>(tensors, first, (int)hd.count, h);
 }
 
 size_t image_bytes(int64_t count) {
@@ -454,14 +461,13 @@ int fill_plan(const grpo_adamw_tensor* tensors, int64_t count, int param_dtype, 
   const size_t ps = param_dtype == GRPO_F32 ? 4 : 2, gs = grad_dtype == GRPO_F32 ? 4 : 2;
   std::vector<Range> ranges;
   ranges.reserve((size_t)count * 7);
-  PlanHeader hd{kMagic, count, 0, param_dtype, grad_dtype, bits, 0, 0, 0};
+  PlanHeader hd{kMagic, count, 0, param_dtype, grad_dtype, bits, 0, kChunk, 0, 0};
   hd.o_tensors = (int64_t)align_up(sizeof(PlanHeader));
   hd.o_first = hd.o_tensors + (int64_t)align_up((size_t)count * sizeof(grpo_adamw_tensor));
   auto* first = (int64_t*)(image + hd.o_first);
-  int64_t with = 0, without = 0;
+  int64_t with = 0, without = 0, elements = 0;
   for (int64_t i = 0; i < count; ++i) {
     const grpo_adamw_tensor& t = tensors[i];
-    first[i] = hd.chunks;
     if (t.n < 0 || t.n > (int64_t)1 << 48)
       return fail(GRPO_ERR_INVALID_ARG, "tensor %lld has %lld elements", (long long)i,
                   (long long)t.n);
@@ -491,6 +497,7 @@ int fill_plan(const grpo_adamw_tensor* tensors, int64_t count, int param_dtype, 
     }
     (t.master != nullptr ? with : without) += 1;
     hd.chunks += (t.n + kChunk - 1) / kChunk;
+    elements += t.n;
   }
   if (with != 0 && without != 0)
     return fail(GRPO_ERR_INVALID_ARG, "%lld tensors have a master and %lld have none: all or none",
@@ -502,6 +509,12 @@ int fill_plan(const grpo_adamw_tensor* tensors, int64_t count, int param_dtype, 
   if (any_overlap(ranges))
     return fail(GRPO_ERR_INVALID_ARG, "two of the tensors overlap (the same one twice?)");
   hd.master = with != 0;
+  if (bits == 32 && elements >= kMany) hd.chunk = kLongChunk;
+  hd.chunks = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    first[i] = hd.chunks;
+    hd.chunks += (tensors[i].n + hd.chunk - 1) / hd.chunk;
+  }
   memcpy(image, &hd, sizeof hd);
   if (count > 0) memcpy(image + hd.o_tensors, tensors, (size_t)count * sizeof(grpo_adamw_tensor));
   return GRPO_OK;

@@ -41,6 +41,14 @@ def test_a_plan_of_many_tensors():
     header = ctypes.cast(image, ctypes.POINTER(ctypes.c_int64))
     assert header[1] == 7                                 # tensors
     assert header[2] == 1 + 0 + 2 + 3 + 1 + 49 + 0        # chunks of 2048
+    big = [tensor(1 << 40, (1 << 26) - 5), tensor(1 << 24, 5)]
+    for i, name in enumerate(NAMES):
+        if getattr(big[0], name):
+            setattr(big[0], name, (1 << 40) + (i << 34))
+    for bits, chunks in ((32, (1 << 14) + 1), (8, (1 << 15) + 1)):      # of 4096, of 2048
+        code, image = plan(big, bits=bits)
+        assert code == 0
+        assert ctypes.cast(image, ctypes.POINTER(ctypes.c_int64))[2] == chunks
     assert plan([])[0] == 0
     assert plan([tensor(1 << 24, 0)])[0] == 0
     assert L.grpo_adamw_plan_bytes(-1) == 0

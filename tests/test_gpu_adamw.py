@@ -184,6 +184,22 @@ def test_an_eps_below_float32_keeps_what_has_no_gradient(bits):
     assert ((p - want).abs() <= 32 * U).all() and (p[1::2] == 2).all()
 
 
+def test_a_plan_of_many_elements_is_that_of_its_pieces():
+    sizes = [(1 << 26) - 12345, 300, 1, 60001]
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda n, t: torch.randn(n, generator=gen, device="cuda").to(t)  # noqa: E731
+    p, g, w = ([rnd(n, t) for n in sizes] for t in (torch.bfloat16, torch.bfloat16, torch.float32))
+    m, v = [rnd(n, torch.float32) for n in sizes], [rnd(n, torch.float32).square() for n in sizes]
+    copies = [[t.clone() for t in x] for x in (p, m, v, w)]
+    gp.grpo_adamw(gp.adamw_plan(p, g, m, v, w), step=3, lr=1e-2)
+    for i, n in enumerate(sizes):
+        for at in range(0, n, 40_000_001):
+            q = [[x[i][at:at + 40_000_001]] for x in (copies[0], g, *copies[1:])]
+            gp.grpo_adamw(gp.adamw_plan(*q), step=3, lr=1e-2)
+    for got, want in zip((p, m, v, w), copies):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_captured_step_follows_its_device_scalars(bits):
     a = make([5000, 300], torch.bfloat16, torch.float32, True, bits, False)
