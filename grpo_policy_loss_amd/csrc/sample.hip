@@ -116,8 +116,8 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row
 
 // 2^t for t <= 0: t = n + f with n whole and |f| <= 1/2, and 2^f by its interpolation at the
 // Chebyshev points of degree 9 (relative error below 2e-14: with 10^5 borders in a row, one row in
-// 10^8 has u that near one).  Below 2^-1000 it stays at 2^-1000: nothing beside the row's maximum,
-// whose weight is 1.
+// 10^8 has u that near one).  Below 2^-1000 it stays at 2^-1000, which adds nothing to a sum beside
+// the row's maximum, whose weight is 1; where a token is drawn it counts as 0 (RowState::mass).
 __device__ __forceinline__ double pow2_down(double t) {
   t = fmax(t, -1000.0);
   const double magic = 0x1.8p52, shifted = t + magic;
@@ -291,6 +291,13 @@ struct RowState {
   RowParams r;
   __device__ __forceinline__ double weight(float x) const {
     return pow2_down(((double)x - (double)max) * r.rate);
+  }
+  // The weight, 0 below 2^-1000: what the pick may draw for u = 0 or 1 must not be what a finite
+  // mask or a temperature near zero leaves.  (The sums go without the test: it would be two more
+  // instructions for each token of k_sample_mass, whose sums it does not change.)
+  __device__ __forceinline__ double mass(float x) const {
+    const double t = ((double)x - (double)max) * r.rate;
+    return t < -1000.0 ? 0.0 : pow2_down(t);
   }
 };
 
@@ -955,7 +962,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
   }
   double e[8], Z = 0.0, target = 0.0;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) e[j] = s[j] > 0.0 ? s[j] * st.weight(m[j]) : 0.0;
+  for (int j = 0; j < 2; ++j) e[j] = s[j] > 0.0 ? s[j] * st.mass(m[j]) : 0.0;
   uint64_t cut = 0;
   const bool filtered = FILTERED && st.r.cls != PLAIN;
   if constexpr (FILTERED) {
@@ -1034,7 +1041,7 @@ __global__ void __launch_bounds__(kPick) k_sample_pick(SampleArgs a) {
       load8(x, c, V, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        e[j] = v[j] > kNone ? st.weight(v[j]) : 0.0;
+        e[j] = v[j] > kNone ? st.mass(v[j]) : 0.0;
         if (filtered)
           e[j] = v[j] > kNone && place(v[j], c + j) >= cut && e[j] >= st.r.min_p ? (double)units(e[j]) * 0x1p-42 : 0.0;
       }

@@ -446,7 +446,10 @@ int grpo_moment_values(const void* codes, const float* scales, int64_t n, int sq
  * -inf logits are tokens that cannot be drawn.  A row with a NaN or +inf, with
  * nothing above -inf, or with a device-side temperature that is negative or
  * not finite has token -1 and lp NaN.
- * Whatever decides a token is computed in 64 bits.  V and B at most 2^20.
+ * Whatever decides a token is computed in 64 bits.  Tokens lighter than 2^-1000
+ * of the heaviest (of a row with a filter: than 2^-43, since its weights are
+ * whole multiples of 2^-42) have no mass and are not drawn, whatever u is.
+ * V and B at most 2^20.
  * workspace: grpo_sample_workspace_bytes(B, V), 256-byte aligned.
  */
 typedef struct grpo_sample_opts {

@@ -135,6 +135,33 @@ def test_far_apart_logits():
         check(x, u, run(x, u, **params), **params)
 
 
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("mask", [-1e4, -1e9, -1e30, "lowest"])
+@pytest.mark.parametrize("V", [50, 4000, 70001])
+def test_tokens_without_weight_are_not_drawn(V, mask, t):
+    """Finite masks, in front of the drawable tokens and behind them, and the bounds of u: where u
+    is 0 the first token of any weight is drawn, where it is 1 the last."""
+    g = torch.Generator().manual_seed(V)
+    x = torch.full((7, V), torch.finfo(t).min if mask == "lowest" else mask)
+    for b in range(7):
+        at = torch.randperm(V - 20, generator=g)[:b + 1] + 10     # never the first or last ten
+        x[b, at] = 2 * torch.randn(b + 1, generator=g)
+    x = x.to(t)
+    u = torch.tensor([0.0, 1.0, 0.0, 1.0 - 2.0 ** -24, -1.0, 3.0, 0.0])
+    off = torch.ones(7)
+    for params in (dict(), dict(T=0.5), dict(T=off * 0.5), dict(p=off), dict(p=0.9), dict(k=5)):
+        check(x, u, run(x, u, **params), **params)
+
+
+def test_bounds_of_u_at_temperatures_near_zero():
+    x, _ = logits(6, 5000)
+    u = torch.tensor([0.0, 1.0, 0.0, 1.0 - 2.0 ** -24, -1.0, 0.5])
+    check(x, u, run(x, u, T=1e-3), T=1e-3)      # where weights of e^-428 and e^-600 are left
+    for T in (1e-30, 1e-300, torch.full((6,), 1e-30)):
+        token, lp = run(x, u, T=T)
+        assert token.tolist() == x.argmax(1).tolist() and not lp.any()
+
+
 def test_rows_that_lie_apart_and_any_alignment():
     for t in (torch.float32, torch.bfloat16):
         x, u = logits(7, 1999, t)
