@@ -165,7 +165,7 @@ def adamw_moments(params, bits: int = 32):
         if bits == 32:
             return torch.zeros(p.shape, dtype=torch.float32, device=p.device)
         return Moment8(torch.zeros(p.shape, dtype=dtype, device=p.device),
-                       torch.zeros(-(-p.numel() // QUANT_BLOCK), device=p.device))
+                       torch.zeros(-(-p.numel() // QUANT_BLOCK), dtype=torch.float32, device=p.device))
     return [zeros(p, torch.int8) for p in params], [zeros(p, torch.uint8) for p in params]
 
 

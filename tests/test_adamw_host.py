@@ -169,6 +169,19 @@ def test_moments():
         gp.adamw_plan([torch.zeros(3)], [torch.zeros(3)], [v[1]][:1], [m[1]])
 
 
+@pytest.mark.parametrize("default", [torch.float64, torch.bfloat16])
+def test_moments_do_not_go_by_the_default_type(default):
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(default)
+    try:
+        for bits in (8, 32):
+            m, v = gp.adamw_moments([torch.zeros(300, dtype=torch.float32)], bits)
+            for q in (m[0], v[0]):
+                assert (q.scales if bits == 8 else q).dtype == torch.float32
+    finally:
+        torch.set_default_dtype(before)
+
+
 def test_structs_match_the_header():
     hdr = open(os.path.join(os.path.dirname(__file__), "..", "include", "grpo.h")).read()
     for struct, cls in (("grpo_adamw_tensor", _lib.AdamWTensor), ("grpo_adamw_opts", _lib.AdamWOpts)):
