@@ -140,6 +140,19 @@ def test_nan_and_infinite_values_stay_in_their_row():
         assert y[7].isnan().all() and y[21, 599].isnan() and dx[7].isnan().all()
 
 
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cols", [3, 50, 100, 300, 1000, 1537, 3000, 5000, 12000, 16387])
+def test_a_mean_whose_normalised_value_leaves_float32(cols, t):
+    """Every element is its row's mean, 2^121 with rstd 2^8: no real column leaves float32's
+    range, but (0 - mean) rstd would, where lanes lie behind the row's end."""
+    i = inputs(5, cols, t)
+    i["x"].fill_(2.0 ** 121)
+    mean, rstd = torch.full((5,), 2.0 ** 121, device="cuda"), torch.full((5,), 256.0, device="cuda")
+    for bias in (False, True):
+        dx, dw, db = gp.grpo_norm_bwd(i["dy"], i["x"], i["w"], mean, rstd, gp.NORM_LAYER, bias)
+        check_bwd(i, mean, rstd, dx, dw, db, True, bias)
+
+
 def test_rows_of_zeros_and_constants():
     x = torch.zeros(3, 256, device="cuda")
     x[1] = 5.0
