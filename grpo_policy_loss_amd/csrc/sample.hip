@@ -114,23 +114,25 @@ __device__ __forceinline__ RowParams row_params(const SampleArgs& a, int64_t row
   return r;
 }
 
-// 2^t for t <= 0: t = n + f with n whole and |f| <= 1/2, and 2^f by its interpolation at the
-// Chebyshev points of degree 9 (relative error below 2e-14: with 10^5 borders in a row, one row in
-// 10^8 has u that near one).  Below 2^-1000 it stays at 2^-1000, which adds nothing to a sum beside
-// the row's maximum, whose weight is 1; where a token is drawn it counts as 0 (RowState::mass).
+// 2^t for t <= 0: t = n + f with n whole and |f| <= 1/2, and 2^f by the polynomial 1 + f q(f) of
+// degree 9 whose largest relative error is the least one, below 1.6e-14 (with 10^5 borders in a
+// row, one row in 10^8 has u that near one).  It is off by the same at both ends, -1.51e-14, so that
+// weights do not jump from one n to the next.  Below 2^-1000 it stays at 2^-1000, which adds nothing
+// to a sum beside the row's maximum, whose weight is 1; where a token is drawn it counts as 0
+// (RowState::mass).
 __device__ __forceinline__ double pow2_down(double t) {
   t = fmax(t, -1000.0);
   const double magic = 0x1.8p52, shifted = t + magic;
   const double f = t - (shifted - magic);
-  double q = 0x1.b6571de2f2351p-24;
-  q = fma(q, f, 0x1.63ef969a64d3cp-20);
-  q = fma(q, f, 0x1.ffcb76789860fp-17);
-  q = fma(q, f, 0x1.43088e257f341p-13);
-  q = fma(q, f, 0x1.5d87fe908f88ap-10);
-  q = fma(q, f, 0x1.3b2ab72b175eep-7);
-  q = fma(q, f, 0x1.c6b08d7044119p-5);
-  q = fma(q, f, 0x1.ebfbdff8149f2p-3);
-  q = fma(q, f, 0x1.62e42fefa39f7p-1);
+  double q = 0x1.b3de31389fe36p-24;
+  q = fma(q, f, 0x1.63e6964c004b3p-20);
+  q = fma(q, f, 0x1.ffce2fc0b9a32p-17);
+  q = fma(q, f, 0x1.430897f348181p-13);
+  q = fma(q, f, 0x1.5d87fd938895cp-10);
+  q = fma(q, f, 0x1.3b2ab72412178p-7);
+  q = fma(q, f, 0x1.c6b08d70c880dp-5);
+  q = fma(q, f, 0x1.ebfbdff81be06p-3);
+  q = fma(q, f, 0x1.62e42fefa37d1p-1);
   q = fma(q, f, 1.0);
   // n into the exponent: q is in [0.7, 1.5] and n at least -1000
   const int n = (int)(uint32_t)__double_as_longlong(shifted);

@@ -1,6 +1,8 @@
 """Sampling's refusals, on the host: no call here gets past the argument checks."""
 import ctypes
 import os
+import re
+from decimal import Decimal, localcontext
 
 import pytest
 import torch
@@ -56,6 +58,28 @@ def test_struct_matches_the_header():
     body = hdr[hdr.index("typedef struct grpo_sample_opts {"):hdr.index("} grpo_sample_opts;")]
     names = [ln.split(";")[0].split()[-1].lstrip("*") for ln in body.splitlines()[1:] if ";" in ln]
     assert names == [n for n, _ in _lib.SampleOpts._fields_]
+
+
+def test_the_polynomial_of_two_to_a_fraction():
+    """The source's own coefficients, in 40 digits: what its comment says of their error (the
+    Horner steps in float64 add a few 2^-53 = 1.1e-16)."""
+    path = os.path.join(os.path.dirname(_lib.__file__), "csrc", "sample.hip")
+    body = open(path).read()
+    body = body[body.index("double pow2_down(double t) {"):]
+    body = body[body.index("double q = "):body.index("// n into the exponent")]
+    coef = [float.fromhex(c) for c in re.findall(r"0x1\.[0-9a-f]+p-\d+", body)] + [1.0]
+    assert len(coef) == 10 and "fma(q, f, 1.0)" in body
+    with localcontext() as ctx:
+        ctx.prec = 40
+
+        def error(f):
+            q = Decimal(0)
+            for c in coef:
+                q = q * f + Decimal(c)
+            return q / Decimal(2) ** f - 1
+        at = [error(Decimal(i) / 4000) for i in range(-2000, 2001)]
+        assert max(abs(e) for e in at) < Decimal("1.6e-14") - 4 * Decimal(2) ** -53
+        assert abs(at[0] - at[-1]) < Decimal("1e-16")     # no jump where one n meets the next
 
 
 @pytest.mark.parametrize("over,err,what", [
