@@ -458,9 +458,11 @@ hipError_t launch_norm_bwd(const T* dY, const T* X, const T* w, const float* mea
                                                               part_w, part_b);                  \
     return hipGetLastError();                                                                   \
   }
-  GRPO_ROW_SHAPES(GRPO_CASE) GRPO_CASE(512, 1)
-  if constexpr (sizeof(T) == 4) {  // 16-bit rows of this length would spill
+  GRPO_ROW_SHAPES(GRPO_CASE)
+  if constexpr (sizeof(T) == 4) {
     GRPO_CASE(1024, 4)
+  } else {
+    GRPO_CASE(512, 1)
   }
 #undef GRPO_CASE
   k_norm_bwd_long<T><<<(unsigned)std::min<int64_t>(rows, 4 * kCUs), 1024, 0, s>>>(
