@@ -392,15 +392,17 @@ __global__ void __launch_bounds__(1024)
 struct RowShape {
   int lpr, nv;
 };
-template <typename T> RowShape row_shape(int64_t n, bool backward) {
+template <typename T> RowShape row_shape(int64_t n, bool backward, bool bias) {
   static const RowShape shapes[] = {{4, 1},   {16, 1},  {64, 1},  {64, 2},  {256, 1},
                                     {256, 2}, {512, 2}, {512, 4}, {1024, 4}};
   for (const RowShape& s : shapes) {
     if (n > (int64_t)s.lpr * s.nv * kVec<T> || (s.lpr == 1024 && sizeof(T) != 4)) continue;
     // The backward of 16-bit rows that nearly fill 512 lanes of one vector is faster in those, with
     // fewer registers (32768 x 4096 with bias 147 us against 180), that of shorter rows in 256 lanes
-    // of two, which keep more rows in flight (32768 x 2880: 110 us against 130).
-    if (backward && sizeof(T) == 2 && s.lpr == 256 && s.nv == 2 && n > 416 * kVec<T>) return {512, 1};
+    // of two, which keep more rows in flight (32768 x 2064, 2880 and 3328 without bias: 92, 110 and
+    // 128 us against 119, 124 and 128).  The sums of a bias would not fit the registers of these: with
+    // bias, 512 lanes at any length (151, 159 and 166 us against 123, 129 and 135).
+    if (backward && sizeof(T) == 2 && s.lpr == 256 && s.nv == 2 && (bias || n > 416 * kVec<T>)) return {512, 1};
     return s;
   }
   return {0, 0};
@@ -424,7 +426,7 @@ template <typename T>
 hipError_t launch_norm_fwd(const T* X, const T* w, const T* b, int64_t rows, int n, int layer,
                            float eps, T* Y, float* mean, float* rstd, hipStream_t s) {
   ScopedKernelTimer t(KK_NORM_FWD, s);
-  const RowShape sh = row_shape<T>(n, false);
+  const RowShape sh = row_shape<T>(n, false, b != nullptr);
   const int64_t rpb = sh.lpr == 0 ? 1 : std::max(1, 256 / sh.lpr);
   const unsigned grid = (unsigned)std::min<int64_t>((rows + rpb - 1) / rpb, 8 * kCUs);
 #define GRPO_CASE(L, N)                                                                      \
@@ -446,20 +448,22 @@ hipError_t launch_norm_bwd(const T* dY, const T* X, const T* w, const float* mea
                            const float* rstd, int64_t rows, int n, T* dX, float* part_w,
                            float* part_b, hipStream_t s) {
   ScopedKernelTimer t(KK_NORM_BWD, s);
-  const RowShape sh = row_shape<T>(n, true);
+  const RowShape sh = row_shape<T>(n, true, part_b != nullptr);
   const unsigned grid = (unsigned)bwd_blocks(rows, n, sh, part_b != nullptr);
 #define GRPO_CASE(L, N)                                                                         \
   if (sh.lpr == L && sh.nv == N) {                                                              \
-    if (part_b != nullptr)                                                                      \
-      k_norm_bwd<T, L, N, true><<<grid, kThreadsBwd<L>, 0, s>>>(dY, X, w, mean, rstd, rows, n, dX, \
-                                                             part_w, part_b);                   \
-    else                                                                                        \
+    if (part_b == nullptr)                                                                      \
       k_norm_bwd<T, L, N, false><<<grid, kThreadsBwd<L>, 0, s>>>(dY, X, w, mean, rstd, rows, n, dX, \
                                                               part_w, part_b);                  \
+    else if constexpr (sizeof(T) == 4 || L != 256 || N != 2)                                    \
+      k_norm_bwd<T, L, N, true><<<grid, kThreadsBwd<L>, 0, s>>>(dY, X, w, mean, rstd, rows, n, dX, \
+                                                             part_w, part_b);                   \
     return hipGetLastError();                                                                   \
   }
   GRPO_ROW_SHAPES(GRPO_CASE)
   if constexpr (sizeof(T) == 4) {
+    // 128 registers do not hold these rows (81 to 116 spill), but the long rows' three passes take
+    // longer: 4096 x 16384 176 us, 210 with bias, against 295 and 298 (512 rows: 42 and 52 against 40)
     GRPO_CASE(1024, 4)
   } else {
     GRPO_CASE(512, 1)
@@ -499,7 +503,7 @@ int check_norm(int64_t rows, int64_t cols, int dtype, int kind) {
 
 // The number of partial rows for either type (their vectors differ, so their lanes do).
 int64_t partial_rows(int64_t rows, int64_t cols, int dtype, bool bias) {
-  return bwd_blocks(rows, cols, dtype == GRPO_F32 ? row_shape<float>(cols, true) : row_shape<__bf16>(cols, true),
+  return bwd_blocks(rows, cols, dtype == GRPO_F32 ? row_shape<float>(cols, true, bias) : row_shape<__bf16>(cols, true, bias),
                     bias);
 }
 
@@ -512,7 +516,10 @@ extern "C" {
 
 size_t grpo_norm_workspace_bytes(int64_t rows, int64_t cols, int dtype) {
   if (grpo::check_norm(rows, cols, dtype, GRPO_NORM_LAYER) != GRPO_OK) return 0;
-  return 2 * grpo::align_up((size_t)(grpo::partial_rows(rows, cols, dtype, false) * cols) * 4);
+  // either form may have more
+  const int64_t most = std::max(grpo::partial_rows(rows, cols, dtype, false),
+                                grpo::partial_rows(rows, cols, dtype, true));
+  return 2 * grpo::align_up((size_t)(most * cols) * 4);
 }
 
 int grpo_norm_fwd(const void* X, const void* weight, const void* bias, int64_t rows, int64_t cols,

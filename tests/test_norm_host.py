@@ -66,6 +66,15 @@ def test_workspace_is_bounded():
         assert L.grpo_norm_workspace_bytes(1 << 20, 1 << 24, dt) == 1 << 27
 
 
+def test_workspace_holds_the_partial_rows_of_either_form():
+    """bfloat16 rows of 2049 to 4096 elements with bias leave one partial row for each row up to
+    512, whatever the form without bias leaves."""
+    for rows in (1, 2, 511, 512, 700, 1023, 1024, 5000):
+        for cols in (2049, 2880, 3328, 3329, 4096):
+            need = 2 * (-(-min(rows, 512) * cols * 4 // 256) * 256)
+            assert L.grpo_norm_workspace_bytes(rows, cols, 1) >= need
+
+
 def _args(t=torch.bfloat16):
     return dict(X=torch.zeros(6, 8, dtype=t), weight=torch.ones(8, dtype=t),
                 bias=torch.zeros(8, dtype=t))

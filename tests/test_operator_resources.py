@@ -52,3 +52,11 @@ def test_backward_instances_are_those_that_rows_get(norm):
         assert ("bf16", 512, 1, bias) in found
         assert ("f32", 512, 1, bias) not in found      # 512 lanes of one vector are for 16-bit rows
         assert ("f32", 1024, 4, bias) in found and ("bf16", 1024, 4, bias) not in found
+
+
+def test_backward_instances_hold_their_rows_in_registers(norm):
+    """All but those of rows above 8192 elements, where every other form is slower still."""
+    for (t, lanes, vectors, bias), k in _backward(norm).items():
+        if vectors < 4:
+            assert k[".vgpr_spill_count"] == k[".private_segment_fixed_size"] == 0, (t, lanes, vectors, bias)
+    assert ("bf16", 256, 2, True) not in _backward(norm) and ("bf16", 256, 2, False) in _backward(norm)
