@@ -172,13 +172,32 @@ def adamw_moments(params, bits: int = 32):
 class AdamWPlan:
     """What grpo_adamw needs of its tensors, made once by adamw_plan.  It keeps the
     tensors' memory alive and holds their addresses: a parameter or gradient that is
-    replaced (p.data = ..., zero_grad(set_to_none=True)) needs a new plan."""
+    replaced (p.data = ..., zero_grad(set_to_none=True), the default) needs a new plan.
+    The step goes by the old ones without noticing, since it looks at no tensor;
+    holds() tells."""
 
-    def __init__(self, tensors, params, image, table):
+    def __init__(self, tensors, params, image, table, lists):
         self.tensors, self.image, self.table = tensors, image, table
+        self.lists = lists      # params, grads and, with masters, those: first in each of tensors
+        self.places = [[t.data_ptr() for t in row] for row in tensors]
         self.versioned = [p for p in params if not p.is_inference()]
         self.device = table.device
         self.stream = torch._C._cuda_getCurrentRawStream(table.get_device())
+
+    def holds(self, params, grads, master=None) -> bool:
+        """Whether these are still the tensors that the plan steps, at the addresses that it
+        holds, and its moments have not moved: adamw_plan's params, grads and master (None
+        where it had none; a gradient of None is not held).  Host work of some 0.8 us a
+        tensor, so it is the caller's to ask where tensors may have been replaced."""
+        lists = [list(x) for x in (params, grads) + (() if master is None else (master,))]
+        if len(lists) != self.lists or any(len(x) != len(self.places) for x in lists):
+            return False
+        for now, row, at in zip(zip(*lists), self.tensors, self.places):
+            if any(t is None or t.data_ptr() != a or t.numel() != row[0].numel() for t, a in zip(now, at)):
+                return False
+            if any(t.data_ptr() != a for t, a in zip(row, at)):
+                return False
+        return True
 
 
 def adamw_plan(params, grads, exp_avg, exp_avg_sq, master=None) -> AdamWPlan:
@@ -225,7 +244,7 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, master=None) -> AdamWPlan:
     with ctx:
         # a copy from pageable memory: it has arrived when the call returns
         table = torch.frombuffer(image, dtype=torch.uint8).to(params[0].device)
-        return AdamWPlan(keep, params, image, table)
+        return AdamWPlan(keep, params, image, table, 2 if master is None else 3)
 
 
 def _scalar(x, name, dtype):

@@ -241,6 +241,44 @@ def test_another_stream():
     assert torch.equal(a["master"][0], b["master"][0]) and torch.equal(a["m"][0].codes, b["m"][0].codes)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("master", [False, True])
+def test_a_plan_tells_whether_it_holds_its_tensors(master, bits):
+    p = [torch.nn.Parameter(torch.randn(300, 5, device="cuda").bfloat16()), torch.nn.Parameter(torch.randn(7, device="cuda").bfloat16())]
+    for x in p:
+        x.grad = torch.randn_like(x)
+    w = [x.detach().float() for x in p] if master else None
+    m, v = gp.adamw_moments(p, bits)
+
+    def grads():
+        return [x.grad for x in p]
+    plan = gp.adamw_plan(p, grads(), m, v, w)
+    gp.grpo_adamw(plan, 1)
+    assert plan.holds(p, grads(), w)
+    assert not plan.holds(p[:1], grads()[:1], w and w[:1])
+    assert not plan.holds(p, grads(), None if master else [x.float() for x in p])
+    assert not plan.holds(p[::-1], grads()[::-1], w and w[::-1])
+    kept = p[1].grad
+    p[1].grad = None                        # zero_grad's default
+    assert not plan.holds(p, grads(), w)
+    p[1].grad = torch.zeros_like(p[1])      # another one
+    assert not plan.holds(p, grads(), w)
+    p[1].grad = kept
+    assert plan.holds(p, grads(), w)
+    old = p[0].data
+    p[0].data = old.clone()
+    assert not plan.holds(p, grads(), w)
+    p[0].data = old
+    assert plan.holds(p, grads(), w)
+    p[0].grad.untyped_storage().resize_(0)  # freed in place
+    assert not plan.holds(p, grads(), w)
+    moved = m[1].codes if bits == 8 else m[1]
+    plan = gp.adamw_plan(p[1:], grads()[1:], m[1:], v[1:], w and w[1:])
+    assert plan.holds(p[1:], grads()[1:], w and w[1:])
+    moved.untyped_storage().resize_(0)
+    assert not plan.holds(p[1:], grads()[1:], w and w[1:])
+
+
 def test_autograd_sees_the_step():
     w = torch.randn(16, 8, device="cuda", requires_grad=True)
     g = torch.randn_like(w)
