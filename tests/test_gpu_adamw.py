@@ -124,6 +124,19 @@ def test_first_step_from_zero_moments(bits):
     assert all(x.isfinite().all() for x in p)
 
 
+def test_first_step_from_zero_float32_moments():
+    gen = torch.Generator().manual_seed(4)
+    p = [torch.randn(777, generator=gen).cuda(), torch.randn(3, 5, generator=gen).cuda()]
+    g = [torch.randn(x.shape, generator=gen).cuda() for x in p]
+    g[0][:256] = 0                                  # a block without a gradient
+    m, v = gp.adamw_moments(p, 32)
+    s = dict(p=p, g=g, m=m, v=v, master=None)
+    old = state64(s, 32)
+    gp.grpo_adamw(gp.adamw_plan(p, g, m, v), 1, **HYPER)
+    check(s, old, 32, 1, 1.0)
+    assert not m[0][:256].any() and not v[0][:256].any()
+
+
 @pytest.mark.parametrize("betas", [(0.9, 0.999), (0.9, 0.95), (0.95, 0.98)])
 def test_scales_that_lie_between_two_float32_values(betas):
     """Bfloat16 gradients and old moments at their blocks' scales: the new scale is often an exact

@@ -89,6 +89,38 @@ def test_both_directions(cols, t, kind):
             check_bwd(i, mean, rstd, dx, dw, db, kind == "layer", bias)
 
 
+# more rows than one round of the grid takes: the forward's 2048 blocks of 64, 16, 4 or 1 rows (by
+# the lanes of a row), the backward's 256 to 1024, and the last round not full
+@pytest.mark.parametrize("rows,cols", [(140003, 7), (33333, 100), (9001, 500), (9001, 900), (5003, 1537),
+                                       (5003, 2880), (2300, 4096), (2100, 8192), (2100, 16384), (2100, 16387)])
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
+def test_blocks_that_take_several_rounds_of_rows(rows, cols, t):
+    for kind in ("layer", "rms") if cols <= 1537 else ("layer",) if t == torch.float32 else ("rms",):
+        i = inputs(rows, cols, t, seed=cols)
+        bias = kind == "layer"
+        y, mean, rstd = gp.grpo_norm_fwd(i["x"], i["w"], i["b"] if bias else None, EPS, KINDS[kind])
+        check_fwd(i, y, mean, rstd, bias, bias)
+        dx, dw, db = gp.grpo_norm_bwd(i["dy"], i["x"], i["w"], mean, rstd, KINDS[kind], bias)
+        check_bwd(i, mean, rstd, dx, dw, db, bias, bias)
+
+
+@pytest.mark.parametrize("rows,cols", [(1041000, 2064), (131100, 16400)])
+def test_offsets_beyond_32_bits(rows, cols):
+    """Rows from 2^31 elements on, whose gradient alone is not zero."""
+    assert (rows - 20) * cols > 1 << 31
+    last = 16
+    i = inputs(last, cols, torch.bfloat16)
+    x, dy = (torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[:, ::3] = 1.0
+    x[-last:], dy[-last:] = i["x"], i["dy"]
+    y, mean, rstd = gp.grpo_norm_fwd(x, i["w"], i["b"], EPS, gp.NORM_LAYER)
+    check_fwd(i, y[-last:], mean[-last:], rstd[-last:], True, True)
+    assert torch.equal(y[0], y[rows - last - 1])
+    dx, dw, db = gp.grpo_norm_bwd(dy, x, i["w"], mean, rstd, gp.NORM_LAYER, True)
+    check_bwd(i, mean[-last:], rstd[-last:], dx[-last:], dw, db, True, True)
+    assert not dx[:-last].any()
+
+
 @pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("cols", [24, 1536, 20000])
 def test_any_element_alignment(t, cols):

@@ -124,6 +124,19 @@ def test_bounds_of_u():
         assert got[0][1] == got[0][1] and (x.gather(1, got[0].cpu().long()[:, None]) > float("-inf")).all()
 
 
+def test_the_largest_u_reaches_the_last_token_that_weighs_enough():
+    """Of two tokens with weights 1 and w: (1 - 2^-24)(1 + w) is above 1, the first one's mass, for
+    w = 2^-20, and below it for w = 2^-30."""
+    x = torch.full((4, 2000), float("-inf"))
+    x[:, 3] = 0.0
+    x[:, 1990] = torch.tensor([2.0 ** -20, 2.0 ** -30] * 2).log()
+    u = torch.full((4,), 1.0 - 2.0 ** -24)
+    for params in (dict(), dict(k=20), dict(p=0.9999999), dict(min_p=2.0 ** -40)):
+        got = run(x, u, **params)
+        assert got[0].tolist() == [1990, 3, 1990, 3]
+        check(x, u, got, **params)
+
+
 def test_far_apart_logits():
     """Weights far below the largest one: none of them is drawn, none disturbs."""
     x = torch.full((3, 4000), -1e30)
