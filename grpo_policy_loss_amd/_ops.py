@@ -172,9 +172,9 @@ def adamw_moments(params, bits: int = 32):
 class AdamWPlan:
     """What grpo_adamw needs of its tensors, made once by adamw_plan.  It keeps the
     tensors' memory alive and holds their addresses: a parameter or gradient that is
-    replaced (p.data = ..., zero_grad(set_to_none=True), the default) needs a new plan.
-    The step goes by the old ones without noticing, since it looks at no tensor;
-    holds() tells."""
+    replaced (p.data = ..., zero_grad(set_to_none=True), the default) or whose storage is
+    freed in place (resize_(0)) needs a new plan.  The step goes by the old addresses
+    without noticing, since it looks at no tensor; holds() tells."""
 
     def __init__(self, tensors, params, image, table, lists):
         self.tensors, self.image, self.table = tensors, image, table
@@ -290,10 +290,10 @@ def grpo_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=N
     bfloat16; rows may lie any distance apart), from u [B] float32 in [0, 1), and its
     log-probability (float32 [B]) under softmax(logits / temperature) of the whole row.
     temperature, top_k, top_p and min_p are numbers, or tensors [B] with one for each row
-    (float32; int32 for top_k).  0 is off for each (temperature 0 means 1), and so is
-    top_p 1; top_k 1 takes the largest logit.  out: (token, lp) to write into.  See
-    grpo_sample in include/grpo.h for the order of the filters and rows without a
-    distribution."""
+    (float32; int32 for top_k).  0 is off for each, and so is top_p 1: temperature 0 samples
+    at temperature 1 and top_p 0 keeps the whole row; top_k 1 takes the largest logit.
+    out: (token, lp) to write into.  See grpo_sample in include/grpo.h for the order of the
+    filters and rows without a distribution."""
     B, V = _matrix(logits, "logits")
     dt = _dt(logits)
     if V > 1 and logits.stride(1) != 1 or B > 1 and logits.stride(0) < V:

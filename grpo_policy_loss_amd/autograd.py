@@ -66,8 +66,11 @@ class _GrpoNorm(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dY):
         if torch.cuda.is_current_stream_capturing():
-            # an eager graph of the same leaves that is still alive would draw its own stream into
-            # the capture, which ends the process
+            # The node that adds up a leaf's gradient is made by the first graph that uses the leaf,
+            # is shared by all later ones while any of them lives, and runs on the stream on which it
+            # was made.  A captured backward that reaches one of an eager graph joins that stream,
+            # which is not captured: the capture fails and the process ends.  Whether such a graph
+            # lives cannot be seen from here.
             raise RuntimeError("grpo_norm's backward cannot be captured: call grpo_norm_bwd, which can")
         X, weight, rstd, *mean = ctx.saved_tensors
         need_x, need_w, need_b = ctx.needs_input_grad[:3]
@@ -83,6 +86,7 @@ def grpo_norm(X, weight, bias=None, eps: float = 1e-5, kind: int = NORM_RMS):
     """The norm of the rows of X [rows, cols], differentiable (once) with respect to X,
     weight and bias.  Arguments as for grpo_norm_fwd.  The gradients of weight and bias
     are formed in float32 and returned in the weight's type (grpo_norm_bwd with float32
-    accumulators keeps them in float32).  The backward cannot be captured into a graph;
-    grpo_norm_fwd and grpo_norm_bwd can."""
+    accumulators keeps them in float32).  The backward raises while its stream is captured
+    into a graph, since an eager graph of the same leaves that is still alive would end the
+    process there; grpo_norm_fwd and grpo_norm_bwd can be captured."""
     return _GrpoNorm.apply(X, weight, bias, eps, kind)

@@ -14,9 +14,9 @@
 // that is not finite has the scale NaN, so all of it reads back as NaN.
 //
 // With float32 moments the step is bound by memory: 20 to 30 bytes an element against some 20
-// instructions (233M bf16 weights with masters: 1.09 ms, 6.4 TB/s).  With 8-bit moments 10 bytes
-// stand against some 80, a third of them in float64, and both count (67M bf16 weights: 175 us,
-// 3.8 TB/s; 245 us with the definition of the codes worked out in every wave that has a root near a
+// instructions (233M bf16 weights with masters: 1.09 to 1.21 ms from card to card, 5.8 to 6.4 TB/s).
+// With 8-bit moments 10 bytes stand against some 80, a third of them in float64, and both count (67M
+// bf16 weights: 175 to 181 us, 3.8 TB/s; 245 us with the definition of the codes worked out in every wave that has a root near a
 // border).  One block takes a chunk of one tensor, 4 elements a lane and load, all loads of the
 // chunk issued before its first use.
 #include <float.h>
@@ -35,9 +35,16 @@ namespace grpo {
 namespace {
 
 // A block of 256 threads takes a chunk of STEPS * 1024 elements: 2048, or 4096 in plans of at least
-// 2^26 elements with float32 moments.  With masters, 2048 against 4096 against 8192: 2^27 elements 712,
-// 689 and 723 us, 2^24 83.3, 83.5 and 85.2 us, 160 small tensors 10.1 and 11.2; moments in 8 bits
-// are 5 % slower with 4096 at any size.
+// 2^26 elements with float32 moments.  2048 against 4096 elements, in us:
+//   parameters, gradients        2^26 elements   2^27 elements
+//   bf16, f32, masters           354   340       719   696   (8192: 723 against 689)
+//   bf16, bf16, masters          296   299       675   656
+//   bf16, f32                    238   231       567   548
+//   bf16, bf16                   246   242       490   500
+//   f32, f32                     318   309       645   631
+//   f32, bf16                    272   271       603   596
+// 2^24 with masters 83.3 and 83.5 us, 160 small tensors 10.1 and 11.2; moments in 8 bits are 5 %
+// slower with 4096 at any size.
 constexpr int kStep = 1024, kChunk = 2 * kStep, kLongChunk = 4 * kStep;
 constexpr int64_t kMany = (int64_t)1 << 26;
 constexpr int kQuantBlock = 256;    // elements per scale: one wave's load

@@ -435,7 +435,7 @@ hipError_t launch_norm_fwd(const T* X, const T* w, const T* b, int64_t rows, int
     return hipGetLastError();                                                                \
   }
   GRPO_ROW_SHAPES(GRPO_CASE)
-  if constexpr (sizeof(T) == 4) {  // 16-bit rows of this length would spill
+  if constexpr (sizeof(T) == 4) {  // 16-bit rows that long would need twice the registers a lane
     GRPO_CASE(1024, 4)
   }
 #undef GRPO_CASE
@@ -462,8 +462,10 @@ hipError_t launch_norm_bwd(const T* dY, const T* X, const T* w, const float* mea
   }
   GRPO_ROW_SHAPES(GRPO_CASE)
   if constexpr (sizeof(T) == 4) {
-    // 128 registers do not hold these rows (81 to 116 spill), but the long rows' three passes take
-    // longer: 4096 x 16384 176 us, 210 with bias, against 295 and 298 (512 rows: 42 and 52 against 40)
+    // 128 registers do not hold these rows (100 spill, with bias 116), but the long rows' passes take
+    // longer: 4096 x 16384 176 us, 210 with bias, against 295 and 298 (512 rows: 42 and 52 against 39
+    // and 40).  The 16-bit form of 512 lanes with four vectors and bias spills 16 (8192 x 12288: 136 us,
+    // 4.4 TB/s).
     GRPO_CASE(1024, 4)
   } else {
     GRPO_CASE(512, 1)

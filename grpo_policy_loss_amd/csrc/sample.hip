@@ -9,7 +9,9 @@
 // A token is right or wrong, so what decides it is computed in 64 bits: a float32 sum over
 // 150 000 tokens would move its borders past u in about one row of a hundred.  Where sums meet
 // in any order (histograms, lists), weights are whole multiples of 2^-42, whose sums over up to
-// 2^20 tokens are exact in 64 bits: no result depends on an order.
+// 2^20 tokens are exact in 64 bits: no result depends on an order.  Each weight of a filtered row is
+// so rounded by up to 2^-43 of the heaviest one's: what lies 30 T below the maximum weighs nothing
+// there, and 10^5 such tokens lose up to 10^-8 of the mass.
 //
 // Rows by what their filters need, each with the fewest passes over the logits:
 //   PLAIN   no filter: one pass for maxima and sums, then one segment of 2048 tokens.
@@ -21,8 +23,11 @@
 //   HIST    top-p, alone or with a larger k: histograms of mass and count over 2048 or 4096 bins of x
 //           tell which bins the cuts fall into; one more pass sums what lies above them and
 //           lists the tokens of those bins, among which the cuts are found.
-// Lists hold up to 4096 tokens; where one overflows (equal logits), the cuts are found among
-// all tokens of the row, by the same search in up to five passes.
+// Lists hold up to 4096 tokens; where one overflows, the cuts are found among all tokens of the row,
+// by the same search in up to five passes of one block.  Equal logits do that, and finite masks where
+// LIST's bins reach from the maximum to the least group's or HIST's, with a k, to the row's minimum:
+// -1e9 in 267 of 151936 tokens leaves all the others in one bin.  64 such rows with top-k 50 take
+// 320 us, with top-p as well 510 us; with -inf there 31 and 32 us.
 #include <math.h>
 
 #include <algorithm>

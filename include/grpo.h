@@ -344,7 +344,9 @@ int grpo_loss_fwd_noalloc(const void* H, const void* W, const int32_t* y, const 
  *   grpo_norm_workspace_bytes(rows, cols, dtype), 256-byte aligned.
  * Y is not X, nor dX dY or X (refused), and outputs overlap no input.
  * Any cols from 1 to 2^24 and any element alignment.  Sums are float32, in a
- * fixed order: results are bitwise reproducible.
+ * fixed order: results are bitwise reproducible.  So are the squares: where a
+ * row's sum of them passes float32's range (|x - mu| about 1e19 / sqrt(cols)),
+ * r is 0 and y the bias.
  */
 typedef enum { GRPO_NORM_LAYER = 0, GRPO_NORM_RMS = 1 } grpo_norm_kind;
 
@@ -428,7 +430,7 @@ int grpo_moment_values(const void* codes, const float* scales, int64_t n, int sq
  * One token for each row of logits [B, V] (GRPO_F32 or GRPO_BF16; row b starts at
  * logits + b * row_stride elements, row_stride >= V), from u [B] float32, one
  * uniform number in [0, 1) per row (a value outside counts as the nearest
- * bound).  The rollout's last step: token [B] int32 becomes y, lp [B] float32
+ * bound, a NaN as 0).  The rollout's last step: token [B] int32 becomes y, lp [B] float32
  * the behaviour policy's log-probability.
  *   z = x / temperature, e = exp(z - max z); the tokens in the order (x down,
  *   index up).  top_k keeps the first top_k; top_p, of those, the ones whose
@@ -439,7 +441,8 @@ int grpo_moment_values(const void* codes, const float* scales, int64_t n, int sq
  *   lp: z[token] - log sum exp z over the whole row, filters or not: what
  *   grpo_loss_fwd_ex gives as lp for that token and temperature.
  * Zeros in opts (or opts = NULL) are "off": temperature 1, no filter; top_k >= V
- * and top_p = 1 are off too, and top_k = 1 takes the largest logit.  The scalars
+ * and top_p = 1 are off too, and top_k = 1 takes the largest logit (temperature
+ * 0 does not: it samples at temperature 1).  The scalars
  * hold for all rows; a non-NULL ..._rows device array [B] gives each row its own
  * instead (there, values out of range are off for the filters; min_p above 1
  * counts as 1).

@@ -89,12 +89,12 @@ def test_both_directions(cols, t, kind):
             check_bwd(i, mean, rstd, dx, dw, db, kind == "layer", bias)
 
 
-# more rows than one round of the grid takes: the forward's 2048 blocks of 64, 16, 4 or 1 rows (by
-# the lanes of a row), the backward's 256 to 1024, and the last round not full
+# more rows than the grid takes at once: the forward's 2048 blocks of 64, 16, 4 or 1 rows (by
+# the lanes of a row), the backward's 256 to 1024, and the last turn not full
 @pytest.mark.parametrize("rows,cols", [(140003, 7), (33333, 100), (9001, 500), (9001, 900), (5003, 1537),
                                        (5003, 2880), (2300, 4096), (2100, 8192), (2100, 16384), (2100, 16387)])
 @pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
-def test_blocks_that_take_several_rounds_of_rows(rows, cols, t):
+def test_blocks_that_take_several_turns_of_rows(rows, cols, t):
     for kind in ("layer", "rms") if cols <= 1537 else ("layer",) if t == torch.float32 else ("rms",):
         i = inputs(rows, cols, t, seed=cols)
         bias = kind == "layer"
