@@ -16,9 +16,9 @@
 // With float32 moments the step is bound by memory: 20 to 30 bytes an element against some 20
 // instructions (233M bf16 weights with masters: 1.09 to 1.21 ms from card to card, 5.8 to 6.4 TB/s).
 // With 8-bit moments 10 bytes stand against some 80, a third of them in float64, and both count (67M
-// bf16 weights: 175 to 181 us, 3.8 TB/s; 245 us with the definition of the codes worked out in every wave that has a root near a
-// border).  One block takes a chunk of one tensor, 4 elements a lane and load, all loads of the
-// chunk issued before its first use.
+// bf16 weights: 175 to 181 us, 3.8 TB/s; 245 us with the definition of the codes worked out in every
+// wave that has a root near a border).  One block takes a chunk of one tensor, 4 elements a lane and
+// load, all loads of the chunk issued before its first use.
 #include <float.h>
 #include <math.h>
 #include <string.h>

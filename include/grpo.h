@@ -344,9 +344,9 @@ int grpo_loss_fwd_noalloc(const void* H, const void* W, const int32_t* y, const 
  *   grpo_norm_workspace_bytes(rows, cols, dtype), 256-byte aligned.
  * Y is not X, nor dX dY or X (refused), and outputs overlap no input.
  * Any cols from 1 to 2^24 and any element alignment.  Sums are float32, in a
- * fixed order: results are bitwise reproducible.  So are the squares: where a
- * row's sum of them passes float32's range (|x - mu| about 1e19 / sqrt(cols)),
- * r is 0 and y the bias.
+ * fixed order: results are bitwise reproducible.  Squares are float32 too:
+ * where a row's sum of them passes its range (|x - mu| of about 1e19 /
+ * sqrt(cols)), r is 0 and y the bias.
  */
 typedef enum { GRPO_NORM_LAYER = 0, GRPO_NORM_RMS = 1 } grpo_norm_kind;
 
