@@ -61,6 +61,24 @@ class SampleOpts(ctypes.Structure):
            ("temperature_rows", "top_p_rows", "min_p_rows", "top_k_rows")]
 
 
+class ClipOpts(ctypes.Structure):
+    """grpo_clip_opts."""
+    _fields_ = [(name, ctypes.c_double) for name in ("clip_low", "clip_high", "clip_dual", "beta")] \
+        + [(name, ctypes.c_int32) for name in ("ratio", "kl_estimator", "aggregation", "adv_per_token")]
+
+
+class PrefOpts(ctypes.Structure):
+    """grpo_pref_opts."""
+    _fields_ = [(name, ctypes.c_double) for name in ("beta", "label_smoothing", "margin", "nll_weight")] \
+        + [(name, ctypes.c_int32) for name in ("kind", "length_mean")]
+
+
+class GradTensor(ctypes.Structure):
+    """grpo_grad_tensor."""
+    _fields_ = [("grad", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 # name -> (restype, argtypes); mirrors include/grpo.h
 SIGNATURES = {
     "grpo_workspace_bytes": (_sz, [_int, _i64, _i64, _i64, _int, _i64]),
@@ -90,6 +108,24 @@ SIGNATURES = {
                                  _f32, _i64, _OPTS_P, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "grpo_loss_bwd_fp8": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
                                  _i64, _i64, _f32, _f32, _i64, _OPTS_P, _vp, _vp, _vp, _sz, _vp]),
+    "grpo_logprobs_fwd": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _int, _i64, _OPTS_P, _vp, _vp,
+                                 _vp, _sz, _vp]),
+    "grpo_logprobs_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _i64,
+                                 _OPTS_P, _int, _vp, _vp, _vp, _sz, _vp]),
+    "grpo_clip_loss_workspace_bytes": (_sz, [_i64, _i64]),
+    "grpo_clip_loss_fwd": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, ctypes.POINTER(ClipOpts), _vp,
+                                  _vp, _vp, _vp, _sz, _vp]),
+    "grpo_clip_loss_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64,
+                                  ctypes.POINTER(ClipOpts), _vp, _vp]),
+    "grpo_pref_loss_workspace_bytes": (_sz, [_i64, _i64]),
+    "grpo_pref_loss_fwd": (_int, [_vp, _vp, _vp, _i64, _i64, ctypes.POINTER(PrefOpts), _vp, _vp, _vp,
+                                  _vp, _sz, _vp]),
+    "grpo_pref_loss_bwd": (_int, [_vp, _vp, _vp, _i64, _i64, _vp, _vp]),
+    "grpo_grad_plan_bytes": (_sz, [_i64]),
+    "grpo_grad_plan": (_int, [ctypes.POINTER(GradTensor), _i64, _vp, _sz]),
+    "grpo_grad_norm_workspace_bytes": (_sz, []),
+    "grpo_grad_norm": (_int, [_vp, _vp, _int, ctypes.c_double, _vp, _vp, _vp, _sz, _vp]),
+    "grpo_grad_clip": (_int, [_vp, _vp, _vp, _vp]),
     "grpo_norm_workspace_bytes": (_sz, [_i64, _i64, _int]),
     "grpo_norm_fwd": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _int, _f32, _vp, _vp, _vp, _vp]),
     "grpo_norm_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _int, _int, _vp, _vp, _vp,

@@ -1,5 +1,6 @@
 """ctypes binding of the operators around the loss (include/grpo.h): the norm in
-front of the LM head, the optimizer's step and the sampling of tokens.
+front of the LM head, the optimizer's step, the gradients' norm and the sampling of
+tokens.
 
 Argument marshalling only, as in _lib.  Every call checks that its tensors share
 one GPU and runs on that GPU's current torch stream, whichever device is current.
@@ -12,7 +13,8 @@ import functools
 
 import torch
 
-from ._lib import (AdamWOpts, AdamWTensor, SampleOpts, _arg, _check, _dev, _dt, _matrix, _ptr, lib)
+from ._lib import (AdamWOpts, AdamWTensor, GradTensor, SampleOpts, _arg, _check, _dev, _dt, _matrix,
+                   _ptr, lib)
 
 # grpo_norm_kind
 NORM_LAYER, NORM_RMS = 0, 1
@@ -273,6 +275,95 @@ def grpo_adamw(plan: AdamWPlan, step, lr=1e-6, betas=(0.9, 0.999), eps: float = 
                                               stream))
     # autograd has to see that the parameters changed
     torch.autograd.graph.increment_version(plan.versioned)
+
+
+# ---------------------------------------------------------------- gradient norm
+# grpo_grad_norm_kind
+GRAD_NORM_L2, GRAD_NORM_MAX = 0, 1
+
+
+class GradPlan:
+    """What grpo_grad_norm and grpo_grad_clip need of the gradients, made once by grad_plan.
+    Like an AdamWPlan it keeps the tensors' memory alive and holds their addresses: gradients
+    that are replaced need a new plan, and holds() tells."""
+
+    def __init__(self, tensors, grads, image, table):
+        self.tensors, self.image, self.table = tensors, image, table
+        self.places = [t.data_ptr() for t in tensors]
+        self.versioned = [g for g in grads if not g.is_inference()]
+        self.device = table.device
+        self.stream = torch._C._cuda_getCurrentRawStream(table.get_device())
+
+    def holds(self, grads) -> bool:
+        """Whether these are still the gradients of the plan, at the addresses that it holds
+        (a gradient of None is not held)."""
+        grads = list(grads)
+        return len(grads) == len(self.tensors) and all(
+            g is not None and g.data_ptr() == a and t.data_ptr() == a and g.numel() == t.numel()
+            and g.dtype == t.dtype for g, t, a in zip(grads, self.tensors, self.places))
+
+
+def grad_plan(grads) -> GradPlan:
+    """The plan of the norm of a list of gradients of one GPU, float32 and bfloat16 in any
+    mixture.  Tensors that share memory are refused."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads is empty")
+    rows = (GradTensor * len(grads))()
+    for i, g in enumerate(grads):
+        _arg(g, f"grads[{i}]")
+        rows[i] = GradTensor(g.data_ptr(), g.numel(), _dt(g), 0)
+    ctx, _ = _on(*grads)
+    size = int(lib().grpo_grad_plan_bytes(len(grads)))
+    image = (ctypes.c_uint8 * size)()
+    _check("grpo_grad_plan", lib().grpo_grad_plan(rows, len(grads), image, size))
+    with ctx:
+        # a copy from pageable memory: it has arrived when the call returns
+        table = torch.frombuffer(image, dtype=torch.uint8).to(grads[0].device)
+        return GradPlan([g.detach() for g in grads], grads, image, table)
+
+
+@functools.lru_cache(maxsize=1)
+def _grad_bytes():
+    return int(lib().grpo_grad_norm_workspace_bytes())
+
+
+def grpo_grad_norm(plan: GradPlan, max_norm: float = 0.0, kind: int = GRAD_NORM_L2, workspace=None):
+    """(norm, scale), float32 tensors of one element: the norm of all gradients of the plan
+    as one vector (of kind GRAD_NORM_L2, or GRAD_NORM_MAX, the largest magnitude), and
+    min(1, max_norm / (norm + 1e-6)), which grpo_adamw takes as its grad_scale and
+    grpo_grad_clip applies in place (max_norm 0: 1).  A captured graph needs the plan to live
+    as long as it does."""
+    need = _grad_bytes()
+    ts = (plan.table,) if workspace is None else (plan.table, _workspace(need, plan.device, workspace))
+    ctx, stream = _on(*ts)
+    with ctx:
+        _keep(plan, stream)
+        norm = torch.empty(1, dtype=torch.float32, device=plan.device)
+        scale = torch.empty(1, dtype=torch.float32, device=plan.device)
+        ws = _workspace(need, plan.device, workspace)
+        _check("grpo_grad_norm", lib().grpo_grad_norm(
+            plan.image, plan.table.data_ptr(), kind, max_norm, norm.data_ptr(), scale.data_ptr(),
+            ws.data_ptr(), ws.numel(), stream))
+    return norm, scale
+
+
+def grpo_grad_clip(plan: GradPlan, scale):
+    """Every gradient of the plan times scale (a float32 tensor of one element), in place,
+    rounded to its type.  For an optimizer that takes no scale of its own."""
+    _arg(scale, "scale", dtype=torch.float32, numel=1)
+    ctx, stream = _on(plan.table, scale)
+    with ctx:
+        _keep(plan, stream)
+        _check("grpo_grad_clip", lib().grpo_grad_clip(plan.image, plan.table.data_ptr(),
+                                                      scale.data_ptr(), stream))
+    # autograd has to see that the gradients changed
+    torch.autograd.graph.increment_version(plan.versioned)
+
+
+def _keep(plan, stream):
+    if stream != plan.stream:   # the allocator must not hand the table on too early
+        plan.table.record_stream(torch.cuda.current_stream(plan.device))
 
 
 # ---------------------------------------------------------------- sampling

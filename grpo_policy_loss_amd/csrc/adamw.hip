@@ -29,6 +29,7 @@
 
 #include "api.hpp"
 #include "elem.hpp"
+#include "plan.hpp"
 #include "timing.hpp"
 
 namespace grpo {
@@ -122,22 +123,6 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   GRPO_STEP(0x143, 0xc);   // row_bcast:31
 #undef GRPO_STEP
   return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-
-// The last tensor whose first chunk is <= chunk: a 64-way search, one load per level.
-// (A tensor of no elements has the first chunk of the next one and is never the last.)
-__device__ __forceinline__ int owner_of(const int64_t* __restrict__ first, int count,
-                                        int64_t chunk) {
-  const int lane = threadIdx.x & 63;
-  int lo = 0, len = count;
-  while (len > 1) {
-    const int stride = (len + 63) / 64;
-    const bool le = lane * stride < len && first[lo + lane * stride] <= chunk;
-    const int k = __popcll(__ballot(le)) - 1;
-    lo += k * stride;
-    len = min(stride, len - k * stride);
-  }
-  return __builtin_amdgcn_readfirstlane(lo);
 }
 
 // The codes from their definition, each operation rounded to float64 (none fused).
@@ -443,25 +428,6 @@ size_t image_bytes(int64_t count) {
   return align_up(sizeof(PlanHeader)) + align_up((size_t)count * sizeof(grpo_adamw_tensor)) +
          align_up((size_t)count * sizeof(int64_t));
 }
-
-struct Range {
-  uintptr_t from, to;
-  bool written;
-};
-
-// Two ranges that share a byte, one of them written, would race.
-bool any_overlap(std::vector<Range>& r) {
-  std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
-  uintptr_t read_end = 0, write_end = 0;
-  for (const Range& x : r) {
-    if (x.from < write_end || (x.written && x.from < read_end)) return true;
-    (x.written ? write_end : read_end) = std::max(x.written ? write_end : read_end, x.to);
-  }
-  return false;
-}
-
-constexpr int64_t kMaxTensors = 1 << 24;
-constexpr int64_t kMaxBlocks = (1 << 24) - 1;   // a grid of 256-thread blocks stays below 2^32 threads
 
 int fill_plan(const grpo_adamw_tensor* tensors, int64_t count, int param_dtype, int grad_dtype,
               int bits, char* image) {

@@ -308,12 +308,15 @@ struct Fp8Recompute {
   float* hs_act = nullptr;
 };
 
+// grad_lp: the loss's gradient with respect to lp is given (mask, adv and ref_lp are not used).
+// A null dH or dW is not formed.
 template <typename T>
 int bwd_pass(const T* H, const T* W, const int32_t* y, const uint8_t* mask, const float* adv,
-             const float* ref_lp, const float* lp, const float* lse, int64_t N, int64_t L,
-             int64_t d, int64_t V, float beta, float grad_loss, int64_t chunk,
-             const grpo::LogitXform& xf, const grpo::LossVariant& lv, T* dH, float* dW,
-             const BwdPlan& p, char* ws, hipStream_t s, const Fp8Recompute& f8 = Fp8Recompute()) {
+             const float* ref_lp, const float* lp, const float* lse, const float* grad_lp,
+             int64_t N, int64_t L, int64_t d, int64_t V, float beta, float grad_loss,
+             int64_t chunk, const grpo::LogitXform& xf, const grpo::LossVariant& lv, T* dH,
+             float* dW, const BwdPlan& p, char* ws, hipStream_t s,
+             const Fp8Recompute& f8 = Fp8Recompute()) {
   int32_t* idx = (int32_t*)(ws + p.o_idx);
   int32_t* cnt = (int32_t*)(ws + p.o_cnt);
   T* H_act = (T*)(ws + p.o_hact);
@@ -327,8 +330,9 @@ int bwd_pass(const T* H, const T* W, const int32_t* y, const uint8_t* mask, cons
   int32_t* seq_n = lv.seq_mean ? (int32_t*)(ws + p.o_seq) : nullptr;
   const int64_t B = N / L;
 
-  GRPO_HIP(grpo::launch_zero(dH, (size_t)(N * d) * sizeof(T), s));
-  GRPO_HIP(grpo::launch_active_scan(mask, N, idx, cnt, s));
+  if (dH != nullptr) GRPO_HIP(grpo::launch_zero(dH, (size_t)(N * d) * sizeof(T), s));
+  if (grad_lp != nullptr) GRPO_HIP(grpo::launch_active_scan(grad_lp, N, idx, cnt, s));
+  else GRPO_HIP(grpo::launch_active_scan(mask, N, idx, cnt, s));
   if (seq_n != nullptr) GRPO_HIP(grpo::launch_seq_counts(mask, B, L, seq_n, s));
   // Chunks are planned for the worst case (every token active); chunks past
   // the device-side active count exit at once, so no host sync is needed.
@@ -336,9 +340,9 @@ int bwd_pass(const T* H, const T* W, const int32_t* y, const uint8_t* mask, cons
     const int64_t c0 = c * p.C;
     const int C = (int)p.C;
     GRPO_HIP(grpo::launch_bwd_prep<T>(H, d, idx, cnt, c0, C, (int)p.cpad, y, mask, adv, ref_lp, lp,
-                                      lse, L, beta, grad_loss, xf, lv, seq_n, B, H_act, coef,
+                                      lse, grad_lp, L, beta, grad_loss, xf, lv, seq_n, B, H_act, coef,
                                       lse_c, y_c, tgt_c, s));
-    GRPO_HIP(grpo::launch_transpose<T>(H_act, p.cpad, d, HT, p.cpad, s));
+    if (dW != nullptr) GRPO_HIP(grpo::launch_transpose<T>(H_act, p.cpad, d, HT, p.cpad, s));
     if (f8.H8 != nullptr)
       GRPO_HIP(grpo::launch_fp8_gather_rows(f8.H8, f8.h_scale, d, idx, cnt, c0, C, (int)p.cpad,
                                             f8.H8_act, f8.hs_act, s));
@@ -353,11 +357,14 @@ int bwd_pass(const T* H, const T* W, const int32_t* y, const uint8_t* mask, cons
         GRPO_HIP(grpo::launch_dz<T>(W, H_act, d, V, v0, vs_valid, (int)p.vs, cnt, c0, C,
                                     (int)p.cpad, xf, nullptr, nullptr, coef, lse_c, y_c, tgt_c,
                                     dZ, s));
-      GRPO_HIP(grpo::launch_dh_gemm<T>(W, v0, vs_valid, dZ, (int)p.vs, d, cnt, c0, C, (int)p.cpad,
-                                       (int)p.nsplit, sl == 0 ? 1 : 0, dH_acc, s));
-      GRPO_HIP(grpo::launch_dw_gemm<T>(HT, (int)p.cpad, dZ, (int)p.vs, d, v0, vs_valid, cnt, c0,
-                                       C, dW, s));
+      if (dH != nullptr)
+        GRPO_HIP(grpo::launch_dh_gemm<T>(W, v0, vs_valid, dZ, (int)p.vs, d, cnt, c0, C,
+                                         (int)p.cpad, (int)p.nsplit, sl == 0 ? 1 : 0, dH_acc, s));
+      if (dW != nullptr)
+        GRPO_HIP(grpo::launch_dw_gemm<T>(HT, (int)p.cpad, dZ, (int)p.vs, d, v0, vs_valid, cnt, c0,
+                                         C, dW, s));
     }
+    if (dH == nullptr) continue;
     GRPO_HIP(grpo::launch_dh_scatter<T>(dH_acc, (int)p.nsplit, (int)p.cpad, d, idx, cnt, c0, C, dH,
                                         s));
   }
@@ -574,12 +581,12 @@ int grpo_loss_bwd_ex(const void* H, const void* W, const int32_t* y, const uint8
                 workspace == nullptr ? (size_t)0 : workspace_bytes);
   hipStream_t s = (hipStream_t)stream;
   if (dtype == GRPO_BF16)
-    return bwd_pass<__bf16>((const __bf16*)H, (const __bf16*)W, y, mask, adv, ref_lp, lp, lse, N,
-                            L, d, V, beta, grad_loss, chunk, xf, lv, (__bf16*)dH, dW, p,
+    return bwd_pass<__bf16>((const __bf16*)H, (const __bf16*)W, y, mask, adv, ref_lp, lp, lse,
+                            nullptr, N, L, d, V, beta, grad_loss, chunk, xf, lv, (__bf16*)dH, dW, p,
                             (char*)workspace, s);
-  return bwd_pass<float>((const float*)H, (const float*)W, y, mask, adv, ref_lp, lp, lse, N, L, d,
-                         V, beta, grad_loss, chunk, xf, lv, (float*)dH, dW, p, (char*)workspace,
-                         s);
+  return bwd_pass<float>((const float*)H, (const float*)W, y, mask, adv, ref_lp, lp, lse, nullptr,
+                         N, L, d, V, beta, grad_loss, chunk, xf, lv, (float*)dH, dW, p,
+                         (char*)workspace, s);
 }
 
 int grpo_loss_bwd(const void* H, const void* W, const int32_t* y, const uint8_t* mask,
@@ -589,6 +596,75 @@ int grpo_loss_bwd(const void* H, const void* W, const int32_t* y, const uint8_t*
                   size_t workspace_bytes, void* stream) {
   return grpo_loss_bwd_ex(H, W, y, mask, adv, ref_lp, lp, lse, B, L, d, V, dtype, beta,
                           grad_loss, chunk, nullptr, dH, dW, workspace, workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------- log-probabilities with a gradient
+int grpo_logprobs_fwd(const void* H, const void* W, const int32_t* y, int64_t N, int64_t d,
+                      int64_t V, int dtype, int64_t chunk, const grpo_opts* opts, float* lp,
+                      float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  grpo::clear_error();
+  grpo::LogitXform xf;
+  grpo::LossVariant lv;
+  if (make_xform(opts, &xf) != GRPO_OK || make_variant(opts, &lv) != GRPO_OK)
+    return GRPO_ERR_INVALID_ARG;
+  GRPO_CHECK_PTR(H);
+  GRPO_CHECK_PTR(W);
+  GRPO_CHECK_PTR(y);
+  GRPO_CHECK_PTR(lp);
+  GRPO_CHECK_PTR(lse);
+  const int st = check_shape(N, d, V, dtype, chunk);
+  if (st != GRPO_OK) return st;
+  const size_t need = plan_fwd(N, V, chunk).total;
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(GRPO_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
+                workspace == nullptr ? (size_t)0 : workspace_bytes);
+  hipStream_t s = (hipStream_t)stream;
+  if (dtype == GRPO_BF16)
+    return lse_pass<__bf16>(0, (const __bf16*)H, (const __bf16*)W, y, nullptr, nullptr, nullptr, N,
+                            1, d, V, 0.f, chunk, xf, lv, nullptr, lp, nullptr, lse,
+                            (char*)workspace, s);
+  return lse_pass<float>(0, (const float*)H, (const float*)W, y, nullptr, nullptr, nullptr, N, 1, d,
+                         V, 0.f, chunk, xf, lv, nullptr, lp, nullptr, lse, (char*)workspace, s);
+}
+
+int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const float* lp,
+                      const float* lse, const float* grad_lp, int64_t N, int64_t d, int64_t V,
+                      int dtype, int64_t chunk, const grpo_opts* opts, int accumulate, void* dH,
+                      float* dW, void* workspace, size_t workspace_bytes, void* stream) {
+  grpo::clear_error();
+  grpo::LogitXform xf;
+  grpo::LossVariant lv;
+  if (make_xform(opts, &xf) != GRPO_OK || make_variant(opts, &lv) != GRPO_OK)
+    return GRPO_ERR_INVALID_ARG;
+  GRPO_CHECK_PTR(H);
+  GRPO_CHECK_PTR(W);
+  GRPO_CHECK_PTR(y);
+  GRPO_CHECK_PTR(lp);
+  GRPO_CHECK_PTR(lse);
+  GRPO_CHECK_PTR(grad_lp);
+  if (dH == nullptr && dW == nullptr) return fail(GRPO_ERR_INVALID_ARG, "null pointer: both dH and dW");
+  if (accumulate != 0 && accumulate != 1)
+    return fail(GRPO_ERR_INVALID_ARG, "accumulate %d is not 0 or 1", accumulate);
+  const int st = check_shape(N, d, V, dtype, chunk);
+  if (st != GRPO_OK) return st;
+  // a caller's size is always a size, as in grpo_loss_bwd_ex
+  const int64_t wsb = std::max<int64_t>(1, (int64_t)std::min<size_t>(workspace_bytes, (size_t)INT64_MAX));
+  const BwdPlan p = plan_bwd(N, d, V, dtype, chunk, workspace == nullptr ? 1 : wsb);
+  if (workspace == nullptr || !p.ok)
+    return fail(GRPO_ERR_WORKSPACE, "workspace needs at least %zu bytes, got %zu",
+                plan_bwd(N, d, V, dtype, chunk, -1).total,
+                workspace == nullptr ? (size_t)0 : workspace_bytes);
+  hipStream_t s = (hipStream_t)stream;
+  lv = grpo::LossVariant{0, 0, 0};
+  if (dW != nullptr && !accumulate)
+    GRPO_HIP(grpo::launch_zero(dW, (size_t)(V * d) * 4, s));
+  if (dtype == GRPO_BF16)
+    return bwd_pass<__bf16>((const __bf16*)H, (const __bf16*)W, y, nullptr, nullptr, nullptr, lp,
+                            lse, grad_lp, N, 1, d, V, 0.f, 0.f, chunk, xf, lv, (__bf16*)dH, dW, p,
+                            (char*)workspace, s);
+  return bwd_pass<float>((const float*)H, (const float*)W, y, nullptr, nullptr, nullptr, lp, lse,
+                         grad_lp, N, 1, d, V, 0.f, 0.f, chunk, xf, lv, (float*)dH, dW, p,
+                         (char*)workspace, s);
 }
 
 // ---------------------------------------------------------------- fp8 e4m3 path
@@ -761,8 +837,8 @@ int grpo_loss_bwd_fp8(const uint8_t* H8, const float* h_scale, const uint8_t* W8
   f8.w_scale = w_scale;
   f8.H8_act = (uint8_t*)(ws + p.o_h8act);
   f8.hs_act = (float*)(ws + p.o_hsact);
-  return bwd_pass<__bf16>(Hb, Wb, y, mask, adv, ref_lp, lp, lse, N, L, d, V, beta, grad_loss, chunk,
-                          xf, lv, (__bf16*)dH, dW, p.b, ws + p.o_bf16, s, f8);
+  return bwd_pass<__bf16>(Hb, Wb, y, mask, adv, ref_lp, lp, lse, nullptr, N, L, d, V, beta,
+                          grad_loss, chunk, xf, lv, (__bf16*)dH, dW, p.b, ws + p.o_bf16, s, f8);
 }
 
 }  // extern "C"

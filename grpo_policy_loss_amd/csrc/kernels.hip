@@ -448,8 +448,8 @@ __global__ void __launch_bounds__(256)
     const int32_t yt = y[tg];
     const float lp = (yt >= 0 && yt < V) ? zy[t] - lse : __builtin_nanf("");
     out_lp[tg] = lp;
+    if (out_lse != nullptr) out_lse[tg] = lse;
     if (mode == 1) {
-      out_lse[tg] = lse;
       const float x = ref_lp[tg] - lp;
       const float kl = kl_value(lv.kl, x, lp);
       out_kl[tg] = kl;
@@ -512,9 +512,11 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------- backward helpers
-// Indices of the unmasked tokens in increasing order, and their count.
+// Indices of the unmasked tokens in increasing order, and their count (M = float: of those whose
+// gradient is not 0, NaN among them).
+template <typename M>
 __global__ void __launch_bounds__(1024)
-    k_active_scan(const uint8_t* __restrict__ mask, int64_t N, int32_t* __restrict__ idx,
+    k_active_scan(const M* __restrict__ mask, int64_t N, int32_t* __restrict__ idx,
                   int32_t* __restrict__ count) {
   __shared__ int sc[1024];
   const int tid = threadIdx.x;
@@ -575,15 +577,16 @@ __global__ void __launch_bounds__(256)
 }
 
 // Gather the hidden states of chunk c's active tokens into H_act and form
-// the per-token backward coefficient c_t, lse and target; padding rows are 0.
+// the per-token backward coefficient c_t (grad_lp's, where that is given), lse
+// and target; padding rows are 0.
 template <typename T>
 __global__ void __launch_bounds__(256)
     k_bwd_prep(const T* __restrict__ H, int64_t d, const int32_t* __restrict__ idx,
                const int32_t* __restrict__ count, int64_t c0, int C,
                const int32_t* __restrict__ y, const float* __restrict__ adv,
                const float* __restrict__ ref_lp, const float* __restrict__ lp,
-               const float* __restrict__ lse, int64_t L, float beta, float grad_loss,
-               LogitXform xf, LossVariant lv, const int32_t* __restrict__ seq_n, int64_t B,
+               const float* __restrict__ lse, const float* __restrict__ grad_lp, int64_t L,
+               float beta, float grad_loss, LogitXform xf, LossVariant lv, const int32_t* __restrict__ seq_n, int64_t B,
                T* __restrict__ H_act, float* __restrict__ coef,
                float* __restrict__ lse_c, int32_t* __restrict__ y_c, float* __restrict__ tgt_c) {
   const int cnt = count[0];
@@ -599,14 +602,19 @@ __global__ void __launch_bounds__(256)
     if (valid) {
       // c_t = d loss / d lp_t = w_t (-[detached] A + beta d kl / d lp), w_t the
       // aggregation weight of an unmasked token
-      const float x = ref_lp[t] - lp[t];
-      const int64_t b = t / L;
-      const float scale =
-          seq_n != nullptr
-              ? grad_loss / ((float)B * (float)(seq_n[b] > 0 ? seq_n[b] : 1))
-              : grad_loss / (float)(cnt > 0 ? cnt : 1);
-      const float a_term = lv.no_detach ? 0.f : -adv[b];
-      const float c = scale * (a_term + beta * kl_slope(lv.kl, x, lp[t]));
+      float c;
+      if (grad_lp != nullptr) {
+        c = grad_lp[t];
+      } else {
+        const float x = ref_lp[t] - lp[t];
+        const int64_t b = t / L;
+        const float scale =
+            seq_n != nullptr
+                ? grad_loss / ((float)B * (float)(seq_n[b] > 0 ? seq_n[b] : 1))
+                : grad_loss / (float)(cnt > 0 ? cnt : 1);
+        const float a_term = lv.no_detach ? 0.f : -adv[b];
+        c = scale * (a_term + beta * kl_slope(lv.kl, x, lp[t]));
+      }
       coef[j] = c;
       lse_c[j] = lse[t];
       y_c[j] = y[t];
@@ -1159,10 +1167,11 @@ hipError_t launch_seq_counts(const uint8_t* mask, int64_t B, int64_t L, int32_t*
   return hipGetLastError();
 }
 
-hipError_t launch_active_scan(const uint8_t* mask, int64_t N, int32_t* idx, int32_t* count,
+template <typename M>
+hipError_t launch_active_scan(const M* mask, int64_t N, int32_t* idx, int32_t* count,
                               hipStream_t s) {
   ScopedKernelTimer timer_(KK_ACTIVE_SCAN, s);
-  hipLaunchKernelGGL(k_active_scan, dim3(1), dim3(1024), 0, s, mask, N, idx, count);
+  hipLaunchKernelGGL(k_active_scan<M>, dim3(1), dim3(1024), 0, s, mask, N, idx, count);
   return hipGetLastError();
 }
 
@@ -1179,15 +1188,15 @@ template <typename T>
 hipError_t launch_bwd_prep(const T* H, int64_t d, const int32_t* idx, const int32_t* count,
                            int64_t c0, int C, int cpad, const int32_t* y, const uint8_t* mask,
                            const float* adv, const float* ref_lp, const float* lp,
-                           const float* lse, int64_t L, float beta, float grad_loss,
-                           const LogitXform& xf, const LossVariant& lv, const int32_t* seq_n,
-                           int64_t B, T* H_act, float* coef, float* lse_c, int32_t* y_c,
-                           float* tgt_c, hipStream_t s) {
+                           const float* lse, const float* grad_lp, int64_t L, float beta,
+                           float grad_loss, const LogitXform& xf, const LossVariant& lv,
+                           const int32_t* seq_n, int64_t B, T* H_act, float* coef, float* lse_c,
+                           int32_t* y_c, float* tgt_c, hipStream_t s) {
   ScopedKernelTimer timer_(KK_BWD_PREP, s);
   (void)mask;
   hipLaunchKernelGGL(k_bwd_prep<T>, dim3(cpad), dim3(256), 0, s, H, d, idx, count, c0, C, y, adv,
-                     ref_lp, lp, lse, L, beta, grad_loss, xf, lv, seq_n, B, H_act, coef, lse_c,
-                     y_c, tgt_c);
+                     ref_lp, lp, lse, grad_lp, L, beta, grad_loss, xf, lv, seq_n, B, H_act, coef,
+                     lse_c, y_c, tgt_c);
   return hipGetLastError();
 }
 
@@ -1300,7 +1309,7 @@ hipError_t launch_gemm_nt(const T* A, const T* B, int64_t M, int64_t N, int64_t 
   template hipError_t launch_bwd_prep<T>(const T*, int64_t, const int32_t*, const int32_t*,       \
                                          int64_t, int, int, const int32_t*, const uint8_t*,        \
                                          const float*, const float*, const float*, const float*,  \
-                                         int64_t, float, float, const LogitXform&,                \
+                                         const float*, int64_t, float, float, const LogitXform&,  \
                                          const LossVariant&, const int32_t*, int64_t, T*, float*,  \
                                          float*, int32_t*, float*, hipStream_t);                  \
   template hipError_t launch_dz<T>(const T*, const T*, int64_t, int64_t, int64_t, int, int,       \
@@ -1317,6 +1326,10 @@ hipError_t launch_gemm_nt(const T* A, const T* B, int64_t M, int64_t N, int64_t 
   template hipError_t launch_gemm_nt<T>(const T*, const T*, int64_t, int64_t, int64_t, float*,    \
                                         hipStream_t);
 
+template hipError_t launch_active_scan<uint8_t>(const uint8_t*, int64_t, int32_t*, int32_t*,
+                                                hipStream_t);
+template hipError_t launch_active_scan<float>(const float*, int64_t, int32_t*, int32_t*,
+                                              hipStream_t);
 GRPO_INSTANTIATE(float)
 GRPO_INSTANTIATE(__bf16)
 template hipError_t launch_dz<uint8_t>(const uint8_t*, const uint8_t*, int64_t, int64_t, int64_t,

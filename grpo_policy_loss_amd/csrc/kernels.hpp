@@ -56,7 +56,7 @@ hipError_t launch_fp8_dequantize(const uint8_t* codes, int64_t rows, int64_t col
                                  const float* scales, int per_row, __bf16* out, hipStream_t s);
 
 // Merge the partials of one chunk (tokens c0 .. c0 + n_tok - 1).
-// mode 0: reference log-probs -> out_lp.  mode 1: loss forward.
+// mode 0: log-probs -> out_lp, and lse -> out_lse unless that is null.  mode 1: loss forward.
 // seq_n (per-sequence unmasked counts) is null for the token mean.
 hipError_t launch_lse_merge(int mode, const float* part_m, const float* part_s, const float* zy,
                             int S, int cpad, int n_tok, int64_t c0, const int32_t* y, int64_t V,
@@ -72,22 +72,24 @@ hipError_t launch_loss_final(const double* loss_part, const int* cnt_part, int n
 // n[b] = unmasked tokens of sequence b (B sequences of L tokens).
 hipError_t launch_seq_counts(const uint8_t* mask, int64_t B, int64_t L, int32_t* n, hipStream_t s);
 
-// Backward helpers.
-hipError_t launch_active_scan(const uint8_t* mask, int64_t N, int32_t* idx, int32_t* count,
+// Backward helpers.  M: uint8_t (a mask) or float (gradients: the tokens whose own is not 0).
+template <typename M>
+hipError_t launch_active_scan(const M* mask, int64_t N, int32_t* idx, int32_t* count,
                               hipStream_t s);
 
 template <typename T>
 hipError_t launch_transpose(const T* in, int64_t R, int64_t Cc, T* out, int64_t Rpad,
                             hipStream_t s);
 
+// grad_lp: the tokens' coefficients (then adv, ref_lp and what the loss has are not used), or null.
 template <typename T>
 hipError_t launch_bwd_prep(const T* H, int64_t d, const int32_t* idx, const int32_t* count,
                            int64_t c0, int C, int cpad, const int32_t* y, const uint8_t* mask,
                            const float* adv, const float* ref_lp, const float* lp,
-                           const float* lse, int64_t L, float beta, float grad_loss,
-                           const LogitXform& xf, const LossVariant& lv, const int32_t* seq_n,
-                           int64_t B, T* H_act, float* coef, float* lse_c, int32_t* y_c,
-                           float* tgt_c, hipStream_t s);
+                           const float* lse, const float* grad_lp, int64_t L, float beta,
+                           float grad_loss, const LogitXform& xf, const LossVariant& lv,
+                           const int32_t* seq_n, int64_t B, T* H_act, float* coef, float* lse_c,
+                           int32_t* y_c, float* tgt_c, hipStream_t s);
 
 // Element type of the dZ slabs: bfloat16 for fp8 operands, the operand type otherwise.
 template <typename T> struct DzOut { typedef T type; };

@@ -23,7 +23,8 @@ const char* const kNames[KK_COUNT] = {
     "bwd_prep",   "dz",           "dh_gemm",   "dw_gemm",    "dh_scatter",  "zero",
     "gemm_nt",    "seq_counts", "fp8_quantize", "fp8_dequantize",
     "norm_fwd", "norm_bwd", "norm_reduce", "adamw", "moment_values", "sample_mass", "sample_cut",
-    "sample_pick"};
+    "sample_pick", "clip_loss_fwd", "clip_loss_bwd", "pref_loss_fwd", "pref_loss_bwd",
+    "loss_finish", "grad_norm", "grad_norm_finish", "grad_clip"};
 
 }  // namespace
 

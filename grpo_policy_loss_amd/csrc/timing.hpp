@@ -35,6 +35,14 @@ enum KernelKind {
   KK_SAMPLE_MASS,
   KK_SAMPLE_CUT,
   KK_SAMPLE_PICK,
+  KK_CLIP_FWD,
+  KK_CLIP_BWD,
+  KK_PREF_FWD,
+  KK_PREF_BWD,
+  KK_LOSS_FINISH,
+  KK_GRAD_NORM,
+  KK_GRAD_FINISH,
+  KK_GRAD_CLIP,
   KK_COUNT
 };
 

@@ -328,6 +328,147 @@ int grpo_loss_fwd_noalloc(const void* H, const void* W, const int32_t* y, const 
                           float* loss, float* lp, float* kl, float* lse, void* stream);
 
 /*
+ * The log-probabilities of the targets and their gradient, for a loss of the caller's own over
+ * them (grpo_clip_loss_*, grpo_pref_loss_*):
+ *   lp_t = z_{t, y_t} - lse_t,  dZ_t = g_t (onehot(y_t) - softmax(z_t)) dz/d(w h)
+ *   dH_t = dZ_t W               dW += sum_t dZ_t^T h_t
+ * with z the transformed logits of the opts (NULL: plain) and g = grad_lp, the loss's gradient
+ * with respect to lp.  The kernels of grpo_loss_fwd and grpo_loss_bwd.
+ * grpo_logprobs_fwd: lp and lse [N] float32, written; workspace
+ *   grpo_workspace_bytes(GRPO_OP_FWD, ...).
+ * grpo_logprobs_bwd: lp and lse as the forward of the same inputs and opts wrote them.  A token with
+ *   g_t = 0 is not visited, whatever its other values are: its row of dH is 0.  dH [N, d] dtype,
+ *   OVERWRITTEN; dW [V, d] float32, ACCUMULATED if accumulate is 1, OVERWRITTEN if it is 0; either
+ *   may be NULL and is then not formed.  workspace as in grpo_loss_bwd.
+ * dtype GRPO_F32 or GRPO_BF16.  Only the logit transform of the opts is used.
+ */
+int grpo_logprobs_fwd(const void* H, const void* W, const int32_t* y, int64_t N, int64_t d,
+                      int64_t V, int dtype, int64_t chunk, const grpo_opts* opts, float* lp,
+                      float* lse, void* workspace, size_t workspace_bytes, void* stream);
+int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const float* lp,
+                      const float* lse, const float* grad_lp, int64_t N, int64_t d, int64_t V,
+                      int dtype, int64_t chunk, const grpo_opts* opts, int accumulate, void* dH,
+                      float* dW, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The clipped policy loss over given log-probabilities, for steps in which the policy is no longer
+ * the one that sampled.  For the unmasked tokens t = b L + j of B sequences, n_b of them in b, n in
+ * all, with D = lp - old_lp (0 where old_lp is NULL):
+ *   r = exp(D_t)                              (GRPO_RATIO_TOKEN)
+ *   r = exp(sum_j m D / n_b)                  (GRPO_RATIO_SEQUENCE: the same for all tokens of b)
+ *   s = min(r, 1 + clip_high) where A >= 0, min(max(r, 1 - clip_low), clip_dual) where A < 0
+ *   l = -A s + beta kl(ref_lp - lp, lp)       kl as in grpo_opts; no term where ref_lp is NULL
+ *   loss = sum_t m_t l_t / max(n, 1), or (1/B) sum_b sum_j m l / max(n_b, 1)
+ * and its gradient with respect to lp (with w_t the weight of l_t in the loss):
+ *   g_t = w_t ((s = r ? -A r : 0) + beta dkl/dlp)
+ * What masked places hold (NaN, infinities) plays no part.  Which side of a border a ratio is on is
+ * decided in float64 by its logarithm; sums are float64, in a fixed order.
+ *   lp, old_lp (NULL), ref_lp (NULL) [N] float32; mask [N] uint8; adv float32 [B], or [N] if
+ *   adv_per_token is 1 (GRPO_RATIO_TOKEN only).
+ * grpo_clip_loss_fwd: loss [1] and stats [4] float32, written: over the unmasked tokens the mean of kl
+ *   (0 without ref_lp), the share of tokens with s > r, the share with s < r, and the mean of
+ *   r - 1 - log r (an estimate of the divergence from the old policy).  weights [2 B + 1] float32, written, for
+ *   the backward.  workspace: grpo_clip_loss_workspace_bytes(B, L), 256-byte aligned.
+ * grpo_clip_loss_bwd: grad_lp [N] float32, OVERWRITTEN (0 where masked) = g times *grad_loss (a device
+ *   scalar; NULL: 1).  Other arguments and opts are the forward's.
+ * opts (NULL: all zeros): zeros are "off": no clipping on that side, no KL term.  clip_low, clip_high
+ * finite and >= 0, clip_dual 0 or finite and > 1, beta finite.  beta != 0 needs ref_lp.
+ * B * L must fit int32.
+ */
+typedef enum { GRPO_RATIO_TOKEN = 0, GRPO_RATIO_SEQUENCE = 1 } grpo_ratio;
+
+typedef struct grpo_clip_opts {
+  double clip_low;
+  double clip_high;
+  double clip_dual;
+  double beta;
+  int32_t ratio;          /* grpo_ratio */
+  int32_t kl_estimator;   /* grpo_kl_estimator */
+  int32_t aggregation;    /* grpo_aggregation */
+  int32_t adv_per_token;  /* 0 or 1 */
+} grpo_clip_opts;
+
+size_t grpo_clip_loss_workspace_bytes(int64_t B, int64_t L);
+int grpo_clip_loss_fwd(const float* lp, const float* old_lp, const float* ref_lp,
+                       const uint8_t* mask, const float* adv, int64_t B, int64_t L,
+                       const grpo_clip_opts* opts, float* loss, float* stats, float* weights,
+                       void* workspace, size_t workspace_bytes, void* stream);
+int grpo_clip_loss_bwd(const float* lp, const float* old_lp, const float* ref_lp,
+                       const uint8_t* mask, const float* adv, const float* weights,
+                       const float* grad_loss, int64_t B, int64_t L, const grpo_clip_opts* opts,
+                       float* grad_lp, void* stream);
+
+/*
+ * The preference loss over P pairs of sequences of padded length L: sequence 2p is the chosen one of
+ * pair p, 2p + 1 the rejected one (N = 2 P L tokens).  For sequence b with n_b unmasked tokens:
+ *   s_b = sum_j m (lp - ref_lp)     (without ref_lp, which may be NULL: sum_j m lp)
+ *         divided by max(n_b, 1) if length_mean is 1
+ *   h = s_{2p} - s_{2p+1},  x = beta h - margin
+ *   l = -(1 - label_smoothing) log sigmoid(x) - label_smoothing log sigmoid(-x)   GRPO_PREF_SIGMOID
+ *       max(0, 1 - x)                                                            GRPO_PREF_HINGE
+ *       (h - margin - 1 / (2 beta))^2                                            GRPO_PREF_SQUARE
+ *   l += nll_weight (-sum_j m lp_{2p} / max(n_{2p}, 1))
+ *   loss = (1/P) sum_p l
+ * grpo_pref_loss_fwd: loss [1], rewards [2 P] = beta s_b and weights [2 P] (the loss's gradient with
+ *   respect to each unmasked lp of a sequence) float32, written.  workspace:
+ *   grpo_pref_loss_workspace_bytes(P, L), 256-byte aligned.
+ * grpo_pref_loss_bwd: grad_lp [N] float32, OVERWRITTEN (0 where masked): the sequence's weight times
+ *   *grad_loss (a device scalar; NULL: 1).
+ * What masked places hold plays no part.  beta finite and > 0, margin and nll_weight finite,
+ * nll_weight >= 0, label_smoothing in [0, 1) and, but for GRPO_PREF_SIGMOID, 0.  2 P L must fit int32.
+ */
+typedef enum { GRPO_PREF_SIGMOID = 0, GRPO_PREF_HINGE = 1, GRPO_PREF_SQUARE = 2 } grpo_pref_kind;
+
+typedef struct grpo_pref_opts {
+  double beta;
+  double label_smoothing;
+  double margin;
+  double nll_weight;
+  int32_t kind;         /* grpo_pref_kind */
+  int32_t length_mean;  /* 0 or 1 */
+} grpo_pref_opts;
+
+size_t grpo_pref_loss_workspace_bytes(int64_t P, int64_t L);
+int grpo_pref_loss_fwd(const float* lp, const float* ref_lp, const uint8_t* mask, int64_t P,
+                       int64_t L, const grpo_pref_opts* opts, float* loss, float* rewards,
+                       float* weights, void* workspace, size_t workspace_bytes, void* stream);
+int grpo_pref_loss_bwd(const uint8_t* mask, const float* weights, const float* grad_loss,
+                       int64_t P, int64_t L, float* grad_lp, void* stream);
+
+/*
+ * The norm of many gradients as one vector, and the factor that clips it: what grpo_adamw takes as
+ * grad_scale.
+ *   norm  = sqrt(sum g^2) (GRPO_GRAD_NORM_L2) or max |g| (GRPO_GRAD_NORM_MAX)
+ *   scale = min(1, max_norm / (norm + 1e-6)), or 1 if max_norm is 0
+ * A NaN makes both NaN (scale 1 if max_norm is 0); infinities make norm inf and scale 0.
+ * grpo_grad_plan (host only) checks the tensors and writes the table into the HOST buffer `image`
+ *   of grpo_grad_plan_bytes(count) bytes, to be copied to device memory once (8-byte aligned) and
+ *   passed along with it, as in grpo_adamw_plan.  Types may be mixed; n = 0 is allowed; tensors that
+ *   share memory are refused.  At most 2^24 tensors, and 2^24 - 1 chunks of 8192 elements.
+ * grpo_grad_norm: norm [1] and scale [1] float32, written.  Squares and sums are float64, in a fixed
+ *   order: nothing overflows, and results are bitwise reproducible.  max_norm finite and >= 0.  workspace:
+ *   grpo_grad_norm_workspace_bytes(), 256-byte aligned.
+ * grpo_grad_clip: every gradient times *scale (a device scalar), in place, rounded to its type;
+ *   nothing is touched where it is 1.
+ */
+typedef enum { GRPO_GRAD_NORM_L2 = 0, GRPO_GRAD_NORM_MAX = 1 } grpo_grad_norm_kind;
+
+typedef struct grpo_grad_tensor {
+  void* grad;
+  int64_t n;
+  int32_t dtype;     /* GRPO_F32 or GRPO_BF16 */
+  int32_t reserved;  /* not read */
+} grpo_grad_tensor;
+
+size_t grpo_grad_plan_bytes(int64_t count);
+int grpo_grad_plan(const grpo_grad_tensor* tensors, int64_t count, void* image,
+                   size_t image_bytes);
+size_t grpo_grad_norm_workspace_bytes(void);
+int grpo_grad_norm(const void* image, const void* plan, int kind, double max_norm, float* norm,
+                   float* scale, void* workspace, size_t workspace_bytes, void* stream);
+int grpo_grad_clip(const void* image, const void* plan, const float* scale, void* stream);
+
+/*
  * The norm in front of the LM head, whose output is H and whose backward takes
  * dH.  For each row x of X [rows, cols]:
  *   mu = mean(x) (GRPO_NORM_LAYER; 0 for GRPO_NORM_RMS)

@@ -1,0 +1,183 @@
+"""The log-probabilities with their gradient on the GPU, against the formulas in float64 and within
+the bounds that tests/plain_update.py counts."""
+import math
+
+import pytest
+import torch
+
+import grpo_policy_loss_amd as gp
+from tests import plain_update
+
+pytestmark = pytest.mark.gpu
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+HALF = {"f32": plain_update.U, "bf16": 2.0 ** -8}
+
+
+def inputs(N, d, V, t, seed=0, dead=0.3):
+    g = torch.Generator().manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    W = (rnd(V, d) / math.sqrt(d)).to(TYPES[t])
+    y = torch.randint(0, V, (N,), generator=g, dtype=torch.int32)
+    H = rnd(N, d) + 6 * torch.rand(N, 1, generator=g) * W[y.long()].float()     # some targets are likely
+    up = rnd(N) * (torch.rand(N, generator=g) >= dead)
+    return dict(H=H.to(TYPES[t]).cuda(), W=W.cuda(), y=y.cuda(), g=up.cuda())
+
+
+def check(i, t, chunk=4096, opts=None, k=1.0, cap=0.0):
+    lp, lse = gp.grpo_logprobs_fwd(i["H"], i["W"], i["y"], chunk, opts=opts)
+    dH, dW = gp.grpo_logprobs_bwd(i["H"], i["W"], i["y"], lp, lse, i["g"], chunk, opts=opts)
+    want = plain_update.logprobs(i["H"], i["W"], i["y"], i["g"], k=k, cap=cap, half=HALF[t])
+    for name, x in (("lp", lp), ("dH", dH), ("dW", dW)):
+        over = (x.cpu().double() - want[name]).abs() - want[name + "_tol"]
+        assert (over <= 0).all(), (name, over.max())
+    assert not dH[i["g"] == 0].any()
+    return lp, lse, dH, dW
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("N,d,V,chunk", [(1, 8, 2, 1), (1, 64, 1000, 4096), (3, 16, 1, 2), (255, 40, 257, 4096), (256, 256, 256, 256),
+                                         (300, 320, 1003, 128), (513, 72, 2051, 512), (40, 1024, 5003, 16)])
+def test_sizes(t, N, d, V, chunk):
+    check(inputs(N, d, V, t, seed=N), t, chunk)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("opts,k,cap", [({"temperature": 0.7}, 1 / 0.7, 0.0), ({"logit_softcapping": 3.0}, 1.0, 3.0),
+                                        ({"logit_softcapping": 3.0, "temperature": 0.8}, 1 / 0.8, 3.0), ({"logit_scale_multiply": 0.5}, 0.5, 0.0)])
+def test_logit_transforms(t, opts, k, cap):
+    check(inputs(130, 64, 700, t), t, 64, opts, k, cap)
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_forward_is_the_reference_calls_and_the_loss_s(t):
+    """The same kernels: lp bitwise grpo_ref_logprobs's, and the loss's gradient given as grad_lp bitwise
+    the loss's backward up to the rounding of the coefficients (half a step each way)."""
+    B, L, d, V = 3, 50, 64, 900
+    i = inputs(B * L, d, V, t)
+    mask = (torch.rand(B * L, device="cuda") < 0.6).to(torch.uint8)
+    adv = torch.randn(B, device="cuda")
+    ref = gp.grpo_ref_logprobs(i["H"], i["W"], i["y"]) + 0.1
+    lp, lse = gp.grpo_logprobs_fwd(i["H"], i["W"], i["y"])
+    assert torch.equal(lp, gp.grpo_ref_logprobs(i["H"], i["W"], i["y"]))
+    loss, lp2, kl, lse2 = gp.grpo_loss_fwd(i["H"], i["W"], i["y"], mask, adv, ref, B, L)
+    assert torch.equal(lp, lp2) and torch.equal(lse, lse2)
+    dH, dW = gp.grpo_loss_bwd(i["H"], i["W"], i["y"], mask, adv, ref, lp, lse, B, L)
+    ours, stats, w = gp.grpo_clip_loss_fwd(lp, mask, adv, B, L, ref_lp=ref, beta=0.04)
+    g = gp.grpo_clip_loss_bwd(lp, mask, adv, w, B, L, ref_lp=ref, beta=0.04)
+    dH2, dW2 = gp.grpo_logprobs_bwd(i["H"], i["W"], i["y"], lp, lse, g)
+    assert abs(loss.item() - ours.item()) <= 1e-6 * (abs(loss.item()) + 1)
+    # coefficients within 16 roundings of float32, and each dZ at most one step apart after that
+    far = 16 * plain_update.U + 2 * HALF[t]
+    want = plain_update.logprobs(i["H"], i["W"], i["y"], g, half=HALF[t])
+    for a, b, n in ((dH, dH2, "dH"), (dW, dW2, "dW")):
+        assert ((a.double() - b.double()).abs().cpu() <= 2 * want[n + "_tol"] + far * want[n].abs()).all()
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_accumulation_and_one_gradient_alone(t):
+    i = inputs(200, 64, 600, t)
+    lp, lse = gp.grpo_logprobs_fwd(i["H"], i["W"], i["y"])
+    args = (i["H"], i["W"], i["y"], lp, lse, i["g"])
+    tol = plain_update.logprobs(i["H"], i["W"], i["y"], i["g"], half=HALF[t])["dW_tol"].cuda()
+    for chunk in (64, 4096):
+        dH, dW = gp.grpo_logprobs_bwd(*args, chunk=chunk)
+        only_h, none = gp.grpo_logprobs_bwd(*args, chunk=chunk, need_w=False)
+        assert none is None and torch.equal(only_h, dH)
+        none, only_w = gp.grpo_logprobs_bwd(*args, chunk=chunk, need_h=False)
+        assert none is None and torch.equal(only_w, dW)
+        start = torch.randn(600, 64, device="cuda")
+        into = start.clone()
+        _, same = gp.grpo_logprobs_bwd(*args, chunk=chunk, dW=into)
+        assert same is into
+        # the same products, summed onto the start: one rounding of it for each chunk
+        assert ((into.double() - start.double() - dW.double()).abs() <= 2 * tol + 6 * plain_update.U * start.abs()).all()
+
+
+def test_no_token_has_a_gradient():
+    for t in TYPES:
+        i = inputs(70, 64, 300, t)
+        i["H"][3] = math.nan                 # tokens without a gradient may hold anything
+        i["g"].zero_()
+        lp, lse = gp.grpo_logprobs_fwd(i["H"], i["W"], i["y"])
+        assert lp[3].isnan() and not lp[:3].isnan().any()
+        for chunk in (16, 4096):
+            dH, dW = gp.grpo_logprobs_bwd(i["H"], i["W"], i["y"], lp, lse, i["g"], chunk)
+            assert not dH.any() and not dW.any()
+        i["g"][5] = -0.5
+        i["g"][6] = -0.0
+        dH, dW = gp.grpo_logprobs_bwd(i["H"], i["W"], i["y"], lp, lse, i["g"])
+        assert not dH.isnan().any() and not dW.isnan().any() and dH[5].any() and not dH[6].any()
+
+
+def test_targets_outside_the_vocabulary():
+    """Padding's -100: NaN log-probabilities, which a loss leaves out, and no gradient."""
+    i = inputs(40, 64, 300, "bf16", dead=0.0)
+    out = torch.arange(40, device="cuda") % 4 == 0
+    i["y"][out] = torch.tensor([-100, 300], dtype=torch.int32, device="cuda").repeat(5)
+    lp = gp.grpo_logprobs(i["H"], i["W"], i["y"])
+    assert torch.equal(lp.isnan(), out)
+    H, W = i["H"].requires_grad_(), i["W"].requires_grad_()
+    lp = gp.grpo_logprobs(H, W, i["y"])
+    loss, _ = gp.grpo_clip_loss(lp, (~out).to(torch.uint8), torch.randn(4, device="cuda"), 4, 10)
+    loss.backward()
+    assert not H.grad.isnan().any() and not W.grad.isnan().any() and not H.grad[out].any() and H.grad[~out].any(1).all()
+
+
+def test_autograd():
+    for t in TYPES:
+        i = inputs(60, 64, 500, t)
+        lp, lse = gp.grpo_logprobs_fwd(i["H"], i["W"], i["y"], opts={"temperature": 0.9})
+        dH, dW = gp.grpo_logprobs_bwd(i["H"], i["W"], i["y"], lp, lse, i["g"], opts={"temperature": 0.9})
+        H, W = i["H"].clone().requires_grad_(), i["W"].clone().requires_grad_()
+        out = gp.grpo_logprobs(H, W, i["y"], opts={"temperature": 0.9})
+        assert torch.equal(out, lp)
+        out.backward(i["g"])
+        assert torch.equal(H.grad, dH) and torch.equal(W.grad, dW.to(W.dtype))
+        # a frozen head, frozen hidden states, and a sum's broadcast gradient
+        H = i["H"].clone().requires_grad_()
+        gp.grpo_logprobs(H, i["W"], i["y"]).sum().backward()
+        W = i["W"].clone().requires_grad_()
+        gp.grpo_logprobs(i["H"], W, i["y"]).sum().backward()
+        ones = torch.ones(60, device="cuda")
+        lp, lse = gp.grpo_logprobs_fwd(i["H"], i["W"], i["y"])
+        dH, dW = gp.grpo_logprobs_bwd(i["H"], i["W"], i["y"], lp, lse, ones)
+        assert torch.equal(H.grad, dH) and torch.equal(W.grad, dW.to(W.dtype))
+
+
+def test_gradient_against_differences():
+    """float32: the log-probabilities' sum moved along dH and dW.  Their roundings are some 2^-20 each,
+    300 of them at random: 2^-15; over 2 h = 2^-5 that is 2^-10 of a slope of the order of hundreds."""
+    i = inputs(300, 64, 500, "f32", dead=0.2)
+    lp, lse = gp.grpo_logprobs_fwd(i["H"], i["W"], i["y"])
+    grads = gp.grpo_logprobs_bwd(i["H"], i["W"], i["y"], lp, lse, i["g"])
+    for name, grad in zip("HW", grads):
+        v = grad / grad.norm()
+        h = 2.0 ** -6
+        f = [(gp.grpo_logprobs_fwd(*(i[n] + s * h * v if n == name else i[n] for n in "HW"), i["y"])[0].double() * i["g"].double()).sum().item()
+             for s in (1, -1)]
+        slope, want = (f[0] - f[1]) / (2 * h), grad.double().norm().item()
+        assert abs(slope - want) <= 1e-3 * want + 2.0 ** -9
+
+
+def test_captured_and_replayed():
+    i = inputs(300, 64, 700, "bf16")
+    lp, lse = gp.grpo_logprobs_fwd(i["H"], i["W"], i["y"], 128)
+    out = {}
+
+    def once():
+        out["lp"], out["lse"] = gp.grpo_logprobs_fwd(i["H"], i["W"], i["y"], 128)
+        out["dH"], out["dW"] = gp.grpo_logprobs_bwd(i["H"], i["W"], i["y"], out["lp"], out["lse"], i["g"], 128)
+    once()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        once()
+    held = dict(out)
+    for k in range(4):
+        i["g"].mul_(-1.5)
+        if k == 2:
+            i["g"].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        once()
+        assert all(torch.equal(held[n], out[n]) for n in out)
