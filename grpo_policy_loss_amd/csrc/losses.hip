@@ -97,7 +97,7 @@ struct ClipArgs {
   int32_t L;
   int32_t adv_per_token, seq_mean, kl;
   double log_high, log_low, log_dual;   // of the borders; infinite where there is none
-  float high, low, dual, beta;          // the borders
+  double high, low, dual, beta;         // the borders
 };
 
 // Which side of the borders a ratio of logarithm D is on, and what stands in for it: NaN is on
@@ -105,12 +105,13 @@ struct ClipArgs {
 struct Clipped {
   bool low, high;
 };
-__device__ __forceinline__ Clipped clip_ratio(const ClipArgs& a, float adv, double D, float& s) {
+template <typename T>
+__device__ __forceinline__ Clipped clip_ratio(const ClipArgs& a, float adv, double D, T& s) {
   const bool above = adv >= 0.f && D > a.log_high, far = adv < 0.f && D > a.log_dual;
   const bool below = adv < 0.f && D < a.log_low;
-  if (above) s = a.high;
-  if (below) s = a.low;
-  if (far) s = a.dual;
+  if (above) s = (T)a.high;
+  if (below) s = (T)a.low;
+  if (far) s = (T)a.dual;
   return {below, above || far};
 }
 
@@ -127,13 +128,18 @@ __device__ __forceinline__ float kl_slope(int kind, float x, float lp) {
   return kind == GRPO_KL_FORWARD ? -x * v.e : -v.em;
 }
 
+// beta kl; where beta is 0 there is no such term, whatever kl is.
+__device__ __forceinline__ double kl_weighed(const ClipArgs& a, double kl) {
+  return a.beta != 0.0 ? a.beta * kl : 0.0;
+}
+
 struct ClipSums {
   double loss, d, kl, excess;
   int n, low, high, pad;
 };
 
-// Adds tokens [c, c + 4) of a row of n that starts at token t0 to the sums.  loss leaves the
-// policy term out where the ratio is the sequence's (SEQ).  A masked token counts as one with
+// Adds tokens [c, c + 4) of a row of n that starts at token t0 to the sums.  loss is the policy
+// term alone, and nothing where the ratio is the sequence's (SEQ).  A masked token counts as one with
 // all logarithms 0 and no advantage, which adds nothing.
 template <bool SEQ>
 __device__ __forceinline__ void clip_add(const ClipArgs& a, int64_t t0, int c, int n, float adv_row,
@@ -164,9 +170,7 @@ __device__ __forceinline__ void clip_add(const ClipArgs& a, int64_t t0, int c, i
       loss = fmaf(-adv, r, loss);
     }
     if (a.ref_lp != nullptr) {
-      const float k = kl_term(a.kl, (m ? ref4[j] : 0.f) - lp, lp);
-      kl += k;
-      loss = fmaf(a.beta, k, loss);
+      kl += kl_term(a.kl, (m ? ref4[j] : 0.f) - lp, lp);
     }
   }
   s.loss += loss;
@@ -174,8 +178,9 @@ __device__ __forceinline__ void clip_add(const ClipArgs& a, int64_t t0, int c, i
   s.excess += excess;
 }
 
-// What a sequence's own sums decide, in one lane for the sequence: the ratio's terms (SEQ), and
-// what the backward takes of it.  Gives the factor of the sequence's loss.
+// What a sequence's own sums decide, in one lane for the sequence: the ratio's terms (SEQ; in
+// float64, since a batch's advantages may nearly cancel), and what the backward takes of it.  Gives
+// the factor of the sequence's loss.
 template <bool SEQ>
 __device__ __forceinline__ double clip_sequence(const ClipArgs& a, int64_t b, float adv, int n,
                                                 double d, bool writes, ClipSums& s) {
@@ -183,15 +188,15 @@ __device__ __forceinline__ double clip_sequence(const ClipArgs& a, int64_t b, fl
   float slope = 0.f;
   if (SEQ) {
     const double D = n > 0 ? d / n : 0.0;
-    const float r = exp_wide(D);
-    float used = r;
+    const double r = exp(D);
+    double used = r;
     const Clipped at = clip_ratio(a, adv, D, used);
-    if (!at.low && !at.high) slope = -adv * r;
+    if (!at.low && !at.high) slope = (float)(-adv * r);
     if (writes && n > 0) {
       s.low += at.low ? n : 0;
       s.high += at.high ? n : 0;
-      s.excess += (double)exp_excess((float)D).excess * n;
-      s.loss += (double)(-adv * used) * n;
+      s.excess += (expm1(D) - D) * n;
+      s.loss -= adv * used * n;
     }
   }
   if (writes && (SEQ || a.seq_mean)) {
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kThreads)
       const double d = SEQ ? group_sum(row.d, width) : 0.0;
       inv = clip_sequence<SEQ>(a, b, adv, all, d, lane == 0, row);
     }
-    s.loss += row.loss * inv;
+    s.loss += (row.loss + kl_weighed(a, row.kl)) * inv;
     s.kl += row.kl;
     s.excess += row.excess;
     s.n += n;
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(kFinish)
         const double d = SEQ ? group_sum(row.d, width) : 0.0;
         inv = clip_sequence<SEQ>(a, b, adv, all, d, lane == 0, row);
       }
-      s.loss += row.loss * inv;
+      s.loss += (row.loss + kl_weighed(a, row.kl)) * inv;
       s.kl += row.kl;
       s.excess += row.excess;
       s.n += n;
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(kThreads)
       const Clipped at = clip_ratio(a, adv, D, r);
       slope = at.low || at.high ? 0.f : -adv * r;
     }
-    if (a.ref_lp != nullptr) slope = fmaf(a.beta, kl_slope(a.kl, (m ? ref4[j] : 0.f) - lp, lp), slope);
+    if (a.ref_lp != nullptr) slope = fmaf((float)a.beta, kl_slope(a.kl, (m ? ref4[j] : 0.f) - lp, lp), slope);
     out[j] = m ? w * slope : 0.f;
   }
   if (c + 4 <= n) {
@@ -670,11 +675,11 @@ int clip_args(const float* lp, const float* old_lp, const float* ref_lp, const u
     return fail(GRPO_ERR_INVALID_ARG, "a ratio for each sequence takes one advantage for each sequence");
   *a = ClipArgs{lp, old_lp, ref_lp, mask, adv, const_cast<float*>(weights), B, (int32_t)L,
                 o.adv_per_token, o.aggregation == GRPO_AGG_SEQUENCE_MEAN, o.kl_estimator,
-                HUGE_VAL, -HUGE_VAL, HUGE_VAL, 0.f, 0.f, 0.f, (float)o.beta};
-  if (o.clip_high > 0.0) a->log_high = log1p(o.clip_high), a->high = (float)(1.0 + o.clip_high);
+                HUGE_VAL, -HUGE_VAL, HUGE_VAL, 0.0, 0.0, 0.0, o.beta};
+  if (o.clip_high > 0.0) a->log_high = log1p(o.clip_high), a->high = 1.0 + o.clip_high;
   // at 1 and beyond nothing is clipped from below: a ratio is not negative
-  if (o.clip_low > 0.0 && o.clip_low < 1.0) a->log_low = log1p(-o.clip_low), a->low = (float)(1.0 - o.clip_low);
-  if (o.clip_dual > 0.0) a->log_dual = log(o.clip_dual), a->dual = (float)o.clip_dual;
+  if (o.clip_low > 0.0 && o.clip_low < 1.0) a->log_low = log1p(-o.clip_low), a->low = 1.0 - o.clip_low;
+  if (o.clip_dual > 0.0) a->log_dual = log(o.clip_dual), a->dual = o.clip_dual;
   return GRPO_OK;
 }
 
@@ -739,6 +744,7 @@ int grpo_clip_loss_bwd(const float* lp, const float* old_lp, const float* ref_lp
   const int64_t N = B * L;
   const unsigned blocks = (unsigned)((N + grpo::kThreads * 4 - 1) / (grpo::kThreads * 4));
   const grpo::Divide by = grpo::divider(L);
+  if (a.beta == 0.0) a.ref_lp = nullptr;
   if (opts != nullptr && opts->ratio == GRPO_RATIO_SEQUENCE)
     grpo::k_clip_bwd<true><<<blocks, grpo::kThreads, 0, s>>>(a, by, N, grad_loss, grad_lp);
   else

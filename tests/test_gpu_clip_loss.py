@@ -92,6 +92,11 @@ def test_without_reference_or_old_policy(L):
     check(i, 4, L, ref=False, old=False, seq_mean=True)
     check(i, 4, L, ref=False, old=False, sequence=True, low=0.2)
     check(i, 4, L, beta=0.0, low=0.2)               # kl in the statistics alone
+    i["ref"].fill_(-math.inf)
+    for sequence in (False, True):                  # and not in the loss where it is infinite
+        loss, stats, grad = run(i, 4, L, low=0.2, sequence=sequence)
+        assert stats[0].item() == math.inf and loss.isfinite() and grad.isfinite().all()
+        assert torch.equal(loss, run(i, 4, L, low=0.2, sequence=sequence, ref=False)[0])
 
 
 @pytest.mark.parametrize("L", [1, 77, 2500])
