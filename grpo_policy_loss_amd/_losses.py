@@ -11,8 +11,8 @@ import functools
 
 import torch
 
-from ._lib import (AGG_TOKEN_MEAN, GRPO_OP_BWD, GRPO_OP_FWD, KL_REVERSE, ClipOpts, PrefOpts, _arg,
-                   _check, _check_workspace, _dt, _matrix, _opts, _ptr, auto_chunk,
+from ._lib import (AGG_TOKEN_MEAN, GRPO_F32, GRPO_OP_LOGPROBS_BWD, GRPO_OP_LOGPROBS_FWD, KL_REVERSE,
+                   ClipOpts, PrefOpts, _arg, _check, _dt, _matrix, _opts, _ptr, auto_chunk,
                    grpo_workspace_bytes, lib)
 from ._ops import _on, _workspace
 
@@ -31,28 +31,29 @@ def _head(H, W, y):
     return N, d, V, dt
 
 
+def _lse_size(N, dt):
+    return 2 * N if dt == GRPO_F32 else N
+
+
 def _head_workspace(op, N, d, V, dt, chunk, device, workspace):
-    if workspace is not None:
-        _check_workspace(workspace, op, N, d, V, dt, chunk)
-        return workspace
     need = grpo_workspace_bytes(op, N, d, V, dt, chunk)
     if need == 0:
         _check("grpo_workspace_bytes", -1)
-    return torch.empty(need, dtype=torch.uint8, device=device)
+    return _workspace(need, device, workspace)
 
 
 def grpo_logprobs_fwd(H, W, y, chunk: int = 4096, workspace=None, opts=None):
-    """(lp, lse), both float32 [N]: the log-probability of y under softmax of the logits of
-    H [N, d] (float32 or bfloat16) and W [V, d], and the log-sum-exp that the backward takes.
-    `opts` and chunk as for grpo_loss_fwd; of the options the logit transform counts."""
+    """(lp [N], lse), float32: the log-probability of y under softmax of the logits of H [N, d]
+    (float32 or bfloat16) and W [V, d], and the log-sum-exp that the backward takes ([N]; for
+    float32 [2 N], its rounding behind it).  `opts` and chunk as for grpo_loss_fwd; of the options the logit transform counts."""
     N, d, V, dt = _head(H, W, y)
     ctx, stream = _on(*(t for t in (H, W, y, workspace) if t is not None))
     with ctx:
         if chunk == 0:
             chunk = auto_chunk(1, N, d, V, dt)
-        ws = _head_workspace(GRPO_OP_FWD, N, d, V, dt, chunk, H.device, workspace)
+        ws = _head_workspace(GRPO_OP_LOGPROBS_FWD, N, d, V, dt, chunk, H.device, workspace)
         lp = torch.empty(N, dtype=torch.float32, device=H.device)
-        lse = torch.empty_like(lp)
+        lse = torch.empty(_lse_size(N, dt), dtype=torch.float32, device=H.device)
         _check("grpo_logprobs_fwd", lib().grpo_logprobs_fwd(
             _ptr(H), _ptr(W), _ptr(y), N, d, V, dt, chunk, _opts(opts), _ptr(lp), _ptr(lse),
             _ptr(ws), ws.numel(), stream))
@@ -66,8 +67,8 @@ def grpo_logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk: int = 4096, dW=None, dH=
     are 0.  dW is accumulated into when given.  need_h or need_w false: that one is not
     formed, and None.  lp, lse and `opts` are the forward's."""
     N, d, V, dt = _head(H, W, y)
-    for t, name in ((lp, "lp"), (lse, "lse"), (grad_lp, "grad_lp")):
-        _arg(t, name, dtype=torch.float32, numel=N)
+    for t, name, n in ((lp, "lp", N), (lse, "lse", _lse_size(N, dt)), (grad_lp, "grad_lp", N)):
+        _arg(t, name, dtype=torch.float32, numel=n)
     if not (need_h or need_w):
         raise ValueError("one of need_h and need_w must be true")
     if dH is not None:
@@ -79,7 +80,7 @@ def grpo_logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk: int = 4096, dW=None, dH=
     with ctx:
         if chunk == 0:
             chunk = auto_chunk(1, N, d, V, dt)
-        ws = _head_workspace(GRPO_OP_BWD, N, d, V, dt, chunk, H.device, workspace)
+        ws = _head_workspace(GRPO_OP_LOGPROBS_BWD, N, d, V, dt, chunk, H.device, workspace)
         if not need_h:
             dH = None
         elif dH is None:

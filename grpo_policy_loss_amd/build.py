@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgrpo.so")
 SOURCES = ["kernels.hip", "grpo_api.hip", "timing.hip", "norm.hip", "adamw.hip",
-           "sample.hip", "losses.hip", "gradnorm.hip"]
+           "sample.hip", "losses.hip", "gradnorm.hip", "tile64.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

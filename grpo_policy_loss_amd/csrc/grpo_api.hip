@@ -196,6 +196,79 @@ BwdPlan plan_bwd(int64_t N, int64_t d, int64_t V, int dtype, int64_t chunk, int6
   return p;
 }
 
+// The log-probabilities' workspace where they run in 64 x 64 tiles (tile64.hip).  Forward: partials
+// of one chunk.  Backward: the dZ of one chunk, of at most kSlabBytesDefault, and dH's shares.
+struct Plan64 {
+  int64_t C, vpad, shares;
+  size_t o_ps, o_zy, o_parts, total;
+};
+
+// Whether the log-probabilities' forward takes 64 x 64 tiles rather than 256 x 256 ones.  bfloat16:
+// never (its lp is bitwise the loss's).  float32: unless the large tiles' waves of one workgroup per
+// CU are at least 3/4 full and a row has 256 elements.  us, small against large tiles:
+//   d     V       N = 256     512         2048        8192
+//   64    32000   55   97     78   146    209   414   734   1537
+//   256   32000   86   88     137  89     438   304   1631  1140
+//   1024  8000    60   273    102  269    352   281   1331  1054
+//   1024  1000    37   267    37   269    55    274   182   272
+bool small_tiles_fwd(int64_t N, int64_t d, int64_t V, int dtype) {
+  if (dtype != GRPO_F32) return false;
+  const int64_t waves = ((N + 255) / 256 * ((V + 255) / 256) + kCUs - 1) / kCUs;
+  return d < 256 || (double)N * (double)V < 0.73 * 65536.0 * (double)(waves * kCUs);
+}
+
+// The same for the backward.  bfloat16: where the products are few, twice as many where tokens fill
+// no more than half a large tile.  us, small against large tiles (70 % of the tokens have a gradient;
+// only the large tiles pass by the others):
+//   d     V       N = 16        128          512          2048
+//   64    1000    28    50      29    52     29    58     44    79
+//   256   32000   62    133     76    138    120   150    384   203
+//   1024  8000    41    93      49    98     108   110    336   134
+//   1024  128000  316   547     439   564    1354  647    4984  1061
+//   4096  1000    45    124     52    129    78    142    187   197
+//   4096  32000   311   342     432   363    1287  412    4885  1003
+// float32: unless there is enough of everything for the large ones: for dH's at most 8 shares, for dW's
+// tiles and in all.
+//   256   32000   92    1118    124   1134   307   1213   1110  1696   (N = 8192: 4306  3673)
+//   1024  8000    75    571     100   591    283   668    1039  936
+//   1024  32000   178   1328    301   1369   1058  1522   4049  2591
+//   4096  1000    124   1081    139   1103   208   1174   527   1565
+//   4096  8000    222   1313    307   1352   1041  1501   3958  2774
+bool small_tiles_bwd(int64_t N, int64_t d, int64_t V, int dtype) {
+  const double products = (double)N * (double)V * (double)d;
+  if (dtype == GRPO_BF16) return products <= (N <= 128 ? 8589934592.0 : 4294967296.0);
+  const int64_t dt = (d + 255) / 256;
+  return dt * ((N + 255) / 256) < 32 || dt * ((V + 255) / 256) < 128 || products < 1.6e10;
+}
+
+Plan64 plan64_fwd(int64_t N, int64_t V, int64_t chunk) {
+  Plan64 p{};
+  p.C = std::min(std::min(chunk, N), std::max<int64_t>(64, kSlabBytesDefault / ((V + 63) / 64 * 4) / 64 * 64));
+  const size_t parts = (size_t)((V + 63) / 64 * p.C) * 4;
+  Carve c;
+  c.take(parts);
+  p.o_ps = c.take(parts);
+  p.o_zy = c.take((size_t)p.C * 4);
+  p.total = c.off;
+  return p;
+}
+
+Plan64 plan64_bwd(int64_t N, int64_t d, int64_t V, int64_t es, int64_t chunk) {
+  Plan64 p{};
+  p.vpad = round_up(V, 64);
+  p.C = std::min(std::min(chunk, N), std::max<int64_t>(64, kSlabBytesDefault / (p.vpad * es) / 64 * 64));
+  // shares of the vocabulary for dH, until it has some 1024 tiles or 4 steps a share
+  const int64_t tiles = (d + 63) / 64 * ((p.C + 63) / 64);
+  p.shares = std::max<int64_t>(1, std::min<int64_t>((4 * kCUs + tiles - 1) / tiles, p.vpad / 256));
+  const int64_t per = (p.vpad / 64 + p.shares - 1) / p.shares;   // tiles of a share: none is empty
+  p.shares = (p.vpad / 64 + per - 1) / per;
+  Carve c;
+  c.take((size_t)(p.C * p.vpad * es));
+  p.o_parts = p.shares > 1 ? c.take((size_t)(p.shares * p.C * d) * 4) : 0;
+  p.total = c.off;
+  return p;
+}
+
 // Shape checks shared by all calls.  Operands are addressed per 256-row tile
 // with 32-bit offsets, so one tile's rows must span < 2 GiB.
 // fp8_ok: GRPO_FP8_E4M3 is accepted (the fp8 calls and the size queries)
@@ -308,15 +381,17 @@ struct Fp8Recompute {
   float* hs_act = nullptr;
 };
 
-// grad_lp: the loss's gradient with respect to lp is given (mask, adv and ref_lp are not used).
-// A null dH or dW is not formed.
+// grad_lp: the loss's gradient with respect to lp is given (mask, adv and ref_lp are not used), and
+// rest, what float32 left of lse, or null.  A null dH or dW is not formed; dw_first: dW is
+// written instead of added to.
 template <typename T>
 int bwd_pass(const T* H, const T* W, const int32_t* y, const uint8_t* mask, const float* adv,
              const float* ref_lp, const float* lp, const float* lse, const float* grad_lp,
              int64_t N, int64_t L, int64_t d, int64_t V, float beta, float grad_loss,
              int64_t chunk, const grpo::LogitXform& xf, const grpo::LossVariant& lv, T* dH,
              float* dW, const BwdPlan& p, char* ws, hipStream_t s,
-             const Fp8Recompute& f8 = Fp8Recompute()) {
+             const Fp8Recompute& f8 = Fp8Recompute(), const float* rest = nullptr,
+             bool dw_first = false) {
   int32_t* idx = (int32_t*)(ws + p.o_idx);
   int32_t* cnt = (int32_t*)(ws + p.o_cnt);
   T* H_act = (T*)(ws + p.o_hact);
@@ -340,7 +415,7 @@ int bwd_pass(const T* H, const T* W, const int32_t* y, const uint8_t* mask, cons
     const int64_t c0 = c * p.C;
     const int C = (int)p.C;
     GRPO_HIP(grpo::launch_bwd_prep<T>(H, d, idx, cnt, c0, C, (int)p.cpad, y, mask, adv, ref_lp, lp,
-                                      lse, grad_lp, L, beta, grad_loss, xf, lv, seq_n, B, H_act, coef,
+                                      lse, grad_lp, rest, L, beta, grad_loss, xf, lv, seq_n, B, H_act, coef,
                                       lse_c, y_c, tgt_c, s));
     if (dW != nullptr) GRPO_HIP(grpo::launch_transpose<T>(H_act, p.cpad, d, HT, p.cpad, s));
     if (f8.H8 != nullptr)
@@ -356,17 +431,36 @@ int bwd_pass(const T* H, const T* W, const int32_t* y, const uint8_t* mask, cons
       else
         GRPO_HIP(grpo::launch_dz<T>(W, H_act, d, V, v0, vs_valid, (int)p.vs, cnt, c0, C,
                                     (int)p.cpad, xf, nullptr, nullptr, coef, lse_c, y_c, tgt_c,
-                                    dZ, s));
+                                    dZ, s, rest != nullptr));
       if (dH != nullptr)
         GRPO_HIP(grpo::launch_dh_gemm<T>(W, v0, vs_valid, dZ, (int)p.vs, d, cnt, c0, C,
                                          (int)p.cpad, (int)p.nsplit, sl == 0 ? 1 : 0, dH_acc, s));
       if (dW != nullptr)
         GRPO_HIP(grpo::launch_dw_gemm<T>(HT, (int)p.cpad, dZ, (int)p.vs, d, v0, vs_valid, cnt, c0,
-                                         C, dW, s));
+                                         C, dW, s, dw_first && c == 0));
     }
     if (dH == nullptr) continue;
     GRPO_HIP(grpo::launch_dh_scatter<T>(dH_acc, (int)p.nsplit, (int)p.cpad, d, idx, cnt, c0, C, dH,
                                         s));
+  }
+  return GRPO_OK;
+}
+
+template <typename T>
+int logprobs_bwd64(const T* H, const T* W, const int32_t* y, const float* lp, const float* lse,
+                   const float* grad_lp, int64_t N, int64_t d, int64_t V, int64_t chunk,
+                   const grpo::LogitXform& xf, int accumulate, T* dH, float* dW, char* ws,
+                   hipStream_t s) {
+  const Plan64 p = plan64_bwd(N, d, V, (int64_t)sizeof(T), chunk);
+  for (int64_t c0 = 0; c0 < N; c0 += p.C) {
+    const int C = (int)std::min(p.C, N - c0);
+    // of lse's two parts bfloat16 has the first
+    const float* rest = sizeof(T) == 4 ? lse + N + c0 : nullptr;
+    GRPO_HIP(grpo::launch64_dz<T>(W, H + c0 * d, y + c0, lp + c0, lse + c0, rest, grad_lp + c0, V, d,
+                                  C, p.vpad, xf, (T*)ws, s));
+    GRPO_HIP(grpo::launch64_grads<T>(W, H + c0 * d, (const T*)ws, grad_lp + c0, V, d, C, p.vpad,
+                                     (int)p.shares, dH == nullptr ? nullptr : dH + c0 * d,
+                                     (float*)(ws + p.o_parts), accumulate || c0 > 0, dW, s));
   }
   return GRPO_OK;
 }
@@ -423,8 +517,19 @@ size_t grpo_workspace_bytes(int op, int64_t N, int64_t d, int64_t V, int dtype, 
       return dtype == GRPO_FP8_E4M3 ? plan_bwd_fp8(N, d, V, chunk, how).total
                                     : plan_bwd(N, d, V, dtype, chunk, how).total;
     }
-    default: fail(GRPO_ERR_INVALID_ARG, "unknown op %d", op); return 0;
+    case GRPO_OP_LOGPROBS_FWD:
+      if (dtype == GRPO_FP8_E4M3) break;
+      return small_tiles_fwd(N, d, V, dtype) ? plan64_fwd(N, V, chunk).total
+                                             : plan_fwd(N, V, chunk).total;
+    case GRPO_OP_LOGPROBS_BWD:
+      if (dtype == GRPO_FP8_E4M3) break;
+      return small_tiles_bwd(N, d, V, dtype)
+                 ? plan64_bwd(N, d, V, (int64_t)esize(dtype), chunk).total
+                 : plan_bwd(N, d, V, dtype, chunk, 0).total;
+    default: break;
   }
+  fail(GRPO_ERR_INVALID_ARG, "unknown op %d for dtype %d", op, dtype);
+  return 0;
 }
 
 int64_t grpo_auto_chunk(int64_t B, int64_t L, int64_t d, int64_t V, int dtype,
@@ -614,17 +719,37 @@ int grpo_logprobs_fwd(const void* H, const void* W, const int32_t* y, int64_t N,
   GRPO_CHECK_PTR(lse);
   const int st = check_shape(N, d, V, dtype, chunk);
   if (st != GRPO_OK) return st;
-  const size_t need = plan_fwd(N, V, chunk).total;
+  const size_t need = grpo_workspace_bytes(GRPO_OP_LOGPROBS_FWD, N, d, V, dtype, chunk);
   if (workspace == nullptr || workspace_bytes < need)
     return fail(GRPO_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
                 workspace == nullptr ? (size_t)0 : workspace_bytes);
   hipStream_t s = (hipStream_t)stream;
+  char* ws = (char*)workspace;
   if (dtype == GRPO_BF16)
     return lse_pass<__bf16>(0, (const __bf16*)H, (const __bf16*)W, y, nullptr, nullptr, nullptr, N,
-                            1, d, V, 0.f, chunk, xf, lv, nullptr, lp, nullptr, lse,
-                            (char*)workspace, s);
-  return lse_pass<float>(0, (const float*)H, (const float*)W, y, nullptr, nullptr, nullptr, N, 1, d,
-                         V, 0.f, chunk, xf, lv, nullptr, lp, nullptr, lse, (char*)workspace, s);
+                            1, d, V, 0.f, chunk, xf, lv, nullptr, lp, nullptr, lse, ws, s);
+  const float *Hf = (const float*)H, *Wf = (const float*)W;
+  if (small_tiles_fwd(N, d, V, dtype)) {
+    const Plan64 p = plan64_fwd(N, V, chunk);
+    float *pm = (float*)ws, *ps = (float*)(ws + p.o_ps), *zy = (float*)(ws + p.o_zy);
+    for (int64_t c0 = 0; c0 < N; c0 += p.C) {
+      const int C = (int)std::min(p.C, N - c0);
+      GRPO_HIP(grpo::launch64_lse(Wf, Hf + c0 * d, y + c0, V, d, C, xf, pm, ps, zy, s));
+      GRPO_HIP(grpo::launch64_merge(pm, ps, zy, y + c0, V, (int)((V + 63) / 64), C, C, lp + c0,
+                                    lse + c0, lse + N + c0, s));
+    }
+    return GRPO_OK;
+  }
+  const FwdPlan p = plan_fwd(N, V, chunk);
+  float *pm = (float*)(ws + p.o_pm), *ps = (float*)(ws + p.o_ps), *zy = (float*)(ws + p.o_zy);
+  for (int64_t c0 = 0; c0 < N; c0 += p.C) {
+    const int C = (int)std::min(p.C, N - c0);
+    GRPO_HIP(grpo::launch_lse_partials<float>(Wf, Hf + c0 * d, y + c0, V, d, C, (int)p.cpad, xf,
+                                              nullptr, nullptr, pm, ps, zy, s));
+    GRPO_HIP(grpo::launch64_merge(pm, ps, zy, y + c0, V, (int)p.S, p.cpad, C, lp + c0, lse + c0,
+                                  lse + N + c0, s));
+  }
+  return GRPO_OK;
 }
 
 int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const float* lp,
@@ -647,6 +772,18 @@ int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const floa
     return fail(GRPO_ERR_INVALID_ARG, "accumulate %d is not 0 or 1", accumulate);
   const int st = check_shape(N, d, V, dtype, chunk);
   if (st != GRPO_OK) return st;
+  hipStream_t s = (hipStream_t)stream;
+  if (small_tiles_bwd(N, d, V, dtype)) {
+    const size_t need = grpo_workspace_bytes(GRPO_OP_LOGPROBS_BWD, N, d, V, dtype, chunk);
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(GRPO_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
+                  workspace == nullptr ? (size_t)0 : workspace_bytes);
+    if (dtype == GRPO_F32)
+      return logprobs_bwd64<float>((const float*)H, (const float*)W, y, lp, lse, grad_lp, N, d, V,
+                                   chunk, xf, accumulate, (float*)dH, dW, (char*)workspace, s);
+    return logprobs_bwd64<__bf16>((const __bf16*)H, (const __bf16*)W, y, lp, lse, grad_lp, N, d, V,
+                                  chunk, xf, accumulate, (__bf16*)dH, dW, (char*)workspace, s);
+  }
   // a caller's size is always a size, as in grpo_loss_bwd_ex
   const int64_t wsb = std::max<int64_t>(1, (int64_t)std::min<size_t>(workspace_bytes, (size_t)INT64_MAX));
   const BwdPlan p = plan_bwd(N, d, V, dtype, chunk, workspace == nullptr ? 1 : wsb);
@@ -654,17 +791,14 @@ int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const floa
     return fail(GRPO_ERR_WORKSPACE, "workspace needs at least %zu bytes, got %zu",
                 plan_bwd(N, d, V, dtype, chunk, -1).total,
                 workspace == nullptr ? (size_t)0 : workspace_bytes);
-  hipStream_t s = (hipStream_t)stream;
   lv = grpo::LossVariant{0, 0, 0};
-  if (dW != nullptr && !accumulate)
-    GRPO_HIP(grpo::launch_zero(dW, (size_t)(V * d) * 4, s));
   if (dtype == GRPO_BF16)
     return bwd_pass<__bf16>((const __bf16*)H, (const __bf16*)W, y, nullptr, nullptr, nullptr, lp,
                             lse, grad_lp, N, 1, d, V, 0.f, 0.f, chunk, xf, lv, (__bf16*)dH, dW, p,
-                            (char*)workspace, s);
+                            (char*)workspace, s, Fp8Recompute(), nullptr, !accumulate);
   return bwd_pass<float>((const float*)H, (const float*)W, y, nullptr, nullptr, nullptr, lp, lse,
                          grad_lp, N, 1, d, V, 0.f, 0.f, chunk, xf, lv, (float*)dH, dW, p,
-                         (char*)workspace, s);
+                         (char*)workspace, s, Fp8Recompute(), lse + N, !accumulate);
 }
 
 // ---------------------------------------------------------------- fp8 e4m3 path

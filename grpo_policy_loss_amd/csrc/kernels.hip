@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "kernels.hpp"
+#include "raster.hpp"
 #include "tile_mma.hpp"
 #include "timing.hpp"
 
@@ -60,36 +61,6 @@ __device__ __forceinline__ void lse_combine(float& m, float& s, float m2, float 
   }
   s = s * ex2((m - M) * kLog2e) + s2 * ex2((m2 - M) * kLog2e);
   m = M;
-}
-
-// Logical tile id p -> (M-tile, N-tile), in groups of GM M-tiles (M
-// fastest), so the ~32 workgroups resident on one XCD share GM A-panels and
-// ~32/GM B-panels in that XCD's L2.
-template <int GM>
-__device__ __forceinline__ void group_coords(int p, int tm, int tn, int& mt, int& nt) {
-  const int per_group = GM * tn;
-  const int g = p / per_group;
-  const int first = g * GM;
-  const int gm = (tm - first) < GM ? (tm - first) : GM;
-  const int rem = p - g * per_group;
-  mt = first + rem % gm;
-  nt = rem / gm;
-}
-
-// Hardware dispatches workgroup b to XCD b % 8.  Deal the logical tile ids
-// [0, tiles) to the XCDs in whole blocks of 32, one wave of an XCD's 32 CUs:
-// XCD x takes a contiguous range of blocks, so the tiles resident on it at
-// one time are always one aligned block of the raster.  (A range starting
-// part-way into a block would straddle two groups of the raster for some of
-// its waves.)  The grid is xcd_grid(tiles) workgroups; false for those past
-// this XCD's range.
-__device__ __forceinline__ bool xcd_tile(int bid, int tiles, int& p) {
-  const int xcd = bid & 7, slot = bid >> 3;
-  const int nb = (tiles + 31) >> 5;
-  const int q = nb >> 3, r = nb & 7;
-  const int nmine = (q + (xcd < r ? 1 : 0)) << 5;
-  p = ((xcd * q + (xcd < r ? xcd : r)) << 5) + slot;
-  return slot < nmine && p < tiles;
 }
 
 // Tile (mt, nt) of workgroup bid in a tm x tn grid: ids in groups of 4
@@ -578,17 +549,19 @@ __global__ void __launch_bounds__(256)
 
 // Gather the hidden states of chunk c's active tokens into H_act and form
 // the per-token backward coefficient c_t (grad_lp's, where that is given), lse
-// and target; padding rows are 0.
+// and target; padding rows are 0.  rest (null: none): what float32 left of lse,
+// in the place of the target's entry.
 template <typename T>
 __global__ void __launch_bounds__(256)
     k_bwd_prep(const T* __restrict__ H, int64_t d, const int32_t* __restrict__ idx,
                const int32_t* __restrict__ count, int64_t c0, int C,
                const int32_t* __restrict__ y, const float* __restrict__ adv,
                const float* __restrict__ ref_lp, const float* __restrict__ lp,
-               const float* __restrict__ lse, const float* __restrict__ grad_lp, int64_t L,
-               float beta, float grad_loss, LogitXform xf, LossVariant lv, const int32_t* __restrict__ seq_n, int64_t B,
-               T* __restrict__ H_act, float* __restrict__ coef,
-               float* __restrict__ lse_c, int32_t* __restrict__ y_c, float* __restrict__ tgt_c) {
+               const float* __restrict__ lse, const float* __restrict__ grad_lp,
+               const float* __restrict__ rest, int64_t L, float beta, float grad_loss,
+               LogitXform xf, LossVariant lv, const int32_t* __restrict__ seq_n, int64_t B,
+               T* __restrict__ H_act, float* __restrict__ coef, float* __restrict__ lse_c,
+               int32_t* __restrict__ y_c, float* __restrict__ tgt_c) {
   const int cnt = count[0];
   if (c0 >= cnt) return;
   const int j = blockIdx.x;
@@ -626,7 +599,7 @@ __global__ void __launch_bounds__(256)
         const float tt = fminf(1.f, fmaxf(-1.f, (lp[t] + lse[t]) / xf.b));
         slope = xf.a * xf.b * (1.f - tt * tt);
       }
-      tgt_c[j] = c * -expm1f(lp[t]) * slope;
+      tgt_c[j] = rest != nullptr ? rest[t] : c * -expm1f(lp[t]) * slope;
     } else {
       coef[j] = 0.f;
       lse_c[j] = 0.f;
@@ -655,6 +628,21 @@ __device__ __forceinline__ float dz_value(float z, float ct, float lb, int64_t v
   const float p = ex2(fmaf(zt, kLog2e, -lb));
   const float onehot = v == yl ? 1.f : 0.f;
   return v < vs_valid ? ct * (onehot - p) * slope : 0.f;
+}
+
+// The same from both parts of lse, hi and what float32 left of it: z - lse nearly
+// cancels where p counts, and 1 - p is formed from it.
+template <bool SC>
+__device__ __forceinline__ float dz_value_rest(float z, float ct, float hi, float rest, int64_t v,
+                                               int64_t yl, int vs_valid, const LogitXform& xf) {
+  float slope = xf.k, zt = xf.k * z;
+  if (SC) {
+    const float t = tanhf(xf.a * z);
+    zt = xf.b * t;
+    slope = xf.a * xf.b * (1.f - t * t);
+  }
+  const float x = (zt - hi) - rest;
+  return v < vs_valid ? -ct * (v == yl ? expm1f(x) : expf(x)) * slope : 0.f;
 }
 
 // Stage -c_t p f'(z) of every accumulator entry of this lane as bf16 into the
@@ -694,8 +682,9 @@ __device__ __forceinline__ void dz_stage(const Acc& acc, int wave, int lane, int
 
 // T = uint8_t: the logits are recomputed from float8 e4m3 codes (w_scale[0] the
 // head's scale, hs_act[j] active token j's), exactly as the fp8 forward formed
-// them, and dZ is bfloat16; other T ignore both scale pointers.
-template <typename T, bool SC>
+// them, and dZ is bfloat16; other T ignore both scale pointers.  REST (float32):
+// tgt_c holds what float32 left of lse.
+template <typename T, bool SC, bool REST = false>
 __global__ void __launch_bounds__(kThreads, 1)
     k_dz(const T* __restrict__ W, const T* __restrict__ H_act, int64_t d, int64_t v0,
          int vs_valid, int vs, const int32_t* __restrict__ count, int64_t c0, int C, int cpad,
@@ -746,7 +735,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float q[kAcc];
 #pragma unroll
         for (int u = 0; u < kAcc; ++u)
-          q[u] = dz_value<SC>(acc[i][j][u], ct[j], lb[j], v + u, yl[j], vs_valid, xf);
+          q[u] = REST ? dz_value_rest<SC>(acc[i][j][u], ct[j], lse_c[t], tgt_c[t], v + u, yl[j],
+                                          vs_valid, xf)
+                      : dz_value<SC>(acc[i][j][u], ct[j], lb[j], v + u, yl[j], vs_valid, xf);
         store4(dZ + ((int64_t)(v >> 8) * cpad + t) * 256 + (v & 255), q[0], q[1], q[2], q[3]);
       }
     }
@@ -909,16 +900,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // hidden-state chunk.
 // The blocks are computed transposed (SWAP), so each lane holds four
 // consecutive hidden columns of one vocabulary row, as dW's rows are laid out.
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_dw_gemm(const T* __restrict__ HT, int cpad, const T* __restrict__ dZ, int vs, int64_t d,
-              int64_t v0, int vs_valid, const int32_t* __restrict__ count, int64_t c0, int C,
-              int tm, int tn, float* __restrict__ dW) {
-  __shared__ __attribute__((aligned(1024))) char smem[kLdsBytes];
-  char GRPO_LDS* lds = (char GRPO_LDS*)smem;
+// FIRST: dW is written, with zeros where no token is active, instead of added to.
+template <typename T, bool FIRST>
+__device__ __forceinline__ void dw_tile(const T* HT, int cpad, const T* dZ, int64_t d, int64_t v0,
+                                        int vs_valid, const int32_t* count, int64_t c0, int C,
+                                        int tm, int tn, float* dW, char GRPO_LDS* lds) {
   int n_act = count[0] - (int)c0;
   n_act = n_act < 0 ? 0 : (n_act > C ? C : n_act);
-  if (n_act <= 0) return;
+  if (n_act <= 0 && !FIRST) return;
   int mt, nt;
   if (!tile_coords_blk(blockIdx.x, tm, tn, mt, nt)) return;
   const int m0 = mt * kBM;                  // first vocabulary row of the slab
@@ -935,7 +924,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   tile_mainloop<T, true, false, true>(acc, A, B, k_slices_of(kb), lds);
 
   const int rows = (vs_valid - m0) < kBM ? (vs_valid - m0) : kBM;
-  store_tile_f32<true>(dW + (v0 + m0) * d, rows, n0, d, acc, true);
+  store_tile_f32<true>(dW + (v0 + m0) * d, rows, n0, d, acc, !FIRST);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_dw_gemm(const T* __restrict__ HT, int cpad, const T* __restrict__ dZ, int vs, int64_t d,
+              int64_t v0, int vs_valid, const int32_t* __restrict__ count, int64_t c0, int C,
+              int tm, int tn, float* __restrict__ dW) {
+  __shared__ __attribute__((aligned(1024))) char smem[kLdsBytes];
+  dw_tile<T, false>(HT, cpad, dZ, d, v0, vs_valid, count, c0, C, tm, tn, dW,
+                    (char GRPO_LDS*)smem);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_dw_first(const T* __restrict__ HT, int cpad, const T* __restrict__ dZ, int vs, int64_t d,
+               int64_t v0, int vs_valid, const int32_t* __restrict__ count, int64_t c0, int C,
+               int tm, int tn, float* __restrict__ dW) {
+  __shared__ __attribute__((aligned(1024))) char smem[kLdsBytes];
+  dw_tile<T, true>(HT, cpad, dZ, d, v0, vs_valid, count, c0, C, tm, tn, dW, (char GRPO_LDS*)smem);
 }
 
 template <typename T>
@@ -1188,14 +1196,14 @@ template <typename T>
 hipError_t launch_bwd_prep(const T* H, int64_t d, const int32_t* idx, const int32_t* count,
                            int64_t c0, int C, int cpad, const int32_t* y, const uint8_t* mask,
                            const float* adv, const float* ref_lp, const float* lp,
-                           const float* lse, const float* grad_lp, int64_t L, float beta,
-                           float grad_loss, const LogitXform& xf, const LossVariant& lv,
+                           const float* lse, const float* grad_lp, const float* rest, int64_t L,
+                           float beta, float grad_loss, const LogitXform& xf, const LossVariant& lv,
                            const int32_t* seq_n, int64_t B, T* H_act, float* coef, float* lse_c,
                            int32_t* y_c, float* tgt_c, hipStream_t s) {
   ScopedKernelTimer timer_(KK_BWD_PREP, s);
   (void)mask;
   hipLaunchKernelGGL(k_bwd_prep<T>, dim3(cpad), dim3(256), 0, s, H, d, idx, count, c0, C, y, adv,
-                     ref_lp, lp, lse, grad_lp, L, beta, grad_loss, xf, lv, seq_n, B, H_act, coef,
+                     ref_lp, lp, lse, grad_lp, rest, L, beta, grad_loss, xf, lv, seq_n, B, H_act, coef,
                      lse_c, y_c, tgt_c);
   return hipGetLastError();
 }
@@ -1205,10 +1213,20 @@ hipError_t launch_dz(const T* W, const T* H_act, int64_t d, int64_t V, int64_t v
                      int vs, const int32_t* count, int64_t c0, int C, int cpad,
                      const LogitXform& xf, const float* w_scale, const float* hs_act,
                      const float* coef, const float* lse_c, const int32_t* y_c,
-                     const float* tgt_c, typename DzOut<T>::type* dZ, hipStream_t s) {
+                     const float* tgt_c, typename DzOut<T>::type* dZ, hipStream_t s, bool rest) {
   ScopedKernelTimer timer_(KK_DZ, s);
   (void)V;
   const int tm = cdiv(vs_valid, kBM), tn = cdiv(C, kBN);
+  if constexpr (std::is_same<T, float>::value) {
+    if (rest) {
+      const auto k = xf.softcap ? k_dz<float, true, true> : k_dz<float, false, true>;
+      hipLaunchKernelGGL(k, dim3(xcd_grid(tm * tn)), dim3(kThreads), 0, s, W, H_act, d, v0,
+                         vs_valid, vs, count, c0, C, cpad, tm, tn, xf, w_scale, hs_act, coef,
+                         lse_c, y_c, tgt_c, dZ);
+      return hipGetLastError();
+    }
+  }
+  (void)rest;
   if (xf.softcap)
     hipLaunchKernelGGL((k_dz<T, true>), dim3(xcd_grid(tm * tn)), dim3(kThreads), 0, s, W, H_act, d, v0,
                        vs_valid, vs, count, c0, C, cpad, tm, tn, xf, w_scale, hs_act, coef, lse_c,
@@ -1261,10 +1279,11 @@ hipError_t launch_dh_gemm(const T* W, int64_t v0, int vs_valid, const T* dZ, int
 template <typename T>
 hipError_t launch_dw_gemm(const T* HT, int cpad, const T* dZ, int vs, int64_t d, int64_t v0,
                           int vs_valid, const int32_t* count, int64_t c0, int C, float* dW,
-                          hipStream_t s) {
+                          hipStream_t s, bool first) {
   ScopedKernelTimer timer_(KK_DW_GEMM, s);
   const int tm = cdiv(vs_valid, kBM), tn = cdiv(d, kBN);
-  hipLaunchKernelGGL(k_dw_gemm<T>, dim3(xcd_grid(tm * tn)), dim3(kThreads), 0, s, HT, cpad, dZ, vs, d, v0,
+  const auto k = first ? k_dw_first<T> : k_dw_gemm<T>;
+  hipLaunchKernelGGL(k, dim3(xcd_grid(tm * tn)), dim3(kThreads), 0, s, HT, cpad, dZ, vs, d, v0,
                      vs_valid, count, c0, C, tm, tn, dW);
   return hipGetLastError();
 }
@@ -1309,18 +1328,19 @@ hipError_t launch_gemm_nt(const T* A, const T* B, int64_t M, int64_t N, int64_t 
   template hipError_t launch_bwd_prep<T>(const T*, int64_t, const int32_t*, const int32_t*,       \
                                          int64_t, int, int, const int32_t*, const uint8_t*,        \
                                          const float*, const float*, const float*, const float*,  \
-                                         const float*, int64_t, float, float, const LogitXform&,  \
+                                         const float*, const float*, int64_t, float, float,       \
+                                         const LogitXform&,                                       \
                                          const LossVariant&, const int32_t*, int64_t, T*, float*,  \
                                          float*, int32_t*, float*, hipStream_t);                  \
   template hipError_t launch_dz<T>(const T*, const T*, int64_t, int64_t, int64_t, int, int,       \
                                    const int32_t*, int64_t, int, int, const LogitXform&,         \
                                    const float*, const float*, const float*, const float*,        \
-                                   const int32_t*, const float*, T*, hipStream_t);                \
+                                   const int32_t*, const float*, T*, hipStream_t, bool);          \
   template hipError_t launch_dh_gemm<T>(const T*, int64_t, int, const T*, int, int64_t,           \
                                         const int32_t*, int64_t, int, int, int, int, float*,      \
                                         hipStream_t);                                             \
   template hipError_t launch_dw_gemm<T>(const T*, int, const T*, int, int64_t, int64_t, int,      \
-                                        const int32_t*, int64_t, int, float*, hipStream_t);       \
+                                        const int32_t*, int64_t, int, float*, hipStream_t, bool); \
   template hipError_t launch_dh_scatter<T>(const float*, int, int, int64_t, const int32_t*,      \
                                            const int32_t*, int64_t, int, T*, hipStream_t);        \
   template hipError_t launch_gemm_nt<T>(const T*, const T*, int64_t, int64_t, int64_t, float*,    \
@@ -1336,7 +1356,7 @@ template hipError_t launch_dz<uint8_t>(const uint8_t*, const uint8_t*, int64_t, 
                                          int, int, const int32_t*, int64_t, int, int,
                                          const LogitXform&, const float*, const float*,
                                          const float*, const float*, const int32_t*, const float*,
-                                         __bf16*, hipStream_t);
+                                         __bf16*, hipStream_t, bool);
 template hipError_t launch_lse_partials<uint8_t>(const uint8_t*, const uint8_t*, const int32_t*,
                                                  int64_t, int64_t, int, int, const LogitXform&,
                                                  const float*, const float*, float*, float*,

@@ -82,12 +82,13 @@ hipError_t launch_transpose(const T* in, int64_t R, int64_t Cc, T* out, int64_t 
                             hipStream_t s);
 
 // grad_lp: the tokens' coefficients (then adv, ref_lp and what the loss has are not used), or null.
+// rest: what float32 left of lse, put into tgt_c in the place of the target's entry, or null.
 template <typename T>
 hipError_t launch_bwd_prep(const T* H, int64_t d, const int32_t* idx, const int32_t* count,
                            int64_t c0, int C, int cpad, const int32_t* y, const uint8_t* mask,
                            const float* adv, const float* ref_lp, const float* lp,
-                           const float* lse, const float* grad_lp, int64_t L, float beta,
-                           float grad_loss, const LogitXform& xf, const LossVariant& lv,
+                           const float* lse, const float* grad_lp, const float* rest, int64_t L,
+                           float beta, float grad_loss, const LogitXform& xf, const LossVariant& lv,
                            const int32_t* seq_n, int64_t B, T* H_act, float* coef, float* lse_c,
                            int32_t* y_c, float* tgt_c, hipStream_t s);
 
@@ -97,12 +98,14 @@ template <> struct DzOut<uint8_t> { typedef __bf16 type; };
 
 // dZ: the slab, vs / 256 strips of [cpad][256].  T = uint8_t: fp8 operands (w_scale,
 // hs_act as in k_lse_partials), bf16 dZ; other T: both scale pointers unused (null).
+// rest (float32 only): tgt_c holds what float32 left of lse.
 template <typename T>
 hipError_t launch_dz(const T* W, const T* H_act, int64_t d, int64_t V, int64_t v0, int vs_valid,
                      int vs, const int32_t* count, int64_t c0, int C, int cpad,
                      const LogitXform& xf, const float* w_scale, const float* hs_act,
                      const float* coef, const float* lse_c, const int32_t* y_c,
-                     const float* tgt_c, typename DzOut<T>::type* dZ, hipStream_t s);
+                     const float* tgt_c, typename DzOut<T>::type* dZ, hipStream_t s,
+                     bool rest = false);
 
 // The fp8 codes and scales of chunk c's active tokens, for the fp8 recompute.
 hipError_t launch_fp8_gather_rows(const uint8_t* H8, const float* h_scale, int64_t d,
@@ -118,11 +121,11 @@ hipError_t launch_dh_gemm(const T* W, int64_t v0, int vs_valid, const T* dZ, int
                           float* dH_acc, hipStream_t s);
 
 // dZ is the slab of strips [vs / 256][cpad][256] (each strip read K-major);
-// C * vs * sizeof(T) must be < 2^31.
+// C * vs * sizeof(T) must be < 2^31.  first: dW is written instead of added to.
 template <typename T>
 hipError_t launch_dw_gemm(const T* HT, int cpad, const T* dZ, int vs, int64_t d, int64_t v0,
                           int vs_valid, const int32_t* count, int64_t c0, int C, float* dW,
-                          hipStream_t s);
+                          hipStream_t s, bool first = false);
 
 template <typename T>
 hipError_t launch_dh_scatter(const float* dH_acc, int nsplit, int cpad, int64_t d,
@@ -130,6 +133,29 @@ hipError_t launch_dh_scatter(const float* dH_acc, int nsplit, int cpad, int64_t 
                              hipStream_t s);
 
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t s);
+
+// The 64 x 64 tiles of tile64.hip (float32; the gradients in bfloat16 too).
+// launch64_lse: partials of ceil(V / 64) vocabulary tiles in part_m and part_s [tiles][C] and the
+// target logits in zy [C].
+// launch64_merge: lp, lse and what float32 leaves of it (rest) from such partials, or those of
+// launch_lse_partials (stride: cpad).
+// launch64_dz: dZ [C][vpad], vpad = V rounded up to 64, its columns from V on 0.  rest may be null.
+// launch64_grads: dH [C, d] and dW [V, d], either null; with more than one share of the
+// vocabulary, parts holds shares x C x d floats.
+hipError_t launch64_lse(const float* W, const float* H, const int32_t* y, int64_t V, int64_t d, int C,
+                        const LogitXform& xf, float* part_m, float* part_s, float* zy,
+                        hipStream_t s);
+hipError_t launch64_merge(const float* part_m, const float* part_s, const float* zy,
+                          const int32_t* y, int64_t V, int tiles, int64_t stride, int C, float* lp,
+                          float* lse, float* rest, hipStream_t s);
+template <typename T>
+hipError_t launch64_dz(const T* W, const T* H, const int32_t* y, const float* lp, const float* lse,
+                       const float* rest, const float* grad_lp, int64_t V, int64_t d, int C,
+                       int64_t vpad, const LogitXform& xf, T* dZ, hipStream_t s);
+template <typename T>
+hipError_t launch64_grads(const T* W, const T* H, const T* dZ, const float* grad_lp, int64_t V,
+                          int64_t d, int C, int64_t vpad, int shares, T* dH, float* parts,
+                          int accumulate, float* dW, hipStream_t s);
 
 // Plain tile GEMM C[m][n] = sum_k A[m][k] B[n][k] into float32 C (diagnostic).
 template <typename T>

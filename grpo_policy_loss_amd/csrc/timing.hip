@@ -24,7 +24,8 @@ const char* const kNames[KK_COUNT] = {
     "gemm_nt",    "seq_counts", "fp8_quantize", "fp8_dequantize",
     "norm_fwd", "norm_bwd", "norm_reduce", "adamw", "moment_values", "sample_mass", "sample_cut",
     "sample_pick", "clip_loss_fwd", "clip_loss_bwd", "pref_loss_fwd", "pref_loss_bwd",
-    "loss_finish", "grad_norm", "grad_norm_finish", "grad_clip"};
+    "loss_finish", "grad_norm", "grad_norm_finish", "grad_clip", "lse64", "merge64", "dz64",
+    "grads64", "join64"};
 
 }  // namespace
 

@@ -43,6 +43,11 @@ enum KernelKind {
   KK_GRAD_NORM,
   KK_GRAD_FINISH,
   KK_GRAD_CLIP,
+  KK_LSE64,
+  KK_MERGE64,
+  KK_DZ64,
+  KK_GRADS64,
+  KK_JOIN64,
   KK_COUNT
 };
 

@@ -68,7 +68,9 @@ typedef enum {
   GRPO_OP_REF = 0,     /* grpo_ref_logprobs */
   GRPO_OP_FWD = 1,     /* grpo_loss_fwd */
   GRPO_OP_BWD = 2,     /* grpo_loss_bwd, default (fastest) dZ slab */
-  GRPO_OP_BWD_MIN = 3  /* grpo_loss_bwd, the least workspace it accepts */
+  GRPO_OP_BWD_MIN = 3, /* grpo_loss_bwd, the least workspace it accepts */
+  GRPO_OP_LOGPROBS_FWD = 4, /* grpo_logprobs_fwd */
+  GRPO_OP_LOGPROBS_BWD = 5  /* grpo_logprobs_bwd */
 } grpo_op;
 
 /*
@@ -333,13 +335,17 @@ int grpo_loss_fwd_noalloc(const void* H, const void* W, const int32_t* y, const 
  *   lp_t = z_{t, y_t} - lse_t,  dZ_t = g_t (onehot(y_t) - softmax(z_t)) dz/d(w h)
  *   dH_t = dZ_t W               dW += sum_t dZ_t^T h_t
  * with z the transformed logits of the opts (NULL: plain) and g = grad_lp, the loss's gradient
- * with respect to lp.  The kernels of grpo_loss_fwd and grpo_loss_bwd.
- * grpo_logprobs_fwd: lp and lse [N] float32, written; workspace
- *   grpo_workspace_bytes(GRPO_OP_FWD, ...).
+ * with respect to lp.
+ * grpo_logprobs_fwd: lp [N] and lse, float32, written.  With GRPO_BF16 lse has N elements, and both
+ *   are bitwise grpo_ref_logprobs's and grpo_loss_fwd's.  With GRPO_F32 lse has 2 N, behind each
+ *   token's value what its rounding to float32 left, N elements on; lp is formed without that rounding,
+ *   and equals theirs within it.
  * grpo_logprobs_bwd: lp and lse as the forward of the same inputs and opts wrote them.  A token with
- *   g_t = 0 is not visited, whatever its other values are: its row of dH is 0.  dH [N, d] dtype,
+ *   g_t = 0 has no part in it, whatever its other values are: its row of dH is 0.  dH [N, d] dtype,
  *   OVERWRITTEN; dW [V, d] float32, ACCUMULATED if accumulate is 1, OVERWRITTEN if it is 0; either
- *   may be NULL and is then not formed.  workspace as in grpo_loss_bwd.
+ *   may be NULL and is then not formed.
+ * workspace: grpo_workspace_bytes(GRPO_OP_LOGPROBS_FWD or GRPO_OP_LOGPROBS_BWD, ...).  A smaller chunk
+ *   needs less; results depend on it through the order in which dW's and, in bfloat16, dH's parts are summed.
  * dtype GRPO_F32 or GRPO_BF16.  Only the logit transform of the opts is used.
  */
 int grpo_logprobs_fwd(const void* H, const void* W, const int32_t* y, int64_t N, int64_t d,

@@ -36,9 +36,32 @@ def check(i, t, chunk=4096, opts=None, k=1.0, cap=0.0):
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
 @pytest.mark.parametrize("N,d,V,chunk", [(1, 8, 2, 1), (1, 64, 1000, 4096), (3, 16, 1, 2), (255, 40, 257, 4096), (256, 256, 256, 256),
-                                         (300, 320, 1003, 128), (513, 72, 2051, 512), (40, 1024, 5003, 16)])
+                                         (300, 320, 1003, 128), (513, 72, 2051, 512), (40, 1024, 5003, 16), (65, 200, 6401, 4096),
+                                         (64, 64, 20000, 4096), (1500, 64, 1100, 700), (130, 520, 64, 100)])
 def test_sizes(t, N, d, V, chunk):
     check(inputs(N, d, V, t, seed=N), t, chunk)
+
+
+@pytest.mark.parametrize("t,N,d,V,chunk", [("bf16", 700, 512, 12100, 256), ("bf16", 700, 512, 12100, 4096), ("f32", 2050, 1024, 8300, 4096),
+                                           ("f32", 2050, 1024, 8300, 900), ("f32", 256, 256, 65500, 4096)])
+def test_sizes_of_the_large_tiles(t, N, d, V, chunk):
+    i = inputs(N, d, V, t, seed=N)
+    lp, lse, dH, dW = check(i, t, chunk)
+    # dW written and dW added to, and each gradient alone
+    args = (i["H"], i["W"], i["y"], lp, lse, i["g"], chunk)
+    into = torch.full_like(dW, 0.5)
+    gp.grpo_logprobs_bwd(*args, dW=into, need_h=False)
+    assert ((into - 0.5 - dW).abs() <= 8 * plain_update.U * (1 + dW.abs())).all()
+    assert torch.equal(gp.grpo_logprobs_bwd(*args, need_w=False)[0], dH)
+    i["g"].zero_()
+    dH, dW = gp.grpo_logprobs_bwd(*args)
+    assert not dH.any() and not dW.any()
+
+
+@pytest.mark.parametrize("N,d,V", [(2050, 1024, 8300), (256, 256, 65500)])
+def test_large_tiles_with_a_cap(N, d, V):
+    i = inputs(N, d, V, "f32", seed=1)
+    check(i, "f32", 4096, {"logit_softcapping": 3.0, "temperature": 0.8}, 1 / 0.8, 3.0)
 
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
@@ -50,18 +73,23 @@ def test_logit_transforms(t, opts, k, cap):
 
 @pytest.mark.parametrize("t", ["f32", "bf16"])
 def test_forward_is_the_reference_calls_and_the_loss_s(t):
-    """The same kernels: lp bitwise grpo_ref_logprobs's, and the loss's gradient given as grad_lp bitwise
-    the loss's backward up to the rounding of the coefficients (half a step each way)."""
+    """bfloat16: lp and lse bitwise grpo_ref_logprobs's and the loss's; float32: within lse's rounding and
+    that of the logits (64 products each way).  The loss's gradient given as grad_lp: the loss's
+    backward up to the roundings of coefficients and of each."""
     B, L, d, V = 3, 50, 64, 900
     i = inputs(B * L, d, V, t)
     mask = (torch.rand(B * L, device="cuda") < 0.6).to(torch.uint8)
     adv = torch.randn(B, device="cuda")
     ref = gp.grpo_ref_logprobs(i["H"], i["W"], i["y"]) + 0.1
     lp, lse = gp.grpo_logprobs_fwd(i["H"], i["W"], i["y"])
-    assert torch.equal(lp, gp.grpo_ref_logprobs(i["H"], i["W"], i["y"]))
+    plain = gp.grpo_ref_logprobs(i["H"], i["W"], i["y"])
     loss, lp2, kl, lse2 = gp.grpo_loss_fwd(i["H"], i["W"], i["y"], mask, adv, ref, B, L)
-    assert torch.equal(lp, lp2) and torch.equal(lse, lse2)
-    dH, dW = gp.grpo_loss_bwd(i["H"], i["W"], i["y"], mask, adv, ref, lp, lse, B, L)
+    if t == "bf16":
+        assert torch.equal(lp, plain) and torch.equal(lp, lp2) and torch.equal(lse, lse2)
+    else:
+        near = plain_update.logprobs(i["H"], i["W"], i["y"], i["g"])["lp_tol"].cuda()
+        assert ((lp - lp2).abs() <= 2 * near).all() and ((lse[:B * L] - lse2).abs() <= 2 * near).all()
+    dH, dW = gp.grpo_loss_bwd(i["H"], i["W"], i["y"], mask, adv, ref, lp2, lse2, B, L)
     ours, stats, w = gp.grpo_clip_loss_fwd(lp, mask, adv, B, L, ref_lp=ref, beta=0.04)
     g = gp.grpo_clip_loss_bwd(lp, mask, adv, w, B, L, ref_lp=ref, beta=0.04)
     dH2, dW2 = gp.grpo_logprobs_bwd(i["H"], i["W"], i["y"], lp, lse, g)

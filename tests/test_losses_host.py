@@ -108,6 +108,20 @@ def test_pref_backward_argument_errors(at, value, code):
     assert L.grpo_last_error()
 
 
+def test_head_workspaces():
+    """No tokens x vocabulary beyond a slab of 1.25 GiB, or of 64 tokens; fp8 and bad shapes have none."""
+    for op in (4, 5):
+        assert L.grpo_workspace_bytes(op, 64, 64, 500, 2, 64) == 0 == L.grpo_workspace_bytes(op, 0, 64, 500, 1, 64)
+        assert L.grpo_workspace_bytes(op, 64, 62, 500, 0, 64) == 0
+    for dt in (0, 1):
+        for n, w, v, chunk in ((1, 64, 2, 1), (64, 1536, 151936, 4096), (4096, 1536, 151936, 4096), (163840, 4096, 128256, 8192), (8192, 64, 100, 8192),
+                               (1 << 24, 64, 100000, 1 << 20)):
+            fwd, bwd = (L.grpo_workspace_bytes(op, n, w, v, dt, chunk) for op in (4, 5))
+            c = min(n, chunk)
+            assert fwd == L.grpo_workspace_bytes(1, n, w, v, 1, chunk) if dt else 0 < fwd <= 3 << 30
+            assert 0 < bwd <= (5 << 28) + 256 * 4 * v + 64 * c * w + 16 * n + (64 << 20) + 4 * 1024 * 64 * 64 * 8, (n, w, v, dt, bwd)
+
+
 def test_workspaces_are_bounded():
     """A few thousand partial results at most, or one a row where there are more rows of more than 1024 tokens."""
     for rows in (1, 3, 8, 1021, 4096, 5000, 100003, 1 << 20):
@@ -156,7 +170,8 @@ def test_binding_logprobs_refusals(over, err, what):
 
 
 @pytest.mark.parametrize("over,err,what", [
-    ({"lp": torch.zeros(N, dtype=torch.float64)}, TypeError, "lp"), ({"lse": torch.zeros(N - 1)}, ValueError, "lse"),
+    ({"lp": torch.zeros(N, dtype=torch.float64)}, TypeError, "lp"), ({"lse": torch.zeros(2 * N)}, ValueError, "lse"),
+    ({"H": torch.zeros(N, d), "W": torch.zeros(V, d)}, ValueError, "lse"),      # float32: 2 N
     ({"grad_lp": torch.zeros(N, dtype=torch.bfloat16)}, TypeError, "grad_lp"), ({"grad_lp": torch.zeros(1)}, ValueError, "grad_lp"),
     ({"dH": torch.zeros(N, d)}, TypeError, "dH"), ({"dW": torch.zeros(V, d, dtype=torch.bfloat16)}, TypeError, "dW"),
     ({"dW": torch.zeros(V, d + 1)}, ValueError, "dW"), ({"need_h": False, "need_w": False}, ValueError, "need")])
