@@ -35,38 +35,73 @@ def _lse_size(N, dt):
     return 2 * N if dt == GRPO_F32 else N
 
 
-def _head_workspace(op, N, d, V, dt, chunk, device, workspace):
+@functools.lru_cache(maxsize=256)
+def _head_bytes(op, N, d, V, dt, chunk):
     need = grpo_workspace_bytes(op, N, d, V, dt, chunk)
     if need == 0:
         _check("grpo_workspace_bytes", -1)
-    return _workspace(need, device, workspace)
+    return need
+
+
+def _logprobs_fwd(H, W, y, chunk, workspace, opts, sizes, on):
+    """The call itself, of tensors that were checked: (lp, lse, chunk)."""
+    N, d, V, dt = sizes
+    ctx, stream = on
+    dev = H.device
+    with ctx:
+        if chunk == 0:
+            chunk = auto_chunk(1, N, d, V, dt)
+        ws = _workspace(_head_bytes(GRPO_OP_LOGPROBS_FWD, N, d, V, dt, chunk), dev, workspace)
+        lp = torch.empty(N, dtype=torch.float32, device=dev)
+        lse = torch.empty(_lse_size(N, dt), dtype=torch.float32, device=dev)
+        _check("grpo_logprobs_fwd", lib().grpo_logprobs_fwd(
+            H.data_ptr(), W.data_ptr(), y.data_ptr(), N, d, V, dt, chunk, opts, lp.data_ptr(),
+            lse.data_ptr(), ws.data_ptr(), ws.numel(), stream))
+    return lp, lse, chunk
+
+
+def _logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk, dW, dH, workspace, opts, need_h, need_w, sizes, on):
+    """The call itself, of tensors that were checked: (dH, dW)."""
+    N, d, V, dt = sizes
+    ctx, stream = on
+    dev = H.device
+    accumulate = int(need_w and dW is not None)
+    with ctx:
+        if chunk == 0:
+            chunk = auto_chunk(1, N, d, V, dt)
+        ws = _workspace(_head_bytes(GRPO_OP_LOGPROBS_BWD, N, d, V, dt, chunk), dev, workspace)
+        if not need_h:
+            dH = None
+        elif dH is None:
+            dH = torch.empty(N, d, dtype=H.dtype, device=dev)
+        if not need_w:
+            dW = None
+        elif dW is None:
+            dW = torch.empty(V, d, dtype=torch.float32, device=dev)
+        _check("grpo_logprobs_bwd", lib().grpo_logprobs_bwd(
+            H.data_ptr(), W.data_ptr(), y.data_ptr(), lp.data_ptr(), lse.data_ptr(),
+            grad_lp.data_ptr(), N, d, V, dt, chunk, opts, accumulate, _ptr(dH), _ptr(dW),
+            ws.data_ptr(), ws.numel(), stream))
+    return dH, dW
 
 
 def grpo_logprobs_fwd(H, W, y, chunk: int = 4096, workspace=None, opts=None):
     """(lp [N], lse), float32: the log-probability of y under softmax of the logits of H [N, d]
     (float32 or bfloat16) and W [V, d], and the log-sum-exp that the backward takes ([N]; for
-    float32 [2 N], its rounding behind it).  `opts` and chunk as for grpo_loss_fwd; of the options the logit transform counts."""
-    N, d, V, dt = _head(H, W, y)
-    ctx, stream = _on(*(t for t in (H, W, y, workspace) if t is not None))
-    with ctx:
-        if chunk == 0:
-            chunk = auto_chunk(1, N, d, V, dt)
-        ws = _head_workspace(GRPO_OP_LOGPROBS_FWD, N, d, V, dt, chunk, H.device, workspace)
-        lp = torch.empty(N, dtype=torch.float32, device=H.device)
-        lse = torch.empty(_lse_size(N, dt), dtype=torch.float32, device=H.device)
-        _check("grpo_logprobs_fwd", lib().grpo_logprobs_fwd(
-            _ptr(H), _ptr(W), _ptr(y), N, d, V, dt, chunk, _opts(opts), _ptr(lp), _ptr(lse),
-            _ptr(ws), ws.numel(), stream))
-    return lp, lse
+    float32 [2 N], its rounding behind it).  `opts` and chunk as for grpo_loss_fwd; of the
+    options the logit transform counts."""
+    sizes = _head(H, W, y)
+    on = _on(*(t for t in (H, W, y, workspace) if t is not None))
+    return _logprobs_fwd(H, W, y, chunk, workspace, _opts(opts), sizes, on)[:2]
 
 
 def grpo_logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk: int = 4096, dW=None, dH=None,
                       workspace=None, opts=None, need_h: bool = True, need_w: bool = True):
     """(dH [N, d] in H's type, dW [V, d] float32) of a loss whose gradient with respect to
-    lp is grad_lp [N] float32.  Tokens with a gradient of 0 are not visited: their rows of dH
+    lp is grad_lp [N] float32.  Tokens with a gradient of 0 have no part in it: their rows of dH
     are 0.  dW is accumulated into when given.  need_h or need_w false: that one is not
     formed, and None.  lp, lse and `opts` are the forward's."""
-    N, d, V, dt = _head(H, W, y)
+    sizes = N, d, V, dt = _head(H, W, y)
     for t, name, n in ((lp, "lp", N), (lse, "lse", _lse_size(N, dt)), (grad_lp, "grad_lp", N)):
         _arg(t, name, dtype=torch.float32, numel=n)
     if not (need_h or need_w):
@@ -75,24 +110,9 @@ def grpo_logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk: int = 4096, dW=None, dH=
         _arg(dH, "dH", dtype=H.dtype, shape=(N, d))
     if dW is not None:
         _arg(dW, "dW", dtype=torch.float32, shape=(V, d))
-    accumulate = dW is not None
-    ctx, stream = _on(*(t for t in (H, W, y, lp, lse, grad_lp, dH, dW, workspace) if t is not None))
-    with ctx:
-        if chunk == 0:
-            chunk = auto_chunk(1, N, d, V, dt)
-        ws = _head_workspace(GRPO_OP_LOGPROBS_BWD, N, d, V, dt, chunk, H.device, workspace)
-        if not need_h:
-            dH = None
-        elif dH is None:
-            dH = torch.empty_like(H)
-        if not need_w:
-            dW = None
-        elif dW is None:
-            dW = torch.empty(V, d, dtype=torch.float32, device=H.device)
-        _check("grpo_logprobs_bwd", lib().grpo_logprobs_bwd(
-            _ptr(H), _ptr(W), _ptr(y), _ptr(lp), _ptr(lse), _ptr(grad_lp), N, d, V, dt, chunk,
-            _opts(opts), int(accumulate), _ptr(dH), _ptr(dW), _ptr(ws), ws.numel(), stream))
-    return dH, dW
+    on = _on(*(t for t in (H, W, y, lp, lse, grad_lp, dH, dW, workspace) if t is not None))
+    return _logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk, dW, dH, workspace, _opts(opts), need_h, need_w,
+                         sizes, on)
 
 
 # ---------------------------------------------------------------- clipped policy loss

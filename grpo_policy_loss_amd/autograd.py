@@ -12,10 +12,11 @@ from __future__ import annotations
 
 import torch
 
-from ._lib import AGG_TOKEN_MEAN, KL_REVERSE, grpo_loss_bwd, grpo_loss_fwd
-from ._losses import (PREF_SIGMOID, RATIO_TOKEN, grpo_clip_loss_bwd, grpo_clip_loss_fwd,
-                      grpo_logprobs_bwd, grpo_logprobs_fwd, grpo_pref_loss_bwd, grpo_pref_loss_fwd)
-from ._ops import NORM_LAYER, NORM_RMS, grpo_norm_bwd, grpo_norm_fwd
+from ._lib import AGG_TOKEN_MEAN, KL_REVERSE, _opts, grpo_loss_bwd, grpo_loss_fwd
+from ._losses import (PREF_SIGMOID, RATIO_TOKEN, _head, _logprobs_bwd, _logprobs_fwd,
+                      grpo_clip_loss_bwd, grpo_clip_loss_fwd, grpo_pref_loss_bwd,
+                      grpo_pref_loss_fwd)
+from ._ops import NORM_LAYER, NORM_RMS, _on, grpo_norm_bwd, grpo_norm_fwd
 
 
 class _GrpoLoss(torch.autograd.Function):
@@ -102,9 +103,10 @@ def grpo_norm(X, weight, bias=None, eps: float = 1e-5, kind: int = NORM_RMS):
 class _GrpoLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, H, W, y, chunk, opts):
-        lp, lse = grpo_logprobs_fwd(H, W, y, chunk, opts=opts)
+        sizes, opts = _head(H, W, y), _opts(opts)
+        lp, lse, chunk = _logprobs_fwd(H, W, y, chunk, None, opts, sizes, _on(H, W, y))
         ctx.save_for_backward(H, W, y, lp, lse)
-        ctx.args = chunk, opts
+        ctx.args = chunk, opts, sizes
         return lp
 
     @staticmethod
@@ -112,12 +114,12 @@ class _GrpoLogprobs(torch.autograd.Function):
     def backward(ctx, grad_lp):
         _refuse_capture("grpo_logprobs", "grpo_logprobs_bwd")
         H, W, y, lp, lse = ctx.saved_tensors
-        chunk, opts = ctx.args
+        chunk, opts, sizes = ctx.args
         need_h, need_w = ctx.needs_input_grad[:2]
-        # an upstream gradient may be a broadcast view (that of a sum is)
-        dH, dW = grpo_logprobs_bwd(H, W, y, lp, lse, grad_lp.contiguous(), chunk, opts=opts,
-                                   need_h=need_h, need_w=need_w)
-        return dH, None if dW is None else dW.to(W.dtype), None, None, None
+        grad_lp = grad_lp.contiguous()       # it may be a broadcast view (that of a sum is)
+        dH, dW = _logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk, None, None, None, opts, need_h, need_w,
+                               sizes, _on(H, W, y, grad_lp))
+        return dH, dW if dW is None or dW.dtype == W.dtype else dW.to(W.dtype), None, None, None
 
 
 def grpo_logprobs(H, W, y, chunk: int = 4096, opts=None):
