@@ -25,17 +25,30 @@ namespace grpo {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRowTokens = 1024;   // the longest row that a wave takes whole
-constexpr int kMaxBlocks = 2048;   // of the first form: 8 blocks on each of 256 CUs
+constexpr int kRowTokens = 1024;   // the longest row that a wave takes whole, or kManyTokens of
+constexpr int kManyTokens = 8192;  // rows enough to fill the chip with waves
+constexpr int kManyItems = 4096;
+constexpr int kMaxBlocks = 1024;   // of the first form: 4 blocks on each of 256 CUs
 constexpr int kMaxParts = 4096;    // segments of the second form, unless there are more rows
 constexpr int kFinish = 1024;      // threads of the finish
+// 2^24 tokens, us of the forward (clipped loss with an old and a reference policy | preference loss
+// without one, 84 MB):
+//                     8 tokens a lane   16          1 load ahead   4           2048 blocks
+//   65536 rows of 256   60 | 29         54 | 25     68 | 42        83 | 36     59 | 25
+//   32768 rows of 511   55 | 30         53 | 25     61 | 31        82 | 37     55 | 25
+//   16384 rows of 1024  55 | 25         52 | 25     61 | 25        83 | 38     55 | 25
+// (4 loads ahead leave two waves a SIMD, and 6 waves asked of the compiler spill: 114 | 43.)
+constexpr int kAhead = 2;          // loads of each array that a lane has on their way
+constexpr int kLaneTokens = 16;    // of a row that is shorter than 64 lanes' worth
 
 typedef __attribute__((ext_vector_type(4), aligned(4))) float F4;
 typedef __attribute__((ext_vector_type(4), aligned(1))) uint8_t U4;
 
-// Elements [c, c + 4) of a row of n; those at n and behind it read as zero.
+// Four elements of a row of n for the lane whose turn is [c, c + 4): those, or the row's last four
+// where they pass its end, so that no load is under a condition and several stay on their way.
+// Rows of less than four read element by element, zeros behind them.
 __device__ __forceinline__ F4 load4(const float* row, int c, int n) {
-  if (c + 4 <= n) return *(const F4*)(row + c);
+  if (n >= 4) return *(const F4*)(row + min(c, n - 4));
   F4 v = {};
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -43,13 +56,15 @@ __device__ __forceinline__ F4 load4(const float* row, int c, int n) {
   return v;
 }
 __device__ __forceinline__ U4 load4(const uint8_t* row, int c, int n) {
-  if (c + 4 <= n) return *(const U4*)(row + c);
+  if (n >= 4) return *(const U4*)(row + min(c, n - 4));
   U4 v = {};
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (c + j < n) v[j] = row[c + j];
   return v;
 }
+// The first of the four that is this lane's.
+__device__ __forceinline__ int first4(int c, int n) { return n >= 4 ? c - min(c, n - 4) : 0; }
 
 // Sums over the lanes of a group of `width` (a power of two up to 64).
 template <typename T>
@@ -138,44 +153,62 @@ struct ClipSums {
   int n, low, high, pad;
 };
 
-// Adds tokens [c, c + 4) of a row of n that starts at token t0 to the sums.  loss is the policy
+// Four tokens of a row of n that starts at token t0, and their part of the sums: loss is the policy
 // term alone, and nothing where the ratio is the sequence's (SEQ).  A masked token counts as one with
 // all logarithms 0 and no advantage, which adds nothing.
 template <bool SEQ>
-__device__ __forceinline__ void clip_add(const ClipArgs& a, int64_t t0, int c, int n, float adv_row,
-                                         ClipSums& s) {
-  const U4 m4 = load4(a.mask + t0, c, n);
-  const F4 lp4 = load4(a.lp + t0, c, n);
-  F4 old4 = {}, ref4 = {}, adv4 = {};
-  if (a.old_lp != nullptr) old4 = load4(a.old_lp + t0, c, n);
-  if (a.ref_lp != nullptr) ref4 = load4(a.ref_lp + t0, c, n);
-  if (a.adv_per_token) adv4 = load4(a.adv + t0, c, n);
-  float loss = 0.f, kl = 0.f, excess = 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const bool m = m4[j] != 0;
-    s.n += m;
-    const float lp = m ? lp4[j] : 0.f;
-    const double D = a.old_lp != nullptr ? (double)lp - (double)(m ? old4[j] : 0.f) : 0.0;
-    if (SEQ) {
-      s.d += D;
-    } else {
-      const float adv = m ? (a.adv_per_token ? adv4[j] : adv_row) : 0.f;
-      const Exp v = exp_excess((float)D);
-      float r = v.e;
-      excess += v.excess;
-      const Clipped at = clip_ratio(a, adv, D, r);
-      s.low += at.low;
-      s.high += at.high;
-      loss = fmaf(-adv, r, loss);
-    }
-    if (a.ref_lp != nullptr) {
-      kl += kl_term(a.kl, (m ? ref4[j] : 0.f) - lp, lp);
-    }
+struct ClipQuad {
+  U4 m4;
+  F4 lp4, old4, ref4, adv4;
+  int first;
+
+  __device__ __forceinline__ void load(const ClipArgs& a, int64_t t0, int c, int n) {
+    first = first4(c, n);
+    m4 = load4(a.mask + t0, c, n);
+    lp4 = load4(a.lp + t0, c, n);
+    if (a.old_lp != nullptr) old4 = load4(a.old_lp + t0, c, n);
+    if (a.ref_lp != nullptr) ref4 = load4(a.ref_lp + t0, c, n);
+    if (!SEQ && a.adv_per_token) adv4 = load4(a.adv + t0, c, n);
   }
-  s.loss += loss;
-  s.kl += kl;
-  s.excess += excess;
+  __device__ __forceinline__ void add(const ClipArgs& a, float adv_row, ClipSums& s) const {
+    float loss = 0.f, kl = 0.f, excess = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool m = m4[j] != 0 && j >= first;
+      s.n += m;
+      const float lp = m ? lp4[j] : 0.f;
+      const double D = a.old_lp != nullptr ? (double)lp - (double)(m ? old4[j] : 0.f) : 0.0;
+      if (SEQ) {
+        s.d += D;
+      } else {
+        const float adv = m ? (a.adv_per_token ? adv4[j] : adv_row) : 0.f;
+        const Exp v = exp_excess((float)D);
+        float r = v.e;
+        excess += v.excess;
+        const Clipped at = clip_ratio(a, adv, D, r);
+        s.low += at.low;
+        s.high += at.high;
+        loss = fmaf(-adv, r, loss);
+      }
+      if (a.ref_lp != nullptr) kl += kl_term(a.kl, (m ? ref4[j] : 0.f) - lp, lp);
+    }
+    s.loss += loss;
+    s.kl += kl;
+    s.excess += excess;
+  }
+};
+
+// All tokens of a row of n, `lanes` lanes apart, kAhead loads of each array ahead.
+template <bool SEQ>
+__device__ __forceinline__ void clip_row(const ClipArgs& a, int64_t t0, int n, int lane, int lanes,
+                                         float adv, ClipSums& s) {
+  for (int c = lane * 4; c < n; c += lanes * 4 * kAhead) {
+    ClipQuad<SEQ> q[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) q[k].load(a, t0, c + k * lanes * 4, n);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) q[k].add(a, adv, s);
+  }
 }
 
 // What a sequence's own sums decide, in one lane for the sequence: the ratio's terms (SEQ; in
@@ -254,7 +287,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int64_t b = (int64_t)blockIdx.x * (kThreads / width) + threadIdx.x / width; b < a.B; b += groups) {
     const float adv = a.adv_per_token ? 0.f : a.adv[b];
     ClipSums row = {};
-    for (int c = lane * 4; c < a.L; c += width * 4) clip_add<SEQ>(a, b * a.L, c, a.L, adv, row);
+    clip_row<SEQ>(a, b * a.L, a.L, lane, width, adv, row);
     const int n = row.n;
     double inv = 1.0;
     if (SEQ || a.seq_mean) {
@@ -285,7 +318,7 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t from = (int64_t)seg * span;
   const int n = (int)min<int64_t>(span, a.L - from);
   ClipSums s = {};
-  for (int c = threadIdx.x * 4; c < n; c += kThreads * 4) clip_add<SEQ>(a, b * a.L + from, c, n, adv, s);
+  clip_row<SEQ>(a, b * a.L + from, n, threadIdx.x, kThreads, adv, s);
   clip_block_sum<kThreads>(s);
   if (threadIdx.x == 0) parts[blockIdx.x] = s;
 }
@@ -355,8 +388,10 @@ __global__ void __launch_bounds__(kThreads)
     k_clip_bwd(ClipArgs a, Divide by, int64_t N, const float* __restrict__ grad_loss,
                float* __restrict__ grad_lp) {
   const int64_t t0 = (int64_t)blockIdx.x * (kThreads * 4);
-  const int n = (int)min<int64_t>(kThreads * 4, N - t0), c = threadIdx.x * 4;
+  const int n = (int)min<int64_t>(kThreads * 4, N - t0);
+  int c = threadIdx.x * 4;
   if (c >= n) return;
+  c -= first4(c, n);     // where they pass the end, two lanes form the same gradients
   float g = a.weights[2 * a.B];
   if (grad_loss != nullptr) g *= *grad_loss;
   const U4 m4 = load4(a.mask + t0, c, n);
@@ -410,18 +445,43 @@ struct PrefSums {
   int n, pad;
 };
 
-__device__ __forceinline__ void pref_add(const PrefArgs& a, int64_t t0, int c, int n, PrefSums& s) {
-  const U4 m4 = load4(a.mask + t0, c, n);
-  const F4 lp4 = load4(a.lp + t0, c, n);
-  F4 ref4 = {};
-  if (a.ref_lp != nullptr) ref4 = load4(a.ref_lp + t0, c, n);
+struct PrefQuad {
+  U4 m4;
+  F4 lp4, ref4;
+  int first;
+
+  __device__ __forceinline__ void load(const PrefArgs& a, int64_t t0, int c, int n) {
+    first = first4(c, n);
+    m4 = load4(a.mask + t0, c, n);
+    lp4 = load4(a.lp + t0, c, n);
+    if (a.ref_lp != nullptr) ref4 = load4(a.ref_lp + t0, c, n);
+  }
+  __device__ __forceinline__ void add(const PrefArgs& a, PrefSums& s) const {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const bool m = m4[j] != 0;
-    const double lp = m ? (double)lp4[j] : 0.0;
-    s.n += m;
-    s.lp += lp;
-    if (a.ref_lp != nullptr) s.d += lp - (m ? (double)ref4[j] : 0.0);
+    for (int j = 0; j < 4; ++j) {
+      const bool m = m4[j] != 0 && j >= first;
+      const double lp = m ? (double)lp4[j] : 0.0;
+      s.n += m;
+      s.lp += lp;
+      if (a.ref_lp != nullptr) s.d += lp - (m ? (double)ref4[j] : 0.0);
+    }
+  }
+};
+
+// All tokens of `ROWS` rows of n that lie `apart` tokens apart.
+template <int ROWS>
+__device__ __forceinline__ void pref_row(const PrefArgs& a, int64_t t0, int64_t apart, int n, int lane,
+                                         int lanes, PrefSums (&s)[ROWS]) {
+  for (int c = lane * 4; c < n; c += lanes * 4 * kAhead) {
+    PrefQuad q[ROWS][kAhead];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) q[r][k].load(a, t0 + r * apart, c + k * lanes * 4, n);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) q[r][k].add(a, s[r]);
   }
 }
 
@@ -496,14 +556,10 @@ __global__ void __launch_bounds__(kThreads)
   const bool with_d = a.ref_lp != nullptr, with_lp = !with_d || a.nll != 0.0;
   double s = 0.0;
   for (int64_t p = (int64_t)blockIdx.x * (kThreads / width) + threadIdx.x / width; p < a.P; p += groups) {
-    PrefSums chosen = {}, rejected = {};
-    const int64_t t0 = 2 * p * a.L;
-    for (int c = lane * 4; c < a.L; c += width * 4) {
-      pref_add(a, t0, c, a.L, chosen);
-      pref_add(a, t0 + a.L, c, a.L, rejected);
-    }
-    chosen = pref_group_sum(chosen, width, with_lp, with_d);
-    rejected = pref_group_sum(rejected, width, with_lp, with_d);
+    PrefSums two[2] = {};
+    pref_row<2>(a, 2 * p * a.L, a.L, a.L, lane, width, two);
+    const PrefSums chosen = pref_group_sum(two[0], width, with_lp, with_d);
+    const PrefSums rejected = pref_group_sum(two[1], width, with_lp, with_d);
     if (lane == 0) s += pref_pair(a, p, chosen, rejected);
   }
   s = block_sum<kThreads>(s);
@@ -517,10 +573,10 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t b = blockIdx.x / (unsigned)segs;
   const int64_t from = (int64_t)(blockIdx.x - b * segs) * span;
   const int n = (int)min<int64_t>(span, a.L - from);
-  PrefSums s = {};
-  for (int c = threadIdx.x * 4; c < n; c += kThreads * 4) pref_add(a, b * a.L + from, c, n, s);
+  PrefSums one[1] = {};
+  pref_row<1>(a, b * a.L + from, 0, n, threadIdx.x, kThreads, one);
   __shared__ PrefSums waves[kThreads / 64];
-  s = pref_group_sum(s, 64, true, true);
+  PrefSums s = pref_group_sum(one[0], 64, true, true);
   if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x != 0) return;
@@ -566,8 +622,10 @@ __global__ void __launch_bounds__(kThreads)
                const float* __restrict__ grad_loss, Divide by, int64_t N,
                float* __restrict__ grad_lp) {
   const int64_t t0 = (int64_t)blockIdx.x * (kThreads * 4);
-  const int n = (int)min<int64_t>(kThreads * 4, N - t0), c = threadIdx.x * 4;
+  const int n = (int)min<int64_t>(kThreads * 4, N - t0);
+  int c = threadIdx.x * 4;
   if (c >= n) return;
+  c -= first4(c, n);
   const float g = grad_loss != nullptr ? *grad_loss : 1.f;
   const U4 m4 = load4(mask + t0, c, n);
   F4 out;
@@ -603,8 +661,8 @@ struct Split {
 
 Split split_rows(int64_t items, int64_t rows, int64_t L) {
   Split p{};
-  if (L <= kRowTokens) {
-    p.width = pow2_at_least((L + 3) / 4, 64);
+  if (L <= kRowTokens || (items >= kManyItems && L <= kManyTokens)) {
+    p.width = pow2_at_least((L + kLaneTokens - 1) / kLaneTokens, 64);
     const int64_t per = kThreads / p.width;
     p.blocks = (int)std::min<int64_t>((items + per - 1) / per, kMaxBlocks);
     p.parts = p.blocks == 1 ? 0 : p.blocks;
@@ -744,6 +802,8 @@ int grpo_clip_loss_bwd(const float* lp, const float* old_lp, const float* ref_lp
   const int64_t N = B * L;
   const unsigned blocks = (unsigned)((N + grpo::kThreads * 4 - 1) / (grpo::kThreads * 4));
   const grpo::Divide by = grpo::divider(L);
+  for (const float* in : {lp, old_lp, ref_lp, adv})
+    if (in == grad_lp) return fail(GRPO_ERR_INVALID_ARG, "grad_lp is one of the inputs");
   if (a.beta == 0.0) a.ref_lp = nullptr;
   if (opts != nullptr && opts->ratio == GRPO_RATIO_SEQUENCE)
     grpo::k_clip_bwd<true><<<blocks, grpo::kThreads, 0, s>>>(a, by, N, grad_loss, grad_lp);
