@@ -112,7 +112,7 @@ SIGNATURES = {
     "grpo_logprobs_fwd": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _int, _i64, _OPTS_P, _vp, _vp,
                                  _vp, _sz, _vp]),
     "grpo_logprobs_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _i64,
-                                 _OPTS_P, _int, _vp, _vp, _vp, _sz, _vp]),
+                                 _OPTS_P, _int, _int, _vp, _vp, _vp, _sz, _vp]),
     "grpo_clip_loss_workspace_bytes": (_sz, [_i64, _i64]),
     "grpo_clip_loss_fwd": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, ctypes.POINTER(ClipOpts), _vp,
                                   _vp, _vp, _vp, _sz, _vp]),

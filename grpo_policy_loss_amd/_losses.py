@@ -60,8 +60,10 @@ def _logprobs_fwd(H, W, y, chunk, workspace, opts, sizes, on):
     return lp, lse, chunk
 
 
-def _logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk, dW, dH, workspace, opts, need_h, need_w, sizes, on):
-    """The call itself, of tensors that were checked: (dH, dW)."""
+def _logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk, dW, dH, workspace, opts, need_h, need_w, sizes, on,
+                  like_w=False):
+    """The call itself, of tensors that were checked: (dH, dW).  like_w: a dW that is made is of
+    W's type where one chunk takes all tokens."""
     N, d, V, dt = sizes
     ctx, stream = on
     dev = H.device
@@ -77,11 +79,12 @@ def _logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk, dW, dH, workspace, opts, nee
         if not need_w:
             dW = None
         elif dW is None:
-            dW = torch.empty(V, d, dtype=torch.float32, device=dev)
+            dW = torch.empty(V, d, dtype=W.dtype if like_w and N <= chunk else torch.float32, device=dev)
         _check("grpo_logprobs_bwd", lib().grpo_logprobs_bwd(
             H.data_ptr(), W.data_ptr(), y.data_ptr(), lp.data_ptr(), lse.data_ptr(),
-            grad_lp.data_ptr(), N, d, V, dt, chunk, opts, accumulate, _ptr(dH), _ptr(dW),
-            ws.data_ptr(), ws.numel(), stream))
+            grad_lp.data_ptr(), N, d, V, dt, chunk, opts, accumulate,
+            GRPO_F32 if dW is None else _dt(dW), _ptr(dH), _ptr(dW), ws.data_ptr(), ws.numel(),
+            stream))
     return dH, dW
 
 

@@ -118,13 +118,13 @@ class _GrpoLogprobs(torch.autograd.Function):
         need_h, need_w = ctx.needs_input_grad[:2]
         grad_lp = grad_lp.contiguous()       # it may be a broadcast view (that of a sum is)
         dH, dW = _logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk, None, None, None, opts, need_h, need_w,
-                               sizes, _on(H, W, y, grad_lp))
+                               sizes, _on(H, W, y, grad_lp), like_w=True)
         return dH, dW if dW is None or dW.dtype == W.dtype else dW.to(W.dtype), None, None, None
 
 
 def grpo_logprobs(H, W, y, chunk: int = 4096, opts=None):
     """The log-probabilities [N] float32 of y, differentiable (once) with respect to H and W:
-    for any loss over them.  Arguments as for grpo_logprobs_fwd.  W's gradient is formed in
+    for any loss over them.  Arguments as for grpo_logprobs_fwd.  W's gradient is summed in
     float32 and returned in W's type (grpo_logprobs_bwd with a float32 dW accumulator keeps it
     in float32); tokens whose gradient is 0 cost nothing.  The backward raises while its stream is
     captured into a graph, as grpo_norm's does."""

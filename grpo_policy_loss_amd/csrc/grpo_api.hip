@@ -236,7 +236,9 @@ bool small_tiles_fwd(int64_t N, int64_t d, int64_t V, int dtype) {
 //   4096  8000    222   1313    307   1352   1041  1501   3958  2774
 bool small_tiles_bwd(int64_t N, int64_t d, int64_t V, int dtype) {
   const double products = (double)N * (double)V * (double)d;
-  if (dtype == GRPO_BF16) return products <= (N <= 128 ? 8589934592.0 : 4294967296.0);
+  // (and a dZ of at most 1 GiB, so that one chunk takes all tokens whenever the caller's does)
+  if (dtype == GRPO_BF16)
+    return products <= (N <= 128 ? 8589934592.0 : 4294967296.0) && (double)N * (double)V <= 536870912.0;
   const int64_t dt = (d + 255) / 256;
   return dt * ((N + 255) / 256) < 32 || dt * ((V + 255) / 256) < 128 || products < 1.6e10;
 }
@@ -382,8 +384,12 @@ struct Fp8Recompute {
 };
 
 // grad_lp: the loss's gradient with respect to lp is given (mask, adv and ref_lp are not used), and
-// rest, what float32 left of lse, or null.  A null dH or dW is not formed; dw_first: dW is
-// written instead of added to.
+// rest, what float32 left of lse, or null.  A null dH or dW is not formed.  into: how dW is written.
+enum class DwInto {
+  kSum,     // added to
+  kNew,     // written by the first chunk, added to by the others
+  kBf16     // bfloat16, written by the only chunk
+};
 template <typename T>
 int bwd_pass(const T* H, const T* W, const int32_t* y, const uint8_t* mask, const float* adv,
              const float* ref_lp, const float* lp, const float* lse, const float* grad_lp,
@@ -391,7 +397,7 @@ int bwd_pass(const T* H, const T* W, const int32_t* y, const uint8_t* mask, cons
              int64_t chunk, const grpo::LogitXform& xf, const grpo::LossVariant& lv, T* dH,
              float* dW, const BwdPlan& p, char* ws, hipStream_t s,
              const Fp8Recompute& f8 = Fp8Recompute(), const float* rest = nullptr,
-             bool dw_first = false) {
+             DwInto into = DwInto::kSum) {
   int32_t* idx = (int32_t*)(ws + p.o_idx);
   int32_t* cnt = (int32_t*)(ws + p.o_cnt);
   T* H_act = (T*)(ws + p.o_hact);
@@ -435,9 +441,17 @@ int bwd_pass(const T* H, const T* W, const int32_t* y, const uint8_t* mask, cons
       if (dH != nullptr)
         GRPO_HIP(grpo::launch_dh_gemm<T>(W, v0, vs_valid, dZ, (int)p.vs, d, cnt, c0, C,
                                          (int)p.cpad, (int)p.nsplit, sl == 0 ? 1 : 0, dH_acc, s));
-      if (dW != nullptr)
+      if (dW == nullptr) continue;
+      if (into == DwInto::kSum || c > 0) {
         GRPO_HIP(grpo::launch_dw_gemm<T>(HT, (int)p.cpad, dZ, (int)p.vs, d, v0, vs_valid, cnt, c0,
-                                         C, dW, s, dw_first && c == 0));
+                                         C, dW, s));
+      } else if (into == DwInto::kNew) {
+        GRPO_HIP((grpo::launch_dw_first<T, float>(HT, (int)p.cpad, dZ, d, v0, vs_valid, cnt, c0, C,
+                                                  dW, s)));
+      } else if constexpr (sizeof(T) == 2) {
+        GRPO_HIP((grpo::launch_dw_first<T, __bf16>(HT, (int)p.cpad, dZ, d, v0, vs_valid, cnt, c0, C,
+                                                   (__bf16*)(void*)dW, s)));
+      }
     }
     if (dH == nullptr) continue;
     GRPO_HIP(grpo::launch_dh_scatter<T>(dH_acc, (int)p.nsplit, (int)p.cpad, d, idx, cnt, c0, C, dH,
@@ -449,8 +463,8 @@ int bwd_pass(const T* H, const T* W, const int32_t* y, const uint8_t* mask, cons
 template <typename T>
 int logprobs_bwd64(const T* H, const T* W, const int32_t* y, const float* lp, const float* lse,
                    const float* grad_lp, int64_t N, int64_t d, int64_t V, int64_t chunk,
-                   const grpo::LogitXform& xf, int accumulate, T* dH, float* dW, char* ws,
-                   hipStream_t s) {
+                   const grpo::LogitXform& xf, int accumulate, int dw_bf16, T* dH, void* dW,
+                   char* ws, hipStream_t s) {
   const Plan64 p = plan64_bwd(N, d, V, (int64_t)sizeof(T), chunk);
   for (int64_t c0 = 0; c0 < N; c0 += p.C) {
     const int C = (int)std::min(p.C, N - c0);
@@ -460,7 +474,7 @@ int logprobs_bwd64(const T* H, const T* W, const int32_t* y, const float* lp, co
                                   C, p.vpad, xf, (T*)ws, s));
     GRPO_HIP(grpo::launch64_grads<T>(W, H + c0 * d, (const T*)ws, grad_lp + c0, V, d, C, p.vpad,
                                      (int)p.shares, dH == nullptr ? nullptr : dH + c0 * d,
-                                     (float*)(ws + p.o_parts), accumulate || c0 > 0, dW, s));
+                                     (float*)(ws + p.o_parts), accumulate || c0 > 0, dw_bf16, dW, s));
   }
   return GRPO_OK;
 }
@@ -754,8 +768,9 @@ int grpo_logprobs_fwd(const void* H, const void* W, const int32_t* y, int64_t N,
 
 int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const float* lp,
                       const float* lse, const float* grad_lp, int64_t N, int64_t d, int64_t V,
-                      int dtype, int64_t chunk, const grpo_opts* opts, int accumulate, void* dH,
-                      float* dW, void* workspace, size_t workspace_bytes, void* stream) {
+                      int dtype, int64_t chunk, const grpo_opts* opts, int accumulate,
+                      int dw_dtype, void* dH, void* dW, void* workspace, size_t workspace_bytes,
+                      void* stream) {
   grpo::clear_error();
   grpo::LogitXform xf;
   grpo::LossVariant lv;
@@ -772,6 +787,11 @@ int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const floa
     return fail(GRPO_ERR_INVALID_ARG, "accumulate %d is not 0 or 1", accumulate);
   const int st = check_shape(N, d, V, dtype, chunk);
   if (st != GRPO_OK) return st;
+  const bool bf16_dw = dw_dtype == GRPO_BF16;
+  if (dw_dtype != GRPO_F32 && !(bf16_dw && dtype == GRPO_BF16))
+    return fail(GRPO_ERR_INVALID_ARG, "dw_dtype %d is neither GRPO_F32 nor the head's type", dw_dtype);
+  if (bf16_dw && (accumulate || chunk < N))
+    return fail(GRPO_ERR_INVALID_ARG, "a bfloat16 dW is written from one chunk: accumulate 0, chunk >= N");
   hipStream_t s = (hipStream_t)stream;
   if (small_tiles_bwd(N, d, V, dtype)) {
     const size_t need = grpo_workspace_bytes(GRPO_OP_LOGPROBS_BWD, N, d, V, dtype, chunk);
@@ -780,9 +800,10 @@ int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const floa
                   workspace == nullptr ? (size_t)0 : workspace_bytes);
     if (dtype == GRPO_F32)
       return logprobs_bwd64<float>((const float*)H, (const float*)W, y, lp, lse, grad_lp, N, d, V,
-                                   chunk, xf, accumulate, (float*)dH, dW, (char*)workspace, s);
+                                   chunk, xf, accumulate, 0, (float*)dH, dW, (char*)workspace, s);
     return logprobs_bwd64<__bf16>((const __bf16*)H, (const __bf16*)W, y, lp, lse, grad_lp, N, d, V,
-                                  chunk, xf, accumulate, (__bf16*)dH, dW, (char*)workspace, s);
+                                  chunk, xf, accumulate, bf16_dw, (__bf16*)dH, dW,
+                                  (char*)workspace, s);
   }
   // a caller's size is always a size, as in grpo_loss_bwd_ex
   const int64_t wsb = std::max<int64_t>(1, (int64_t)std::min<size_t>(workspace_bytes, (size_t)INT64_MAX));
@@ -792,13 +813,14 @@ int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const floa
                 plan_bwd(N, d, V, dtype, chunk, -1).total,
                 workspace == nullptr ? (size_t)0 : workspace_bytes);
   lv = grpo::LossVariant{0, 0, 0};
+  const DwInto into = bf16_dw ? DwInto::kBf16 : accumulate ? DwInto::kSum : DwInto::kNew;
   if (dtype == GRPO_BF16)
     return bwd_pass<__bf16>((const __bf16*)H, (const __bf16*)W, y, nullptr, nullptr, nullptr, lp,
-                            lse, grad_lp, N, 1, d, V, 0.f, 0.f, chunk, xf, lv, (__bf16*)dH, dW, p,
-                            (char*)workspace, s, Fp8Recompute(), nullptr, !accumulate);
+                            lse, grad_lp, N, 1, d, V, 0.f, 0.f, chunk, xf, lv, (__bf16*)dH,
+                            (float*)dW, p, (char*)workspace, s, Fp8Recompute(), nullptr, into);
   return bwd_pass<float>((const float*)H, (const float*)W, y, nullptr, nullptr, nullptr, lp, lse,
-                         grad_lp, N, 1, d, V, 0.f, 0.f, chunk, xf, lv, (float*)dH, dW, p,
-                         (char*)workspace, s, Fp8Recompute(), lse + N, !accumulate);
+                         grad_lp, N, 1, d, V, 0.f, 0.f, chunk, xf, lv, (float*)dH, (float*)dW, p,
+                         (char*)workspace, s, Fp8Recompute(), lse + N, into);
 }
 
 // ---------------------------------------------------------------- fp8 e4m3 path

@@ -844,6 +844,28 @@ __device__ __forceinline__ void store_tile_f32(float* base, int rows, int64_t m0
   }
 }
 
+// The tile written as bfloat16 (SW's layout): 4 adjacent columns of a row a lane.
+__device__ __forceinline__ void store_tile_bf16(__bf16* base, int rows, int64_t m0, int64_t d,
+                                                const Acc& acc) {
+  typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4_t;
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, (uint32_t)((int64_t)rows * d * 2));
+  const int wr = (wave >> 1) * 128, wc = (wave & 1) * 128;
+#pragma unroll
+  for (int j = 0; j < kWN; ++j) {
+    const uint32_t r = (uint32_t)(wr + 16 * j + (lane & 15)) * (uint32_t)d * 2u;
+#pragma unroll
+    for (int i = 0; i < kWM; ++i) {
+      const int64_t nd = m0 + wc + 16 * i + 4 * (lane >> 4);
+      const f32x4_t& x = acc[j][i];
+      const bf16x4_t q = {(__bf16)x[0], (__bf16)x[1], (__bf16)x[2], (__bf16)x[3]};
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, q), rs,
+                                            nd < d ? r + (uint32_t)nd * 2u : kOOB, 0, 0);
+    }
+  }
+}
+
 // dH partial of split `sp`: vocabulary columns [k0, k1) of the slab.  Split
 // sp accumulates into its own buffer dH_acc[sp], so no two workgroups ever
 // write the same element and the final sum over splits has a fixed order.
@@ -900,11 +922,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // hidden-state chunk.
 // The blocks are computed transposed (SWAP), so each lane holds four
 // consecutive hidden columns of one vocabulary row, as dW's rows are laid out.
-// FIRST: dW is written, with zeros where no token is active, instead of added to.
-template <typename T, bool FIRST>
+// FIRST: dW is written, with zeros where no token is active, instead of added to; it may then be
+// bfloat16 (D).
+template <typename T, bool FIRST, typename D>
 __device__ __forceinline__ void dw_tile(const T* HT, int cpad, const T* dZ, int64_t d, int64_t v0,
                                         int vs_valid, const int32_t* count, int64_t c0, int C,
-                                        int tm, int tn, float* dW, char GRPO_LDS* lds) {
+                                        int tm, int tn, D* dW, char GRPO_LDS* lds) {
   int n_act = count[0] - (int)c0;
   n_act = n_act < 0 ? 0 : (n_act > C ? C : n_act);
   if (n_act <= 0 && !FIRST) return;
@@ -924,7 +947,10 @@ __device__ __forceinline__ void dw_tile(const T* HT, int cpad, const T* dZ, int6
   tile_mainloop<T, true, false, true>(acc, A, B, k_slices_of(kb), lds);
 
   const int rows = (vs_valid - m0) < kBM ? (vs_valid - m0) : kBM;
-  store_tile_f32<true>(dW + (v0 + m0) * d, rows, n0, d, acc, !FIRST);
+  if constexpr (sizeof(D) == 4)
+    store_tile_f32<true>(dW + (v0 + m0) * d, rows, n0, d, acc, !FIRST);
+  else
+    store_tile_bf16(dW + (v0 + m0) * d, rows, n0, d, acc);
 }
 
 template <typename T>
@@ -933,17 +959,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               int64_t v0, int vs_valid, const int32_t* __restrict__ count, int64_t c0, int C,
               int tm, int tn, float* __restrict__ dW) {
   __shared__ __attribute__((aligned(1024))) char smem[kLdsBytes];
-  dw_tile<T, false>(HT, cpad, dZ, d, v0, vs_valid, count, c0, C, tm, tn, dW,
-                    (char GRPO_LDS*)smem);
+  dw_tile<T, false, float>(HT, cpad, dZ, d, v0, vs_valid, count, c0, C, tm, tn, dW,
+                           (char GRPO_LDS*)smem);
 }
 
-template <typename T>
+template <typename T, typename D>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_dw_first(const T* __restrict__ HT, int cpad, const T* __restrict__ dZ, int vs, int64_t d,
-               int64_t v0, int vs_valid, const int32_t* __restrict__ count, int64_t c0, int C,
-               int tm, int tn, float* __restrict__ dW) {
+    k_dw_first(const T* __restrict__ HT, int cpad, const T* __restrict__ dZ, int64_t d, int64_t v0,
+               int vs_valid, const int32_t* __restrict__ count, int64_t c0, int C, int tm, int tn,
+               D* __restrict__ dW) {
   __shared__ __attribute__((aligned(1024))) char smem[kLdsBytes];
-  dw_tile<T, true>(HT, cpad, dZ, d, v0, vs_valid, count, c0, C, tm, tn, dW, (char GRPO_LDS*)smem);
+  dw_tile<T, true, D>(HT, cpad, dZ, d, v0, vs_valid, count, c0, C, tm, tn, dW,
+                      (char GRPO_LDS*)smem);
 }
 
 template <typename T>
@@ -1279,12 +1306,22 @@ hipError_t launch_dh_gemm(const T* W, int64_t v0, int vs_valid, const T* dZ, int
 template <typename T>
 hipError_t launch_dw_gemm(const T* HT, int cpad, const T* dZ, int vs, int64_t d, int64_t v0,
                           int vs_valid, const int32_t* count, int64_t c0, int C, float* dW,
-                          hipStream_t s, bool first) {
+                          hipStream_t s) {
   ScopedKernelTimer timer_(KK_DW_GEMM, s);
   const int tm = cdiv(vs_valid, kBM), tn = cdiv(d, kBN);
-  const auto k = first ? k_dw_first<T> : k_dw_gemm<T>;
-  hipLaunchKernelGGL(k, dim3(xcd_grid(tm * tn)), dim3(kThreads), 0, s, HT, cpad, dZ, vs, d, v0,
+  hipLaunchKernelGGL(k_dw_gemm<T>, dim3(xcd_grid(tm * tn)), dim3(kThreads), 0, s, HT, cpad, dZ, vs, d, v0,
                      vs_valid, count, c0, C, tm, tn, dW);
+  return hipGetLastError();
+}
+
+template <typename T, typename D>
+hipError_t launch_dw_first(const T* HT, int cpad, const T* dZ, int64_t d, int64_t v0,
+                           int vs_valid, const int32_t* count, int64_t c0, int C, D* dW,
+                           hipStream_t s) {
+  ScopedKernelTimer timer_(KK_DW_GEMM, s);
+  const int tm = cdiv(vs_valid, kBM), tn = cdiv(d, kBN);
+  hipLaunchKernelGGL((k_dw_first<T, D>), dim3(xcd_grid(tm * tn)), dim3(kThreads), 0, s, HT, cpad,
+                     dZ, d, v0, vs_valid, count, c0, C, tm, tn, dW);
   return hipGetLastError();
 }
 
@@ -1340,7 +1377,10 @@ hipError_t launch_gemm_nt(const T* A, const T* B, int64_t M, int64_t N, int64_t 
                                         const int32_t*, int64_t, int, int, int, int, float*,      \
                                         hipStream_t);                                             \
   template hipError_t launch_dw_gemm<T>(const T*, int, const T*, int, int64_t, int64_t, int,      \
-                                        const int32_t*, int64_t, int, float*, hipStream_t, bool); \
+                                        const int32_t*, int64_t, int, float*, hipStream_t);       \
+  template hipError_t launch_dw_first<T, float>(const T*, int, const T*, int64_t, int64_t, int,   \
+                                                const int32_t*, int64_t, int, float*,             \
+                                                hipStream_t);                                     \
   template hipError_t launch_dh_scatter<T>(const float*, int, int, int64_t, const int32_t*,      \
                                            const int32_t*, int64_t, int, T*, hipStream_t);        \
   template hipError_t launch_gemm_nt<T>(const T*, const T*, int64_t, int64_t, int64_t, float*,    \
@@ -1352,6 +1392,9 @@ template hipError_t launch_active_scan<float>(const float*, int64_t, int32_t*, i
                                               hipStream_t);
 GRPO_INSTANTIATE(float)
 GRPO_INSTANTIATE(__bf16)
+template hipError_t launch_dw_first<__bf16, __bf16>(const __bf16*, int, const __bf16*, int64_t,
+                                                    int64_t, int, const int32_t*, int64_t, int,
+                                                    __bf16*, hipStream_t);
 template hipError_t launch_dz<uint8_t>(const uint8_t*, const uint8_t*, int64_t, int64_t, int64_t,
                                          int, int, const int32_t*, int64_t, int, int,
                                          const LogitXform&, const float*, const float*,

@@ -121,11 +121,16 @@ hipError_t launch_dh_gemm(const T* W, int64_t v0, int vs_valid, const T* dZ, int
                           float* dH_acc, hipStream_t s);
 
 // dZ is the slab of strips [vs / 256][cpad][256] (each strip read K-major);
-// C * vs * sizeof(T) must be < 2^31.  first: dW is written instead of added to.
+// C * vs * sizeof(T) must be < 2^31.
 template <typename T>
 hipError_t launch_dw_gemm(const T* HT, int cpad, const T* dZ, int vs, int64_t d, int64_t v0,
                           int vs_valid, const int32_t* count, int64_t c0, int C, float* dW,
-                          hipStream_t s, bool first = false);
+                          hipStream_t s);
+// The same with dW written instead of added to, in float32 or (of bfloat16 operands) bfloat16.
+template <typename T, typename D>
+hipError_t launch_dw_first(const T* HT, int cpad, const T* dZ, int64_t d, int64_t v0,
+                           int vs_valid, const int32_t* count, int64_t c0, int C, D* dW,
+                           hipStream_t s);
 
 template <typename T>
 hipError_t launch_dh_scatter(const float* dH_acc, int nsplit, int cpad, int64_t d,
@@ -140,8 +145,8 @@ hipError_t launch_zero(void* p, size_t bytes, hipStream_t s);
 // launch64_merge: lp, lse and what float32 leaves of it (rest) from such partials, or those of
 // launch_lse_partials (stride: cpad).
 // launch64_dz: dZ [C][vpad], vpad = V rounded up to 64, its columns from V on 0.  rest may be null.
-// launch64_grads: dH [C, d] and dW [V, d], either null; with more than one share of the
-// vocabulary, parts holds shares x C x d floats.
+// launch64_grads: dH [C, d] and dW [V, d] (float32, or with dw_bf16 and accumulate 0 bfloat16), either
+// null; with more than one share of the vocabulary, parts holds shares x C x d floats.
 hipError_t launch64_lse(const float* W, const float* H, const int32_t* y, int64_t V, int64_t d, int C,
                         const LogitXform& xf, float* part_m, float* part_s, float* zy,
                         hipStream_t s);
@@ -155,7 +160,7 @@ hipError_t launch64_dz(const T* W, const T* H, const int32_t* y, const float* lp
 template <typename T>
 hipError_t launch64_grads(const T* W, const T* H, const T* dZ, const float* grad_lp, int64_t V,
                           int64_t d, int C, int64_t vpad, int shares, T* dH, float* parts,
-                          int accumulate, float* dW, hipStream_t s);
+                          int accumulate, int dw_bf16, void* dW, hipStream_t s);
 
 // Plain tile GEMM C[m][n] = sum_k A[m][k] B[n][k] into float32 C (diagnostic).
 template <typename T>

@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads64)
     k64_grads(const T* __restrict__ W, const T* __restrict__ H, const T* __restrict__ dZ,
               const float* __restrict__ grad_lp, int V, int d, int C, int vpad, int h_grid, int shares,
               int share_v, T* __restrict__ dH, float* __restrict__ parts, int accumulate,
-              float* __restrict__ dW) {
+              int dw_bf16, void* __restrict__ dW) {
   __shared__ __attribute__((aligned(16))) T lds[4 * kSlot<T>];
   const int tm = (d + kT - 1) / kT;
   int mt, nt;
@@ -441,9 +441,16 @@ __global__ void __launch_bounds__(kThreads64)
     for (int i = 0; i < 2; ++i) {
       const int n = n0 + row64(i);
       if (v >= V || n >= d) continue;
-      typedef typename Four<float>::type V4;
-      V4* to = (V4*)(dW + (int64_t)v * d + n);
-      *to = accumulate ? *to + (V4)acc[i][j] : (V4)acc[i][j];
+      if (dw_bf16) {
+        typename Four<__bf16>::type q;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[e] = (__bf16)acc[i][j][e];
+        *(typename Four<__bf16>::type*)((__bf16*)dW + (int64_t)v * d + n) = q;
+      } else {
+        typedef typename Four<float>::type V4;
+        V4* to = (V4*)((float*)dW + (int64_t)v * d + n);
+        *to = accumulate ? *to + (V4)acc[i][j] : (V4)acc[i][j];
+      }
     }
   }
 }
@@ -498,7 +505,7 @@ hipError_t launch64_dz(const T* W, const T* H, const int32_t* y, const float* lp
 template <typename T>
 hipError_t launch64_grads(const T* W, const T* H, const T* dZ, const float* grad_lp, int64_t V,
                           int64_t d, int C, int64_t vpad, int shares, T* dH, float* parts,
-                          int accumulate, float* dW, hipStream_t s) {
+                          int accumulate, int dw_bf16, void* dW, hipStream_t s) {
   const int tm = cdiv(d, kT);
   const int64_t h = dH != nullptr ? tile_grid((int64_t)tm * cdiv(C, kT) * shares) : 0;
   const int64_t w = dW != nullptr ? tile_grid((int64_t)tm * cdiv(V, kT)) : 0;
@@ -506,7 +513,7 @@ hipError_t launch64_grads(const T* W, const T* H, const T* dZ, const float* grad
     ScopedKernelTimer timer(KK_GRADS64, s);
     const int share_v = cdiv(vpad / kT, shares) * kT;
     k64_grads<T><<<(unsigned)(h + w), kThreads64, 0, s>>>(W, H, dZ, grad_lp, (int)V, (int)d, C, (int)vpad, (int)h,
-                                                         shares, share_v, dH, parts, accumulate, dW);
+                                                         shares, share_v, dH, parts, accumulate, dw_bf16, dW);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -522,7 +529,7 @@ hipError_t launch64_grads(const T* W, const T* H, const T* dZ, const float* grad
                                      const float*, const float*, const float*, int64_t, int64_t,  \
                                      int, int64_t, const LogitXform&, T*, hipStream_t);           \
   template hipError_t launch64_grads<T>(const T*, const T*, const T*, const float*, int64_t,      \
-                                        int64_t, int, int64_t, int, T*, float*, int, float*,      \
+                                        int64_t, int, int64_t, int, T*, float*, int, int, void*,  \
                                         hipStream_t);
 GRPO_INSTANTIATE64(float)
 GRPO_INSTANTIATE64(__bf16)

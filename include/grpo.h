@@ -342,8 +342,9 @@ int grpo_loss_fwd_noalloc(const void* H, const void* W, const int32_t* y, const 
  *   and equals theirs within it.
  * grpo_logprobs_bwd: lp and lse as the forward of the same inputs and opts wrote them.  A token with
  *   g_t = 0 has no part in it, whatever its other values are: its row of dH is 0.  dH [N, d] dtype,
- *   OVERWRITTEN; dW [V, d] float32, ACCUMULATED if accumulate is 1, OVERWRITTEN if it is 0; either
- *   may be NULL and is then not formed.
+ *   OVERWRITTEN; dW [V, d] dw_dtype, ACCUMULATED if accumulate is 1, OVERWRITTEN if it is 0; either
+ *   may be NULL and is then not formed.  dw_dtype is GRPO_F32, or with a bfloat16 head, accumulate 0
+ *   and chunk >= N also GRPO_BF16: then each sum is rounded once.
  * workspace: grpo_workspace_bytes(GRPO_OP_LOGPROBS_FWD or GRPO_OP_LOGPROBS_BWD, ...).  A smaller chunk
  *   needs less; results depend on it through the order in which dW's and, in bfloat16, dH's parts are summed.
  * dtype GRPO_F32 or GRPO_BF16.  Only the logit transform of the opts is used.
@@ -353,8 +354,9 @@ int grpo_logprobs_fwd(const void* H, const void* W, const int32_t* y, int64_t N,
                       float* lse, void* workspace, size_t workspace_bytes, void* stream);
 int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const float* lp,
                       const float* lse, const float* grad_lp, int64_t N, int64_t d, int64_t V,
-                      int dtype, int64_t chunk, const grpo_opts* opts, int accumulate, void* dH,
-                      float* dW, void* workspace, size_t workspace_bytes, void* stream);
+                      int dtype, int64_t chunk, const grpo_opts* opts, int accumulate,
+                      int dw_dtype, void* dH, void* dW, void* workspace, size_t workspace_bytes,
+                      void* stream);
 
 /*
  * The clipped policy loss over given log-probabilities, for steps in which the policy is no longer

@@ -90,10 +90,10 @@ static void rejected_calls() {
   CHECK(grpo_pref_loss_bwd(&m, &f, nullptr, INT64_MAX, 1, &f, nullptr) == GRPO_ERR_UNSUPPORTED);
   CHECK(grpo_logprobs_fwd(FAKE, FAKE, &y, INT64_MAX, 16, 32, GRPO_BF16, 8, nullptr, &f, &f, FAKE, 1 << 20, nullptr) ==
         GRPO_ERR_UNSUPPORTED);
-  CHECK(grpo_logprobs_bwd(FAKE, FAKE, &y, &f, &f, &f, 8, 16, 32, GRPO_BF16, 8, nullptr, 0, FAKE, &f, FAKE, 64, nullptr) ==
+  CHECK(grpo_logprobs_bwd(FAKE, FAKE, &y, &f, &f, &f, 8, 16, 32, GRPO_BF16, 8, nullptr, 0, GRPO_F32, FAKE, &f, FAKE, 64, nullptr) ==
         GRPO_ERR_WORKSPACE);
-  CHECK(grpo_logprobs_bwd(FAKE, FAKE, &y, &f, &f, &f, 8, 16, 32, GRPO_FP8_E4M3, 8, nullptr, 0, FAKE, &f, FAKE, 1 << 20,
-                          nullptr) == GRPO_ERR_INVALID_ARG);
+  CHECK(grpo_logprobs_bwd(FAKE, FAKE, &y, &f, &f, &f, 8, 16, 32, GRPO_FP8_E4M3, 8, nullptr, 0, GRPO_F32, FAKE, &f, FAKE,
+                          1 << 20, nullptr) == GRPO_ERR_INVALID_ARG);
 }
 
 int main() {

@@ -53,9 +53,15 @@ def test_sizes_of_the_large_tiles(t, N, d, V, chunk):
     gp.grpo_logprobs_bwd(*args, dW=into, need_h=False)
     assert ((into - 0.5 - dW).abs() <= 8 * plain_update.U * (1 + dW.abs())).all()
     assert torch.equal(gp.grpo_logprobs_bwd(*args, need_w=False)[0], dH)
+    W = i["W"].clone().requires_grad_()
+    gp.grpo_logprobs(i["H"], W, i["y"], chunk).backward(i["g"])
+    assert torch.equal(W.grad, dW.to(W.dtype))
     i["g"].zero_()
     dH, dW = gp.grpo_logprobs_bwd(*args)
     assert not dH.any() and not dW.any()
+    W.grad = None
+    gp.grpo_logprobs(i["H"], W, i["y"], chunk).backward(i["g"])
+    assert not W.grad.any()
 
 
 @pytest.mark.parametrize("N,d,V", [(2050, 1024, 8300), (256, 256, 65500)])
@@ -161,6 +167,11 @@ def test_autograd():
         assert torch.equal(out, lp)
         out.backward(i["g"])
         assert torch.equal(H.grad, dH) and torch.equal(W.grad, dW.to(W.dtype))
+        # several chunks: the sum over them is rounded, not the parts
+        Wp = i["W"].clone().requires_grad_()
+        gp.grpo_logprobs(i["H"], Wp, i["y"], chunk=20, opts={"temperature": 0.9}).backward(i["g"])
+        parts = gp.grpo_logprobs_bwd(i["H"], i["W"], i["y"], lp, lse, i["g"], chunk=20, opts={"temperature": 0.9})[1]
+        assert torch.equal(Wp.grad, parts.to(W.dtype))
         # a frozen head, frozen hidden states, and a sum's broadcast gradient
         H = i["H"].clone().requires_grad_()
         gp.grpo_logprobs(H, i["W"], i["y"]).sum().backward()

@@ -26,7 +26,7 @@ def logprobs_fwd(**kw):
 
 
 def logprobs_bwd(**kw):
-    a = dict(H=FAKE, W=FAKE, y=FAKE, lp=FAKE, lse=FAKE, g=FAKE, N=8, d=16, V=32, dt=1, chunk=8, opts=None, acc=0,
+    a = dict(H=FAKE, W=FAKE, y=FAKE, lp=FAKE, lse=FAKE, g=FAKE, N=8, d=16, V=32, dt=1, chunk=8, opts=None, acc=0, dwt=0,
              dH=FAKE, dW=FAKE, ws=FAKE, wsb=1 << 30)
     a.update(kw)
     return L.grpo_logprobs_bwd(*a.values(), None)
@@ -43,7 +43,8 @@ def test_logprobs_forward_argument_errors(kw, code):
     assert L.grpo_last_error()
 
 
-@pytest.mark.parametrize("kw,code", SHAPES + [({"g": None}, -1), ({"dH": None, "dW": None}, -1), ({"acc": 2}, -1)])
+@pytest.mark.parametrize("kw,code", SHAPES + [({"g": None}, -1), ({"dH": None, "dW": None}, -1), ({"acc": 2}, -1), ({"dwt": 2}, -1),
+                                             ({"dwt": 1, "dt": 0}, -1), ({"dwt": 1, "acc": 1}, -1), ({"dwt": 1, "chunk": 7}, -1)])
 def test_logprobs_backward_argument_errors(kw, code):
     assert logprobs_bwd(**kw) == code
     assert L.grpo_last_error()
