@@ -25,7 +25,9 @@ namespace {
 
 constexpr int kLanes = 256;       // threads of a chunk
 constexpr int kChunk = 8192;      // elements: 8 loads of 16 bytes a thread in float32, 4 in bfloat16
-constexpr int kBlocks = 2048;     // 8 on each of 256 CUs
+constexpr int kClip = 2048;       // elements that a block clips: 332 us for 233M in float32, 340 and 357 of 4096 and 8192
+constexpr int64_t kMaxChunks = kMaxBlocks / (kChunk / kClip);
+constexpr int kBlocks = 2048;     // 8 on each of 256 CUs (4: 171 against 163 us for 233M in float32, 16: 162)
 constexpr int kAlone = 1024;      // threads of the one block that needs no second launch
 constexpr int kAloneChunks = 16;  // and the most chunks it takes
 
@@ -53,7 +55,9 @@ template <> struct Running<GRPO_GRAD_NORM_MAX> {
   static __device__ __forceinline__ double norm(type r) { return (double)__uint_as_float(r); }
 };
 
-// A chunk of n elements (FULL: kChunk of them): all loads first.
+// A chunk of n elements (FULL: kChunk of them): all loads first.  Non-temporal, since whole gradients
+// rarely stay in a cache until the optimizer reads them: 142 against 162 us for 233M in float32, 30
+// against 33 for 68M in bfloat16 (and clipped after it 83 against 84).
 template <int KIND, typename T, bool FULL>
 __device__ __forceinline__ void add_chunk(const T* p, int n, typename Running<KIND>::type& r) {
   constexpr int kSteps = kChunk / (kLanes * kVec<T>);
@@ -62,7 +66,7 @@ __device__ __forceinline__ void add_chunk(const T* p, int n, typename Running<KI
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
     const int e = (k * kLanes + lane) * kVec<T>;
-    v[k] = FULL ? *(const typename Vec16<T>::type*)(p + e) : load_vec(p, e, n);
+    v[k] = FULL ? __builtin_nontemporal_load((const typename Vec16<T>::type*)(p + e)) : load_vec(p, e, n);
   }
 #pragma unroll
   for (int k = 0; k < kSteps; ++k)
@@ -139,9 +143,10 @@ __global__ void __launch_bounds__(kAlone)
   if (threadIdx.x == 0) result(Running<KIND>::norm(r), max_norm, norm, scale);
 }
 
+// A block's part of a chunk, or what there is of it.
 template <typename T>
 __device__ __forceinline__ void clip_chunk(T* p, int n, float s) {
-  constexpr int kSteps = kChunk / (kLanes * kVec<T>);
+  constexpr int kSteps = kClip / (kLanes * kVec<T>);
   typename Vec16<T>::type v[kSteps];
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) v[k] = load_vec((const T*)p, (k * kLanes + (int)threadIdx.x) * kVec<T>, n);
@@ -158,11 +163,12 @@ __global__ void __launch_bounds__(kLanes)
                 int count, const float* __restrict__ scale) {
   const float s = *scale;
   if (s == 1.f) return;
-  const int64_t c = blockIdx.x;
+  const int64_t c = blockIdx.x / (kChunk / kClip);
   const int at = owner_of(first, count, c);
   const grpo_grad_tensor t = tensors[at];
-  const int64_t base = (c - first[at]) * kChunk;
-  const int n = (int)min<int64_t>(kChunk, t.n - base);
+  const int64_t base = (c - first[at]) * kChunk + (blockIdx.x % (kChunk / kClip)) * kClip;
+  const int n = (int)min<int64_t>(kClip, t.n - base);
+  if (n <= 0) return;
   if (t.dtype == GRPO_F32) clip_chunk((float*)t.grad + base, n, s);
   else clip_chunk((__bf16*)t.grad + base, n, s);
 }
@@ -194,8 +200,8 @@ int fill_plan(const grpo_grad_tensor* tensors, int64_t count, char* image) {
       return fail(GRPO_ERR_INVALID_ARG, "tensor %lld is not aligned to its elements", (long long)i);
     ranges.push_back({(uintptr_t)t.grad, (uintptr_t)t.grad + (size_t)t.n * es, true});
     hd.chunks += (t.n + kChunk - 1) / kChunk;
-    if (hd.chunks > kMaxBlocks)
-      return fail(GRPO_ERR_UNSUPPORTED, "more than 2^24 - 1 chunks of %d elements", kChunk);
+    if (hd.chunks > kMaxChunks)
+      return fail(GRPO_ERR_UNSUPPORTED, "more than 2^22 - 1 chunks of %d elements", kChunk);
   }
   if (any_overlap(ranges))
     return fail(GRPO_ERR_INVALID_ARG, "two of the tensors overlap (the same one twice?)");
@@ -304,7 +310,8 @@ int grpo_grad_clip(const void* image, const void* plan, const float* scale, void
   hipStream_t s = (hipStream_t)stream;
   grpo::ScopedKernelTimer timer(grpo::KK_GRAD_CLIP, s);
   const char* p = (const char*)plan;
-  grpo::k_grad_clip<<<(unsigned)hd.chunks, grpo::kLanes, 0, s>>>(
+  const unsigned blocks = (unsigned)hd.chunks * (grpo::kChunk / grpo::kClip);
+  grpo::k_grad_clip<<<blocks, grpo::kLanes, 0, s>>>(
       (const grpo_grad_tensor*)(p + hd.o_tensors), (const int64_t*)(p + hd.o_first), (int)hd.count, scale);
   GRPO_HIP(hipGetLastError());
   return GRPO_OK;

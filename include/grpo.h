@@ -452,7 +452,7 @@ int grpo_pref_loss_bwd(const uint8_t* mask, const float* weights, const float* g
  * grpo_grad_plan (host only) checks the tensors and writes the table into the HOST buffer `image`
  *   of grpo_grad_plan_bytes(count) bytes, to be copied to device memory once (8-byte aligned) and
  *   passed along with it, as in grpo_adamw_plan.  Types may be mixed; n = 0 is allowed; tensors that
- *   share memory are refused.  At most 2^24 tensors, and 2^24 - 1 chunks of 8192 elements.
+ *   share memory are refused.  At most 2^24 tensors, and 2^22 - 1 chunks of 8192 elements (3.4e10).
  * grpo_grad_norm: norm [1] and scale [1] float32, written.  Squares and sums are float64, in a fixed
  *   order: nothing overflows, and results are bitwise reproducible.  max_norm finite and >= 0.  workspace:
  *   grpo_grad_norm_workspace_bytes(), 256-byte aligned.

@@ -38,7 +38,7 @@ def norm(image, **kw):
     ([(0x10000, 0, F32), (0x10000, 8, F32), (0, 0, BF16)], 0),     # empty ones have no place
     ([(0, 8, F32)], -1), ([(0x10002, 8, F32)], -1), ([(0x10001, 8, BF16)], -1), ([(0x10002, 8, BF16)], 0),
     ([(0x10000, -1, F32)], -1), ([(0x10000, 8, 2)], -1), ([(0x10000, 0, 7)], -1), ([(0x10000, (1 << 48) + 1, F32)], -1),
-    ([(1 << 50, 8192 * ((1 << 24) - 1), F32)], 0), ([(1 << 50, 8192 * ((1 << 24) - 1) + 1, F32)], -3), ([], 0)])
+    ([(1 << 50, 8192 * ((1 << 22) - 1), F32)], 0), ([(1 << 50, 8192 * ((1 << 22) - 1) + 1, F32)], -3), ([], 0)])
 def test_plan(rows, code):
     assert image_of(rows)[0] == code
     assert (code == 0) == (L.grpo_last_error() == b"")
