@@ -126,8 +126,8 @@ def grpo_logprobs(H, W, y, chunk: int = 4096, opts=None):
     """The log-probabilities [N] float32 of y, differentiable (once) with respect to H and W:
     for any loss over them.  Arguments as for grpo_logprobs_fwd.  W's gradient is summed in
     float32 and returned in W's type (grpo_logprobs_bwd with a float32 dW accumulator keeps it
-    in float32); tokens whose gradient is 0 cost nothing.  The backward raises while its stream is
-    captured into a graph, as grpo_norm's does."""
+    in float32); tokens whose gradient is 0 have no part in it, whatever their hidden states
+    hold.  The backward raises while its stream is captured into a graph, as grpo_norm's does."""
     return _GrpoLogprobs.apply(H, W, y, chunk, opts)
 
 

@@ -238,7 +238,8 @@ bool small_tiles_bwd(int64_t N, int64_t d, int64_t V, int dtype) {
   const double products = (double)N * (double)V * (double)d;
   // (and a dZ of at most 1 GiB, so that one chunk takes all tokens whenever the caller's does)
   if (dtype == GRPO_BF16)
-    return products <= (N <= 128 ? 8589934592.0 : 4294967296.0) && (double)N * (double)V <= 536870912.0;
+    return products <= (N <= 128 ? 8589934592.0 : 4294967296.0) &&
+           (double)N * (double)round_up(V, 64) <= 536870912.0;
   const int64_t dt = (d + 255) / 256;
   return dt * ((N + 255) / 256) < 32 || dt * ((V + 255) / 256) < 128 || products < 1.6e10;
 }
@@ -466,6 +467,7 @@ int logprobs_bwd64(const T* H, const T* W, const int32_t* y, const float* lp, co
                    const grpo::LogitXform& xf, int accumulate, int dw_bf16, T* dH, void* dW,
                    char* ws, hipStream_t s) {
   const Plan64 p = plan64_bwd(N, d, V, (int64_t)sizeof(T), chunk);
+  if (dw_bf16 && p.C < N) return fail(GRPO_ERR_UNSUPPORTED, "a bfloat16 dW of more than one chunk");
   for (int64_t c0 = 0; c0 < N; c0 += p.C) {
     const int C = (int)std::min(p.C, N - c0);
     // of lse's two parts bfloat16 has the first
