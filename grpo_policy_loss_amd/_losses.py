@@ -43,21 +43,28 @@ def _head_bytes(op, N, d, V, dt, chunk):
     return need
 
 
-def _logprobs_fwd(H, W, y, chunk, workspace, opts, sizes, on):
-    """The call itself, of tensors that were checked: (lp, lse, chunk)."""
-    N, d, V, dt = sizes
-    ctx, stream = on
+def _logprobs_saved_fwd(H, W, y, chunk, opts):
+    """The forward for autograd: (lp, lse, (chunk, opts, sizes)).  A small workspace lies behind
+    lse in one tensor, since each allocation costs a small call some 4 us in all."""
+    sizes = N, d, V, dt = _head(H, W, y)
+    ctx, stream = _on(H, W, y)
     dev = H.device
     with ctx:
         if chunk == 0:
             chunk = auto_chunk(1, N, d, V, dt)
-        ws = _workspace(_head_bytes(GRPO_OP_LOGPROBS_FWD, N, d, V, dt, chunk), dev, workspace)
+        need = _head_bytes(GRPO_OP_LOGPROBS_FWD, N, d, V, dt, chunk)
+        at = -(-4 * _lse_size(N, dt) // 256) * 256
         lp = torch.empty(N, dtype=torch.float32, device=dev)
-        lse = torch.empty(_lse_size(N, dt), dtype=torch.float32, device=dev)
+        lse = torch.empty((at + (need if need <= 1 << 20 else 0)) // 4, dtype=torch.float32, device=dev)
+        if need <= 1 << 20:
+            ws = lse.data_ptr() + at
+        else:
+            apart = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws = apart.data_ptr()
         _check("grpo_logprobs_fwd", lib().grpo_logprobs_fwd(
             H.data_ptr(), W.data_ptr(), y.data_ptr(), N, d, V, dt, chunk, opts, lp.data_ptr(),
-            lse.data_ptr(), ws.data_ptr(), ws.numel(), stream))
-    return lp, lse, chunk
+            lse.data_ptr(), ws, need, stream))
+    return lp, lse, (chunk, opts, sizes)
 
 
 def _logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk, dW, dH, workspace, opts, need_h, need_w, sizes, on,
@@ -76,15 +83,17 @@ def _logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk, dW, dH, workspace, opts, nee
             dH = None
         elif dH is None:
             dH = torch.empty(N, d, dtype=H.dtype, device=dev)
+        dw_type = GRPO_F32
         if not need_w:
             dW = None
         elif dW is None:
-            dW = torch.empty(V, d, dtype=W.dtype if like_w and N <= chunk else torch.float32, device=dev)
+            like_w = like_w and N <= chunk
+            dW = torch.empty(V, d, dtype=W.dtype if like_w else torch.float32, device=dev)
+            dw_type = dt if like_w else GRPO_F32
         _check("grpo_logprobs_bwd", lib().grpo_logprobs_bwd(
             H.data_ptr(), W.data_ptr(), y.data_ptr(), lp.data_ptr(), lse.data_ptr(),
-            grad_lp.data_ptr(), N, d, V, dt, chunk, opts, accumulate,
-            GRPO_F32 if dW is None else _dt(dW), _ptr(dH), _ptr(dW), ws.data_ptr(), ws.numel(),
-            stream))
+            grad_lp.data_ptr(), N, d, V, dt, chunk, opts, accumulate, dw_type, _ptr(dH), _ptr(dW),
+            ws.data_ptr(), ws.numel(), stream))
     return dH, dW
 
 
@@ -93,9 +102,18 @@ def grpo_logprobs_fwd(H, W, y, chunk: int = 4096, workspace=None, opts=None):
     (float32 or bfloat16) and W [V, d], and the log-sum-exp that the backward takes ([N]; for
     float32 [2 N], its rounding behind it).  `opts` and chunk as for grpo_loss_fwd; of the
     options the logit transform counts."""
-    sizes = _head(H, W, y)
-    on = _on(*(t for t in (H, W, y, workspace) if t is not None))
-    return _logprobs_fwd(H, W, y, chunk, workspace, _opts(opts), sizes, on)[:2]
+    N, d, V, dt = _head(H, W, y)
+    ctx, stream = _on(*(t for t in (H, W, y, workspace) if t is not None))
+    with ctx:
+        if chunk == 0:
+            chunk = auto_chunk(1, N, d, V, dt)
+        ws = _workspace(_head_bytes(GRPO_OP_LOGPROBS_FWD, N, d, V, dt, chunk), H.device, workspace)
+        lp = torch.empty(N, dtype=torch.float32, device=H.device)
+        lse = torch.empty(_lse_size(N, dt), dtype=torch.float32, device=H.device)
+        _check("grpo_logprobs_fwd", lib().grpo_logprobs_fwd(
+            _ptr(H), _ptr(W), _ptr(y), N, d, V, dt, chunk, _opts(opts), _ptr(lp), _ptr(lse), _ptr(ws),
+            ws.numel(), stream))
+    return lp, lse
 
 
 def grpo_logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk: int = 4096, dW=None, dH=None,

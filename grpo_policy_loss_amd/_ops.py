@@ -33,7 +33,7 @@ def _on(*ts, strided=()):
     for t in strided:
         if t.get_device() != at:
             _refuse(ts + strided, ts)
-    ctx = _HERE if at == torch.cuda.current_device() else torch.cuda.device(at)
+    ctx = _HERE if at == torch._C._cuda_getDevice() else torch.cuda.device(at)
     return ctx, torch._C._cuda_getCurrentRawStream(at)
 
 

@@ -13,7 +13,7 @@ from __future__ import annotations
 import torch
 
 from ._lib import AGG_TOKEN_MEAN, KL_REVERSE, _opts, grpo_loss_bwd, grpo_loss_fwd
-from ._losses import (PREF_SIGMOID, RATIO_TOKEN, _head, _logprobs_bwd, _logprobs_fwd,
+from ._losses import (PREF_SIGMOID, RATIO_TOKEN, _logprobs_bwd, _logprobs_saved_fwd,
                       grpo_clip_loss_bwd, grpo_clip_loss_fwd, grpo_pref_loss_bwd,
                       grpo_pref_loss_fwd)
 from ._ops import NORM_LAYER, NORM_RMS, _on, grpo_norm_bwd, grpo_norm_fwd
@@ -103,10 +103,8 @@ def grpo_norm(X, weight, bias=None, eps: float = 1e-5, kind: int = NORM_RMS):
 class _GrpoLogprobs(torch.autograd.Function):
     @staticmethod
     def forward(ctx, H, W, y, chunk, opts):
-        sizes, opts = _head(H, W, y), _opts(opts)
-        lp, lse, chunk = _logprobs_fwd(H, W, y, chunk, None, opts, sizes, _on(H, W, y))
+        lp, lse, ctx.args = _logprobs_saved_fwd(H, W, y, chunk, _opts(opts))
         ctx.save_for_backward(H, W, y, lp, lse)
-        ctx.args = chunk, opts, sizes
         return lp
 
     @staticmethod
@@ -118,7 +116,7 @@ class _GrpoLogprobs(torch.autograd.Function):
         need_h, need_w = ctx.needs_input_grad[:2]
         grad_lp = grad_lp.contiguous()       # it may be a broadcast view (that of a sum is)
         dH, dW = _logprobs_bwd(H, W, y, lp, lse, grad_lp, chunk, None, None, None, opts, need_h, need_w,
-                               sizes, _on(H, W, y, grad_lp), like_w=True)
+                               sizes, _on(H, grad_lp), like_w=True)
         return dH, dW if dW is None or dW.dtype == W.dtype else dW.to(W.dtype), None, None, None
 
 
