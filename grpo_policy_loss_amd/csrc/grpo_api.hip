@@ -246,8 +246,9 @@ bool small_tiles_bwd(int64_t N, int64_t d, int64_t V, int dtype) {
 
 Plan64 plan64_fwd(int64_t N, int64_t V, int64_t chunk) {
   Plan64 p{};
-  p.C = std::min(std::min(chunk, N), std::max<int64_t>(64, kSlabBytesDefault / ((V + 63) / 64 * 4) / 64 * 64));
-  const size_t parts = (size_t)((V + 63) / 64 * p.C) * 4;
+  const int64_t tiles = (V + 31) / 32;   // the last chunk may have the smaller tiles
+  p.C = std::min(std::min(chunk, N), std::max<int64_t>(64, kSlabBytesDefault / (tiles * 4) / 64 * 64));
+  const size_t parts = (size_t)(tiles * p.C) * 4;
   Carve c;
   c.take(parts);
   p.o_ps = c.take(parts);
@@ -749,9 +750,9 @@ int grpo_logprobs_fwd(const void* H, const void* W, const int32_t* y, int64_t N,
     const Plan64 p = plan64_fwd(N, V, chunk);
     float *pm = (float*)ws, *ps = (float*)(ws + p.o_ps), *zy = (float*)(ws + p.o_zy);
     for (int64_t c0 = 0; c0 < N; c0 += p.C) {
-      const int C = (int)std::min(p.C, N - c0);
+      const int C = (int)std::min(p.C, N - c0), rows = grpo::tile_rows(V, C);
       GRPO_HIP(grpo::launch64_lse(Wf, Hf + c0 * d, y + c0, V, d, C, xf, pm, ps, zy, s));
-      GRPO_HIP(grpo::launch64_merge(pm, ps, zy, y + c0, V, (int)((V + 63) / 64), C, C, lp + c0,
+      GRPO_HIP(grpo::launch64_merge(pm, ps, zy, y + c0, V, (int)((V + rows - 1) / rows), C, C, lp + c0,
                                     lse + c0, lse + N + c0, s));
     }
     return GRPO_OK;

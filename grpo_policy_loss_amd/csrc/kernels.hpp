@@ -140,13 +140,15 @@ hipError_t launch_dh_scatter(const float* dH_acc, int nsplit, int cpad, int64_t 
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t s);
 
 // The 64 x 64 tiles of tile64.hip (float32; the gradients in bfloat16 too).
-// launch64_lse: partials of ceil(V / 64) vocabulary tiles in part_m and part_s [tiles][C] and the
-// target logits in zy [C].
+// tile_rows: their rows and columns, 64 or 32, for an output of rows x cols.
+// launch64_lse: partials of ceil(V / tile_rows(V, C)) vocabulary tiles in part_m and part_s [tiles][C]
+// and the target logits in zy [C].
 // launch64_merge: lp, lse and what float32 leaves of it (rest) from such partials, or those of
 // launch_lse_partials (stride: cpad).
 // launch64_dz: dZ [C][vpad], vpad = V rounded up to 64, its columns from V on 0.  rest may be null.
 // launch64_grads: dH [C, d] and dW [V, d] (float32, or with dw_bf16 and accumulate 0 bfloat16), either
 // null; with more than one share of the vocabulary, parts holds shares x C x d floats.
+int tile_rows(int64_t rows, int64_t cols);
 hipError_t launch64_lse(const float* W, const float* H, const int32_t* y, int64_t V, int64_t d, int C,
                         const LogitXform& xf, float* part_m, float* part_s, float* zy,
                         hipStream_t s);
