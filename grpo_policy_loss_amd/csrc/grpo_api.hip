@@ -261,9 +261,12 @@ Plan64 plan64_bwd(int64_t N, int64_t d, int64_t V, int64_t es, int64_t chunk) {
   Plan64 p{};
   p.vpad = round_up(V, 64);
   p.C = std::min(std::min(chunk, N), std::max<int64_t>(64, kSlabBytesDefault / (p.vpad * es) / 64 * 64));
-  // shares of the vocabulary for dH, until it has some 1024 tiles or 4 steps a share
-  const int64_t tiles = (d + 63) / 64 * ((p.C + 63) / 64);
-  p.shares = std::max<int64_t>(1, std::min<int64_t>((4 * kCUs + tiles - 1) / tiles, p.vpad / 256));
+  // shares of the vocabulary for dH, until it has some 1024 tiles, or 8 steps of 64 a share, or 16 of
+  // a larger vocabulary.  us of the backward with 4 | 8 | 16 steps, 16 tokens: d 256, V 8000
+  // float32 26 | 30 | 41, d 1024, V 2000 26 | 31 | 42, d 256, V 32000 81 | 60 | 54, bfloat16 57 | 39 | 33;
+  // 300 tokens, d 64, V 32000 bfloat16 71 | 54 | 47.  A small call with one share is one launch less.
+  const int64_t tiles = (d + 63) / 64 * ((p.C + 63) / 64), least = p.vpad >= 16384 ? 1024 : 512;
+  p.shares = std::max<int64_t>(1, std::min<int64_t>((4 * kCUs + tiles - 1) / tiles, p.vpad / least));
   const int64_t per = (p.vpad / 64 + p.shares - 1) / p.shares;   // tiles of a share: none is empty
   p.shares = (p.vpad / 64 + per - 1) / per;
   Carve c;
