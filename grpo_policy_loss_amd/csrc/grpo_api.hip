@@ -200,48 +200,51 @@ BwdPlan plan_bwd(int64_t N, int64_t d, int64_t V, int dtype, int64_t chunk, int6
 // of one chunk.  Backward: the dZ of one chunk, of at most kSlabBytesDefault, and dH's shares.
 struct Plan64 {
   int64_t C, vpad, shares;
-  size_t o_ps, o_zy, o_parts, total;
+  size_t o_ps, o_zy, o_parts, o_wparts, total;
 };
 
-// Whether the log-probabilities' forward takes 64 x 64 tiles rather than 256 x 256 ones.  bfloat16:
-// never (its lp is bitwise the loss's).  float32: unless the large tiles' waves of one workgroup per
-// CU are at least 3/4 full and a row has 256 elements.  us, small against large tiles:
+// Whether the log-probabilities' forward takes the small tiles rather than 256 x 256 ones.  bfloat16:
+// never (its lp is bitwise the loss's).  float32: unless the large tiles fill 0.6 of the CUs they take
+// in turn.  us, small against large tiles:
 //   d     V       N = 256     512         2048        8192
-//   64    32000   55   97     78   146    209   414   734   1537
-//   256   32000   86   88     137  89     438   304   1631  1140
-//   1024  8000    60   273    102  269    352   281   1331  1054
-//   1024  1000    37   267    37   269    55    274   182   272
+//   64    32000   34    34    50    35    146   108   504   380
+//   256   32000   60    85    101   88    336   309   1265  1126
+//   1024  1000    18    264   22    265   51    272   152   279
+//   1024  8000    53    269   84    273   288   281   1079  1041
+//   4096  8000    165   1031  285   1040  1071  1021
 bool small_tiles_fwd(int64_t N, int64_t d, int64_t V, int dtype) {
   if (dtype != GRPO_F32) return false;
-  const int64_t waves = ((N + 255) / 256 * ((V + 255) / 256) + kCUs - 1) / kCUs;
-  return d < 256 || (double)N * (double)V < 0.73 * 65536.0 * (double)(waves * kCUs);
+  const int64_t turns = ((N + 255) / 256 * ((V + 255) / 256) + kCUs - 1) / kCUs;
+  return (double)N * (double)V < 0.6 * 65536.0 * (double)(turns * kCUs);
 }
 
-// The same for the backward.  bfloat16: where the products are few, twice as many where tokens fill
-// no more than half a large tile.  us, small against large tiles (70 % of the tokens have a gradient;
-// only the large tiles pass by the others):
-//   d     V       N = 16        128          512          2048
-//   64    1000    28    50      29    52     29    58     44    79
-//   256   32000   62    133     76    138    120   150    384   203
-//   1024  8000    41    93      49    98     108   110    336   134
-//   1024  128000  316   547     439   564    1354  647    4984  1061
-//   4096  1000    45    124     52    129    78    142    187   197
-//   4096  32000   311   342     432   363    1287  412    4885  1003
+// The same for the backward.  bfloat16: where the products are few, twice as many where tokens fill no
+// more than one large tile.  us, small against large tiles (70 % of the tokens have a gradient; only the
+// large tiles pass by the others):
+//   d     V       N = 16      256         1024        2048
+//   64    1000    13    43    14    46    17    58    20    72
+//   64    128000  58    339   115   352   317   419   592   522
+//   256   32000   35    126   68    136   186   168   339   203
+//   1024  8000    31    85    61    98    171   114   306   135
+//   1024  128000  330   546   656   574
+//   4096  1000    30    117   44    126   95    151   171   195
+//   4096  8000    68    154   175   175   578   245   1136  326
 // float32: unless there is enough of everything for the large ones: for dH's at most 8 shares, for dW's
-// tiles and in all.
-//   256   32000   92    1118    124   1134   307   1213   1110  1696   (N = 8192: 4306  3673)
-//   1024  8000    75    571     100   591    283   668    1039  936
-//   1024  32000   178   1328    301   1369   1058  1522   4049  2591
-//   4096  1000    124   1081    139   1103   208   1174   527   1565
-//   4096  8000    222   1313    307   1352   1041  1501   3958  2774
+// tiles and in all, and a row is not less than a tile.
+//   d     V       N = 256     1024        4096        8192
+//   64    128000  186   4041  634   4658  2312  6674  4608  12190
+//   256   32000   145   1165  473   1418  1795  2359  3572  3652
+//   1024  8000    137   621   451   754   1708  1836  3384  3327
+//   1024  32000   461   1442  1711  1959  6713  5103
+//   4096  4000    253   1204  863   1499  3369  2791  6693  5468
 bool small_tiles_bwd(int64_t N, int64_t d, int64_t V, int dtype) {
   const double products = (double)N * (double)V * (double)d;
   // (and a dZ of at most 1 GiB, so that one chunk takes all tokens whenever the caller's does)
   if (dtype == GRPO_BF16)
-    return products <= (N <= 128 ? 8589934592.0 : 4294967296.0) &&
+    return products <= (N <= 256 ? 8589934592.0 : 4294967296.0) &&
            (double)N * (double)round_up(V, 64) <= 536870912.0;
   const int64_t dt = (d + 255) / 256;
-  return dt * ((N + 255) / 256) < 32 || dt * ((V + 255) / 256) < 128 || products < 1.6e10;
+  return d < 256 || dt * ((N + 255) / 256) < 32 || dt * ((V + 255) / 256) < 256 || products < 5e10;
 }
 
 Plan64 plan64_fwd(int64_t N, int64_t V, int64_t chunk) {
@@ -272,6 +275,8 @@ Plan64 plan64_bwd(int64_t N, int64_t d, int64_t V, int64_t es, int64_t chunk) {
   Carve c;
   c.take((size_t)(p.C * p.vpad * es));
   p.o_parts = p.shares > 1 ? c.take((size_t)(p.shares * p.C * d) * 4) : 0;
+  const int64_t of_dw = grpo::dw_shares(V, d, p.C);
+  p.o_wparts = of_dw > 1 ? c.take((size_t)(of_dw * V * d) * 4) : 0;
   p.total = c.off;
   return p;
 }
@@ -480,7 +485,8 @@ int logprobs_bwd64(const T* H, const T* W, const int32_t* y, const float* lp, co
                                   C, p.vpad, xf, (T*)ws, s));
     GRPO_HIP(grpo::launch64_grads<T>(W, H + c0 * d, (const T*)ws, grad_lp + c0, V, d, C, p.vpad,
                                      (int)p.shares, dH == nullptr ? nullptr : dH + c0 * d,
-                                     (float*)(ws + p.o_parts), accumulate || c0 > 0, dw_bf16, dW, s));
+                                     (float*)(ws + p.o_parts), (float*)(ws + p.o_wparts),
+                                     accumulate || c0 > 0, dw_bf16, dW, s));
   }
   return GRPO_OK;
 }

@@ -147,7 +147,9 @@ hipError_t launch_zero(void* p, size_t bytes, hipStream_t s);
 // launch_lse_partials (stride: cpad).
 // launch64_dz: dZ [C][vpad], vpad = V rounded up to 64, its columns from V on 0.  rest may be null.
 // launch64_grads: dH [C, d] and dW [V, d] (float32, or with dw_bf16 and accumulate 0 bfloat16), either
-// null; with more than one share of the vocabulary, parts holds shares x C x d floats.
+// null; with more than one share of the vocabulary, parts holds shares x C x d floats, and with
+// dw_shares(V, d, C) above 1, w_parts as many times V x d.
+int64_t dw_shares(int64_t V, int64_t d, int64_t C);
 int tile_rows(int64_t rows, int64_t cols);
 hipError_t launch64_lse(const float* W, const float* H, const int32_t* y, int64_t V, int64_t d, int C,
                         const LogitXform& xf, float* part_m, float* part_s, float* zy,
@@ -162,7 +164,7 @@ hipError_t launch64_dz(const T* W, const T* H, const int32_t* y, const float* lp
 template <typename T>
 hipError_t launch64_grads(const T* W, const T* H, const T* dZ, const float* grad_lp, int64_t V,
                           int64_t d, int C, int64_t vpad, int shares, T* dH, float* parts,
-                          int accumulate, int dw_bf16, void* dW, hipStream_t s);
+                          float* w_parts, int accumulate, int dw_bf16, void* dW, hipStream_t s);
 
 // Plain tile GEMM C[m][n] = sum_k A[m][k] B[n][k] into float32 C (diagnostic).
 template <typename T>

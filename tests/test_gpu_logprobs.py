@@ -43,7 +43,8 @@ def test_sizes(t, N, d, V, chunk):
 
 
 @pytest.mark.parametrize("t,N,d,V,chunk", [("bf16", 700, 512, 12100, 256), ("bf16", 700, 512, 12100, 4096), ("f32", 2050, 1024, 8300, 4096),
-                                           ("f32", 2050, 1024, 8300, 900), ("f32", 256, 256, 65500, 4096)])
+                                           ("f32", 2050, 1024, 8300, 900), ("f32", 256, 256, 65500, 4096),
+                                           ("f32", 2050, 1024, 24600, 4096), ("f32", 2050, 1024, 24600, 900)])
 def test_sizes_of_the_large_tiles(t, N, d, V, chunk):
     i = inputs(N, d, V, t, seed=N)
     lp, lse, dH, dW = check(i, t, chunk)
@@ -64,7 +65,25 @@ def test_sizes_of_the_large_tiles(t, N, d, V, chunk):
     assert not W.grad.any()
 
 
-@pytest.mark.parametrize("N,d,V", [(2050, 1024, 8300), (256, 256, 65500)])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("N,d,V,chunk", [(1100, 8, 2, 4096), (1024, 8, 1, 4096), (2100, 64, 130, 4096), (3001, 72, 1003, 1500), (4200, 328, 70, 8192),
+                                         (1601, 256, 1100, 8192), (9001, 40, 5, 8192)])
+def test_many_tokens_of_a_small_head(t, N, d, V, chunk):
+    """dW's sums are split over the tokens."""
+    i = inputs(N, d, V, t, seed=N)
+    lp, lse, dH, dW = check(i, t, chunk)
+    args = (i["H"], i["W"], i["y"], lp, lse, i["g"], chunk)
+    assert torch.equal(gp.grpo_logprobs_bwd(*args, need_h=False)[1], dW)
+    assert torch.equal(gp.grpo_logprobs_bwd(*args, need_w=False)[0], dH)
+    into = torch.full_like(dW, 0.5)
+    gp.grpo_logprobs_bwd(*args, dW=into)
+    assert ((into - 0.5 - dW).abs() <= 8 * plain_update.U * (1 + dW.abs())).all()
+    W = i["W"].clone().requires_grad_()
+    gp.grpo_logprobs(i["H"], W, i["y"], chunk).backward(i["g"])
+    assert torch.equal(W.grad, dW.to(W.dtype))
+
+
+@pytest.mark.parametrize("N,d,V", [(2050, 1024, 8300), (256, 256, 65500), (2050, 1024, 24600)])
 def test_large_tiles_with_a_cap(N, d, V):
     i = inputs(N, d, V, "f32", seed=1)
     check(i, "f32", 4096, {"logit_softcapping": 3.0, "temperature": 0.8}, 1 / 0.8, 3.0)

@@ -110,7 +110,8 @@ def test_pref_backward_argument_errors(at, value, code):
 
 
 def test_head_workspaces():
-    """No tokens x vocabulary beyond a slab of 1.25 GiB, or of 64 tokens; fp8 and bad shapes have none."""
+    """The loss's forward's, or no tokens x vocabulary beyond a slab of 1.25 GiB, or of 64 tokens; fp8 and bad shapes have
+    none."""
     for op in (4, 5):
         assert L.grpo_workspace_bytes(op, 64, 64, 500, 2, 64) == 0 == L.grpo_workspace_bytes(op, 0, 64, 500, 1, 64)
         assert L.grpo_workspace_bytes(op, 64, 62, 500, 0, 64) == 0
@@ -119,7 +120,7 @@ def test_head_workspaces():
                                (1 << 24, 64, 100000, 1 << 20)):
             fwd, bwd = (L.grpo_workspace_bytes(op, n, w, v, dt, chunk) for op in (4, 5))
             c = min(n, chunk)
-            assert fwd == L.grpo_workspace_bytes(1, n, w, v, 1, chunk) if dt else 0 < fwd <= 3 << 30
+            assert fwd == L.grpo_workspace_bytes(1, n, w, v, dt, chunk) or dt == 0 and 0 < fwd <= 3 << 30
             assert 0 < bwd <= (5 << 28) + 256 * 4 * v + 64 * c * w + 16 * n + (64 << 20) + 4 * 1024 * 64 * 64 * 8, (n, w, v, dt, bwd)
 
 
