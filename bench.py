@@ -48,7 +48,7 @@ PROFILES = os.path.join(ROOT, "profiles")
 COPY_BYTES = 1 << 30      # calibration copy for the HBM byte counters
 
 
-LOSS_SOURCES = ("api.hpp", "grpo_api.hip", "kernels.hip", "kernels.hpp", "tile_mma.hpp",
+LOSS_SOURCES = ("api.hpp", "grpo_api.hip", "kernels.hip", "kernels.hpp", "raster.hpp", "tile_mma.hpp",
                 "timing.hip", "timing.hpp")
 
 

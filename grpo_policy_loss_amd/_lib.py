@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgrpo.so"
 
 GRPO_F32, GRPO_BF16, GRPO_FP8_E4M3 = 0, 1, 2
 GRPO_OP_REF, GRPO_OP_FWD, GRPO_OP_BWD, GRPO_OP_BWD_MIN = 0, 1, 2, 3
-GRPO_OP_LOGPROBS_FWD, GRPO_OP_LOGPROBS_BWD = 4, 5
+GRPO_OP_LOGPROBS_FWD, GRPO_OP_LOGPROBS_BWD = 16, 17
 STATUS = {0: "GRPO_OK", -1: "GRPO_ERR_INVALID_ARG", -2: "GRPO_ERR_WORKSPACE",
           -3: "GRPO_ERR_UNSUPPORTED", -4: "GRPO_ERR_HIP"}
 

@@ -797,13 +797,13 @@ int grpo_clip_loss_bwd(const float* lp, const float* old_lp, const float* ref_lp
   grpo::ClipArgs a;
   const int st = grpo::clip_args(lp, old_lp, ref_lp, mask, adv, weights, B, L, opts, &a);
   if (st != GRPO_OK) return st;
+  for (const float* in : {lp, old_lp, ref_lp, adv})
+    if (in == grad_lp) return fail(GRPO_ERR_INVALID_ARG, "grad_lp is one of the inputs");
   hipStream_t s = (hipStream_t)stream;
   grpo::ScopedKernelTimer timer(grpo::KK_CLIP_BWD, s);
   const int64_t N = B * L;
   const unsigned blocks = (unsigned)((N + grpo::kThreads * 4 - 1) / (grpo::kThreads * 4));
   const grpo::Divide by = grpo::divider(L);
-  for (const float* in : {lp, old_lp, ref_lp, adv})
-    if (in == grad_lp) return fail(GRPO_ERR_INVALID_ARG, "grad_lp is one of the inputs");
   if (a.beta == 0.0) a.ref_lp = nullptr;
   if (opts != nullptr && opts->ratio == GRPO_RATIO_SEQUENCE)
     grpo::k_clip_bwd<true><<<blocks, grpo::kThreads, 0, s>>>(a, by, N, grad_loss, grad_lp);

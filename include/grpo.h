@@ -69,8 +69,8 @@ typedef enum {
   GRPO_OP_FWD = 1,     /* grpo_loss_fwd */
   GRPO_OP_BWD = 2,     /* grpo_loss_bwd, default (fastest) dZ slab */
   GRPO_OP_BWD_MIN = 3, /* grpo_loss_bwd, the least workspace it accepts */
-  GRPO_OP_LOGPROBS_FWD = 4, /* grpo_logprobs_fwd */
-  GRPO_OP_LOGPROBS_BWD = 5  /* grpo_logprobs_bwd */
+  GRPO_OP_LOGPROBS_FWD = 16, /* grpo_logprobs_fwd */
+  GRPO_OP_LOGPROBS_BWD = 17  /* grpo_logprobs_bwd */
 } grpo_op;
 
 /*

@@ -112,13 +112,13 @@ def test_pref_backward_argument_errors(at, value, code):
 def test_head_workspaces():
     """The loss's forward's, or no tokens x vocabulary beyond a slab of 1.25 GiB, or of 64 tokens; fp8 and bad shapes have
     none."""
-    for op in (4, 5):
+    for op in (16, 17):
         assert L.grpo_workspace_bytes(op, 64, 64, 500, 2, 64) == 0 == L.grpo_workspace_bytes(op, 0, 64, 500, 1, 64)
         assert L.grpo_workspace_bytes(op, 64, 62, 500, 0, 64) == 0
     for dt in (0, 1):
         for n, w, v, chunk in ((1, 64, 2, 1), (64, 1536, 151936, 4096), (4096, 1536, 151936, 4096), (163840, 4096, 128256, 8192), (8192, 64, 100, 8192),
                                (1 << 24, 64, 100000, 1 << 20)):
-            fwd, bwd = (L.grpo_workspace_bytes(op, n, w, v, dt, chunk) for op in (4, 5))
+            fwd, bwd = (L.grpo_workspace_bytes(op, n, w, v, dt, chunk) for op in (16, 17))
             c = min(n, chunk)
             assert fwd == L.grpo_workspace_bytes(1, n, w, v, dt, chunk) or dt == 0 and 0 < fwd <= 3 << 30
             assert 0 < bwd <= (5 << 28) + 256 * 4 * v + 64 * c * w + 16 * n + (64 << 20) + 4 * 1024 * 64 * 64 * 8, (n, w, v, dt, bwd)
