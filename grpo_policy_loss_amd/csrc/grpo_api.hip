@@ -730,6 +730,21 @@ int grpo_loss_bwd(const void* H, const void* W, const int32_t* y, const uint8_t*
 }
 
 // ---------------------------------------------------------------- log-probabilities with a gradient
+namespace {
+// Rows are read, some of them straight into LDS, 16 bytes at a time, and the workspace is carved up.
+int check_aligned(const void* H, const void* W, const void* dH, const void* dW, const void* ws) {
+  for (const void* p : {H, W, dH, dW})
+    if ((uintptr_t)p % 16 != 0) return fail(GRPO_ERR_INVALID_ARG, "H, W, dH and dW must be 16-byte aligned");
+  if ((uintptr_t)ws % 256 != 0) return fail(GRPO_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+  return GRPO_OK;
+}
+
+// The gradients are written while the inputs are still read.
+bool overlaps(const void* a, size_t n, const void* b, size_t m) {
+  return a != nullptr && b != nullptr && (uintptr_t)a < (uintptr_t)b + m && (uintptr_t)b < (uintptr_t)a + n;
+}
+}  // namespace
+
 int grpo_logprobs_fwd(const void* H, const void* W, const int32_t* y, int64_t N, int64_t d,
                       int64_t V, int dtype, int64_t chunk, const grpo_opts* opts, float* lp,
                       float* lse, void* workspace, size_t workspace_bytes, void* stream) {
@@ -743,7 +758,8 @@ int grpo_logprobs_fwd(const void* H, const void* W, const int32_t* y, int64_t N,
   GRPO_CHECK_PTR(y);
   GRPO_CHECK_PTR(lp);
   GRPO_CHECK_PTR(lse);
-  const int st = check_shape(N, d, V, dtype, chunk);
+  int st = check_shape(N, d, V, dtype, chunk);
+  if (st == GRPO_OK) st = check_aligned(H, W, nullptr, nullptr, workspace);
   if (st != GRPO_OK) return st;
   const size_t need = grpo_workspace_bytes(GRPO_OP_LOGPROBS_FWD, N, d, V, dtype, chunk);
   if (workspace == nullptr || workspace_bytes < need)
@@ -797,11 +813,17 @@ int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const floa
   if (dH == nullptr && dW == nullptr) return fail(GRPO_ERR_INVALID_ARG, "null pointer: both dH and dW");
   if (accumulate != 0 && accumulate != 1)
     return fail(GRPO_ERR_INVALID_ARG, "accumulate %d is not 0 or 1", accumulate);
-  const int st = check_shape(N, d, V, dtype, chunk);
+  int st = check_shape(N, d, V, dtype, chunk);
+  if (st == GRPO_OK) st = check_aligned(H, W, dH, dW, workspace);
   if (st != GRPO_OK) return st;
   const bool bf16_dw = dw_dtype == GRPO_BF16;
   if (dw_dtype != GRPO_F32 && !(bf16_dw && dtype == GRPO_BF16))
     return fail(GRPO_ERR_INVALID_ARG, "dw_dtype %d is neither GRPO_F32 nor the head's type", dw_dtype);
+  const size_t es = esize(dtype), h_bytes = (size_t)(N * d) * es, w_bytes = (size_t)(V * d) * es;
+  const size_t dw_bytes = (size_t)(V * d) * (bf16_dw ? 2 : 4);
+  if (overlaps(dH, h_bytes, H, h_bytes) || overlaps(dH, h_bytes, W, w_bytes) || overlaps(dW, dw_bytes, H, h_bytes) ||
+      overlaps(dW, dw_bytes, W, w_bytes) || overlaps(dH, h_bytes, dW, dw_bytes))
+    return fail(GRPO_ERR_INVALID_ARG, "dH or dW overlaps H, W or the other");
   if (bf16_dw && (accumulate || chunk < N))
     return fail(GRPO_ERR_INVALID_ARG, "a bfloat16 dW is written from one chunk: accumulate 0, chunk >= N");
   hipStream_t s = (hipStream_t)stream;

@@ -19,6 +19,7 @@ static int g_fail = 0;
     }                                                                          \
   } while (0)
 
+static void* const FAKE2 = (void*)0x100000;
 static void* const FAKE = (void*)0x1000;   // never dereferenced
 
 static void workspaces() {
@@ -90,8 +91,10 @@ static void rejected_calls() {
   CHECK(grpo_pref_loss_bwd(&m, &f, nullptr, INT64_MAX, 1, &f, nullptr) == GRPO_ERR_UNSUPPORTED);
   CHECK(grpo_logprobs_fwd(FAKE, FAKE, &y, INT64_MAX, 16, 32, GRPO_BF16, 8, nullptr, &f, &f, FAKE, 1 << 20, nullptr) ==
         GRPO_ERR_UNSUPPORTED);
-  CHECK(grpo_logprobs_bwd(FAKE, FAKE, &y, &f, &f, &f, 8, 16, 32, GRPO_BF16, 8, nullptr, 0, GRPO_F32, FAKE, &f, FAKE, 64, nullptr) ==
-        GRPO_ERR_WORKSPACE);
+  CHECK(grpo_logprobs_bwd(FAKE, FAKE, &y, &f, &f, &f, 8, 16, 32, GRPO_BF16, 8, nullptr, 0, GRPO_F32, FAKE2, nullptr, FAKE, 64,
+                          nullptr) == GRPO_ERR_WORKSPACE);
+  CHECK(grpo_logprobs_bwd(FAKE, FAKE, &y, &f, &f, &f, 8, 16, 32, GRPO_BF16, 8, nullptr, 0, GRPO_F32, nullptr, FAKE, FAKE, 1 << 30,
+                          nullptr) == GRPO_ERR_INVALID_ARG);
   CHECK(grpo_logprobs_bwd(FAKE, FAKE, &y, &f, &f, &f, 8, 16, 32, GRPO_FP8_E4M3, 8, nullptr, 0, GRPO_F32, FAKE, &f, FAKE,
                           1 << 20, nullptr) == GRPO_ERR_INVALID_ARG);
 }

@@ -239,3 +239,45 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         once()
         assert all(torch.equal(held[n], out[n]) for n in out)
+
+
+@pytest.mark.parametrize("t,N,d,V", [("f32", 300, 64, 700), ("f32", 256, 256, 65500), ("bf16", 300, 64, 700), ("bf16", 700, 512, 12100)])
+def test_bitwise_the_same_on_two_streams_at_once(t, N, d, V):
+    i = inputs(N, d, V, t)
+    lp, lse = gp.grpo_logprobs_fwd(i["H"], i["W"], i["y"])
+    want = (lp, lse, *gp.grpo_logprobs_bwd(i["H"], i["W"], i["y"], lp, lse, i["g"]))
+    torch.cuda.synchronize()
+    sides, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(3):
+        for s in sides:
+            with torch.cuda.stream(s):
+                lp, lse = gp.grpo_logprobs_fwd(i["H"], i["W"], i["y"])
+                got.append((lp, lse, *gp.grpo_logprobs_bwd(i["H"], i["W"], i["y"], lp, lse, i["g"])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("N,d,V", [(70, 64, 300), (700, 512, 12100)])
+def test_neighbours_are_left_as_they_were(t, N, d, V):
+    """Inputs and gradients inside larger buffers, filled with NaN around them."""
+    i = inputs(N, d, V, t, seed=5)
+    lp, lse = gp.grpo_logprobs_fwd(i["H"], i["W"], i["y"])
+    want = gp.grpo_logprobs_bwd(i["H"], i["W"], i["y"], lp, lse, i["g"])
+
+    def inside(x, fill=None):
+        buf = torch.full((x.numel() + 128,), math.nan, dtype=x.dtype, device="cuda")
+        view = buf[64:-64].view(x.shape)
+        view.copy_(x if fill is None else torch.full_like(x, fill))
+        return buf, view
+    H, W = inside(i["H"])[1], inside(i["W"])[1]
+    g = torch.full((N + 32,), math.nan, device="cuda")
+    g[16:-16] = i["g"]
+    lp2, lse2 = gp.grpo_logprobs_fwd(H, W, i["y"])
+    assert torch.equal(lp, lp2) and torch.equal(lse, lse2)
+    hb, dH = inside(want[0], 7.0)
+    wb, dW = inside(want[1], 0.0)
+    gp.grpo_logprobs_bwd(H, W, i["y"], lp2, lse2, g[16:-16], dH=dH, dW=dW)
+    assert torch.equal(dH, want[0]) and torch.equal(dW, want[1])
+    for b in (hb, wb):
+        assert b[:64].isnan().all() and b[-64:].isnan().all()

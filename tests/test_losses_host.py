@@ -16,6 +16,7 @@ if not os.path.exists(_lib.LIB_PATH):
 
 L = _lib.lib()
 FAKE = ctypes.c_void_p(0x1000)     # never dereferenced
+FAKE2, FAKE3 = ctypes.c_void_p(0x100000), ctypes.c_void_p(0x200000)
 BIG = (1 << 31) - 1
 
 
@@ -27,14 +28,14 @@ def logprobs_fwd(**kw):
 
 def logprobs_bwd(**kw):
     a = dict(H=FAKE, W=FAKE, y=FAKE, lp=FAKE, lse=FAKE, g=FAKE, N=8, d=16, V=32, dt=1, chunk=8, opts=None, acc=0, dwt=0,
-             dH=FAKE, dW=FAKE, ws=FAKE, wsb=1 << 30)
+             dH=FAKE2, dW=FAKE3, ws=FAKE, wsb=1 << 30)
     a.update(kw)
     return L.grpo_logprobs_bwd(*a.values(), None)
 
 
 SHAPES = [({"N": 0}, -1), ({"V": -1}, -1), ({"d": 12}, -3), ({"dt": 2}, -1), ({"dt": 0, "d": 6}, -3), ({"chunk": 0}, -1),
           ({"N": 1 << 31}, -3), ({"ws": None}, -2), ({"wsb": 64}, -2), ({"H": None}, -1), ({"W": None}, -1), ({"y": None}, -1),
-          ({"lp": None}, -1), ({"lse": None}, -1)]
+          ({"lp": None}, -1), ({"lse": None}, -1), ({"H": 0x1008}, -1), ({"W": 0x1002}, -1), ({"ws": 0x1010}, -2)]
 
 
 @pytest.mark.parametrize("kw,code", SHAPES)
@@ -44,7 +45,9 @@ def test_logprobs_forward_argument_errors(kw, code):
 
 
 @pytest.mark.parametrize("kw,code", SHAPES + [({"g": None}, -1), ({"dH": None, "dW": None}, -1), ({"acc": 2}, -1), ({"dwt": 2}, -1),
-                                             ({"dwt": 1, "dt": 0}, -1), ({"dwt": 1, "acc": 1}, -1), ({"dwt": 1, "chunk": 7}, -1)])
+                                             ({"dwt": 1, "dt": 0}, -1), ({"dwt": 1, "acc": 1}, -1), ({"dwt": 1, "chunk": 7}, -1),
+                                             ({"dH": 0x100004}, -1), ({"dW": 0x100008}, -1), ({"dH": FAKE}, -1), ({"dW": 0x10f0}, -1),
+                                             ({"dW": 0x1000 - 2032}, -1), ({"dW": FAKE2}, -1), ({"dH": 0x200000 + 2032}, -1)])
 def test_logprobs_backward_argument_errors(kw, code):
     assert logprobs_bwd(**kw) == code
     assert L.grpo_last_error()
