@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kFinish)
     const int lane = threadIdx.x & (width - 1);
     for (int64_t b = threadIdx.x / width; b < a.B; b += kFinish / width) {
       ClipSums row = {};
+#pragma unroll 4
       for (int i = lane; i < segs; i += width) {
         const ClipSums p = parts[b * segs + i];
         row.loss += p.loss;
@@ -602,6 +603,7 @@ __global__ void __launch_bounds__(kFinish)
       PrefSums two[2] = {};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
+#pragma unroll 4
         for (int i = lane; i < segs; i += width) {
           const PrefSums q = rows[(2 * p + k) * segs + i];
           two[k].d += q.d;
@@ -676,7 +678,10 @@ Split split_rows(int64_t items, int64_t rows, int64_t L) {
   p.span = (int)(((L + p.segs - 1) / p.segs + 3) / 4 * 4);
   p.segs = (int)((L + p.span - 1) / p.span);
   p.blocks = p.parts = (int)(rows * p.segs);
+  // lanes for all of a row's segments, but no more than let every row have its turn at once (forward
+  // with a sequence ratio: 200 rows of 20000 tokens 29 -> 21 us, 1021 of 16385 37 -> 35)
   p.finish_width = pow2_at_least(p.segs, 64);
+  while (p.finish_width > 1 && items * p.finish_width > kFinish) p.finish_width /= 2;
   return p;
 }
 
