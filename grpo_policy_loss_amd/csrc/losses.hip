@@ -6,12 +6,18 @@
 // over the tokens leaves float64 sums; what a sequence's sums decide is then worked out once
 // for the sequence.  Two forms, by the length of the rows:
 //   rows of at most 1024 tokens   a group of 1 to 64 lanes takes a whole sequence (or pair),
-//                                 4 tokens a lane and load, so that its sums stay in a wave;
+//   (8192 where they are many)    4 tokens a lane and load, so that its sums stay in a wave;
 //                                 a block leaves one partial result of all its sequences
 //   longer rows                   a block takes a segment of one sequence and leaves the
 //                                 segment's sums; the finish joins a sequence's segments
 // A second launch of one block finishes (none where one block held everything).  The backward
 // goes token by token from what the forward kept of each sequence.
+//
+// Bound by memory where there are tokens enough: of 1021 rows of 16385 tokens with a sequence ratio and a
+// KL term the forward reads 13 bytes a token in 52 us (4.2 TB/s), and the finish takes 9 us more;
+// the backward moves 13 in 43 us (5.1 TB/s).  16384 pairs of 511 tokens, 5 bytes a token each way: 26 us
+// (3.2 TB/s; float64 sums beside short rows) and 4.5, 19 us (4.5 TB/s).  Smaller ones are bound by launches:
+// 8 rows of 20480 tokens 6.4, 4.4 and 4.8 us.
 #include <float.h>
 #include <math.h>
 
