@@ -281,3 +281,20 @@ def test_neighbours_are_left_as_they_were(t, N, d, V):
     assert torch.equal(dH, want[0]) and torch.equal(dW, want[1])
     for b in (hb, wb):
         assert b[:64].isnan().all() and b[-64:].isnan().all()
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_offsets_beyond_32_bits(t):
+    """2.25e9 elements of H, of which the last tokens alone have a gradient."""
+    N, d, V, last = 2_200_000, 1024, 40, 200
+    H = torch.empty(N, d, dtype=TYPES[t], device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(3))
+    i = inputs(last, d, V, t, seed=2)
+    H[-last:] = i["H"]
+    y, g = torch.zeros(N, dtype=torch.int32, device="cuda"), torch.zeros(N, device="cuda")
+    y[-last:], g[-last:] = i["y"], i["g"]
+    lp, lse = gp.grpo_logprobs_fwd(H, i["W"], y, 1 << 20)
+    dH, dW = gp.grpo_logprobs_bwd(H, i["W"], y, lp, lse, g, 1 << 20)
+    want = plain_update.logprobs(i["H"], i["W"], i["y"], i["g"], half=HALF[t])
+    for name, x in (("lp", lp[-last:]), ("dH", dH[-last:]), ("dW", dW)):
+        assert ((x.cpu().double() - want[name]).abs() <= want[name + "_tol"]).all(), name
+    assert not dH[:-last].any()
