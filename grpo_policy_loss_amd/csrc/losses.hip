@@ -14,10 +14,10 @@
 // goes token by token from what the forward kept of each sequence.
 //
 // Bound by memory where there are tokens enough: of 1021 rows of 16385 tokens with a sequence ratio and a
-// KL term the forward reads 13 bytes a token in 52 us (4.2 TB/s), and the finish takes 9 us more;
-// the backward moves 13 in 43 us (5.1 TB/s).  16384 pairs of 511 tokens, 5 bytes a token each way: 26 us
-// (3.2 TB/s; float64 sums beside short rows) and 4.5, 19 us (4.5 TB/s).  Smaller ones are bound by launches:
-// 8 rows of 20480 tokens 6.4, 4.4 and 4.8 us.
+// KL term the forward reads 13 bytes a token in 42 us (5.2 TB/s), and the finish takes 9 us more; the
+// backward moves 13 in 45 us (4.8 TB/s).  16384 pairs of 511 tokens, 5 bytes a token each way: 23 us
+// (3.7 TB/s; float64 sums beside short rows) and 4, 17 us (4.9 TB/s).  Smaller ones are bound by launches:
+// 8 rows of 20480 tokens 6.5, 4.4 and 4.8 us.
 #include <float.h>
 #include <math.h>
 
@@ -69,6 +69,10 @@ __device__ __forceinline__ U4 load4(const uint8_t* row, int c, int n) {
     if (c + j < n) v[j] = row[c + j];
   return v;
 }
+// Four gradients.  Non-temporal, so that the inputs stay in the caches rather: 1021 rows of 16385 tokens,
+// both directions, 101 -> 91 us, 32768 of 511 111 -> 101, pairs 46.5 -> 42.7, 8 rows of 20480 16 either way.
+// (Non-temporal loads in the forward take those of the backward out of the caches: 91 -> 93, 101 -> 112.)
+__device__ __forceinline__ void store4(float* to, F4 v) { __builtin_nontemporal_store(v, (F4*)to); }
 // The first of the four that is this lane's.
 __device__ __forceinline__ int first4(int c, int n) { return n >= 4 ? c - min(c, n - 4) : 0; }
 
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(kThreads)
     out[j] = m ? w * slope : 0.f;
   }
   if (c + 4 <= n) {
-    *(F4*)(grad_lp + t0 + c) = out;
+    store4(grad_lp + t0 + c, out);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__(kThreads)
     out[j] = m4[j] != 0 ? g * weights[b] : 0.f;
   }
   if (c + 4 <= n) {
-    *(F4*)(grad_lp + t0 + c) = out;
+    store4(grad_lp + t0 + c, out);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
