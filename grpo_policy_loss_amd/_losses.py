@@ -175,7 +175,7 @@ def grpo_clip_loss_fwd(lp, mask, adv, B: int, L: int, old_lp=None, ref_lp=None, 
     """(loss [1], stats [4], weights) of the clipped policy loss of lp [B * L] float32 (the
     policy's log-probabilities) against old_lp (the sampling policy's; None: lp's own values),
     with adv [B] (one a sequence) or [B * L] (one a token) and the KL term beta kl(ref_lp - lp)
-    where beta is not 0.  The ratio is clipped to [1 - clip_low, 1 + clip_high], and for negative
+    where beta is not 0; all three under the same logit transform.  The ratio is clipped to [1 - clip_low, 1 + clip_high], and for negative
     advantages to clip_dual from above; 0 switches each off.  stats: the means over the unmasked
     tokens of kl, of being clipped from below and from above, and of r - 1 - log r.  weights
     [2 B + 1] is what grpo_clip_loss_bwd takes.  See grpo_clip_loss_fwd in include/grpo.h."""

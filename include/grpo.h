@@ -373,7 +373,7 @@ int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const floa
  * What masked places hold (NaN, infinities) plays no part.  Which side of a border a ratio is on is
  * decided in float64 by its logarithm; sums are float64, in a fixed order.
  *   lp, old_lp (NULL), ref_lp (NULL) [N] float32; mask [N] uint8; adv float32 [B], or [N] if
- *   adv_per_token is 1 (GRPO_RATIO_TOKEN only).
+ *   adv_per_token is 1 (GRPO_RATIO_TOKEN only).  lp, old_lp and ref_lp under the same logit transform.
  * grpo_clip_loss_fwd: loss [1] and stats [4] float32, written: over the unmasked tokens the mean of kl
  *   (0 without ref_lp), the share of tokens with s > r, the share with s < r, and the mean of
  *   r - 1 - log r (an estimate of the divergence from the old policy).  weights [2 B + 1] float32, written, for
