@@ -796,8 +796,13 @@ int grpo_clip_loss_fwd(const float* lp, const float* old_lp, const float* ref_lp
   grpo::ClipArgs a;
   int st = grpo::clip_args(lp, old_lp, ref_lp, mask, adv, weights, B, L, opts, &a);
   if (st != GRPO_OK) return st;
-  st = grpo::check_workspace(workspace, workspace_bytes, grpo_clip_loss_workspace_bytes(B, L));
+  const size_t need = grpo_clip_loss_workspace_bytes(B, L);
+  st = grpo::check_workspace(workspace, workspace_bytes, need);
   if (st != GRPO_OK) return st;
+  const size_t n = (size_t)(B * L);
+  if (!grpo::apart({{loss, 4}, {stats, 16}, {weights, (2 * (size_t)B + 1) * 4}, {workspace, need}},
+                   {{lp, 4 * n}, {old_lp, 4 * n}, {ref_lp, 4 * n}, {mask, n}, {adv, 4 * (a.adv_per_token ? n : (size_t)B)}}))
+    return fail(GRPO_ERR_INVALID_ARG, "loss, stats, weights or workspace overlaps an input or another of them");
   const bool seq = opts != nullptr && opts->ratio == GRPO_RATIO_SEQUENCE;
   return seq ? grpo::clip_forward<true>(a, loss, stats, workspace, (hipStream_t)stream)
              : grpo::clip_forward<false>(a, loss, stats, workspace, (hipStream_t)stream);
@@ -812,8 +817,11 @@ int grpo_clip_loss_bwd(const float* lp, const float* old_lp, const float* ref_lp
   grpo::ClipArgs a;
   const int st = grpo::clip_args(lp, old_lp, ref_lp, mask, adv, weights, B, L, opts, &a);
   if (st != GRPO_OK) return st;
-  for (const float* in : {lp, old_lp, ref_lp, adv})
-    if (in == grad_lp) return fail(GRPO_ERR_INVALID_ARG, "grad_lp is one of the inputs");
+  const size_t n = (size_t)(B * L);
+  if (!grpo::apart({{grad_lp, 4 * n}},
+                   {{lp, 4 * n}, {old_lp, 4 * n}, {ref_lp, 4 * n}, {mask, n}, {adv, 4 * (a.adv_per_token ? n : (size_t)B)},
+                    {weights, (2 * (size_t)B + 1) * 4}, {grad_loss, 4}}))
+    return fail(GRPO_ERR_INVALID_ARG, "grad_lp overlaps an input");
   hipStream_t s = (hipStream_t)stream;
   grpo::ScopedKernelTimer timer(grpo::KK_CLIP_BWD, s);
   const int64_t N = B * L;
@@ -859,8 +867,12 @@ int grpo_pref_loss_fwd(const float* lp, const float* ref_lp, const uint8_t* mask
                 o.label_smoothing);
   if (o.length_mean != 0 && o.length_mean != 1)
     return fail(GRPO_ERR_INVALID_ARG, "length_mean %d is not 0 or 1", (int)o.length_mean);
-  st = grpo::check_workspace(workspace, workspace_bytes, grpo_pref_loss_workspace_bytes(P, L));
+  const size_t need = grpo_pref_loss_workspace_bytes(P, L), n = (size_t)(2 * P * L), rows = (size_t)(2 * P);
+  st = grpo::check_workspace(workspace, workspace_bytes, need);
   if (st != GRPO_OK) return st;
+  if (!grpo::apart({{loss, 4}, {rewards, 4 * rows}, {weights, 4 * rows}, {workspace, need}},
+                   {{lp, 4 * n}, {ref_lp, 4 * n}, {mask, n}}))
+    return fail(GRPO_ERR_INVALID_ARG, "loss, rewards, weights or workspace overlaps an input or another of them");
   const grpo::PrefArgs a{lp, ref_lp, mask, rewards, weights, P, (int32_t)L, o.kind, o.length_mean, o.beta,
                          o.label_smoothing, o.margin, o.nll_weight};
   const grpo::Split p = grpo::split_rows(P, 2 * P, L);
@@ -889,9 +901,11 @@ int grpo_pref_loss_bwd(const uint8_t* mask, const float* weights, const float* g
   GRPO_CHECK_PTR(grad_lp);
   const int st = grpo::check_rows(P, L, 2);
   if (st != GRPO_OK) return st;
+  const int64_t N = 2 * P * L;
+  if (!grpo::apart({{grad_lp, 4 * (size_t)N}}, {{mask, (size_t)N}, {weights, 8 * (size_t)P}, {grad_loss, 4}}))
+    return fail(GRPO_ERR_INVALID_ARG, "grad_lp overlaps an input");
   hipStream_t s = (hipStream_t)stream;
   grpo::ScopedKernelTimer timer(grpo::KK_PREF_BWD, s);
-  const int64_t N = 2 * P * L;
   const unsigned blocks = (unsigned)((N + grpo::kThreads * 4 - 1) / (grpo::kThreads * 4));
   grpo::k_pref_bwd<<<blocks, grpo::kThreads, 0, s>>>(mask, weights, grad_loss, grpo::divider(L), N, grad_lp);
   GRPO_HIP(hipGetLastError());

@@ -380,6 +380,7 @@ int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const floa
  *   the backward.  workspace: grpo_clip_loss_workspace_bytes(B, L), 256-byte aligned.
  * grpo_clip_loss_bwd: grad_lp [N] float32, OVERWRITTEN (0 where masked) = g times *grad_loss (a device
  *   scalar; NULL: 1).  Other arguments and opts are the forward's.
+ * Outputs and workspace lie apart from the inputs and from each other (others are refused).
  * opts (NULL: all zeros): zeros are "off": no clipping on that side, no KL term.  clip_low, clip_high
  * finite and >= 0, clip_dual 0 or finite and > 1, beta finite.  beta != 0 needs ref_lp.
  * B * L must fit int32.
@@ -423,6 +424,7 @@ int grpo_clip_loss_bwd(const float* lp, const float* old_lp, const float* ref_lp
  *   grpo_pref_loss_workspace_bytes(P, L), 256-byte aligned.
  * grpo_pref_loss_bwd: grad_lp [N] float32, OVERWRITTEN (0 where masked): the sequence's weight times
  *   *grad_loss (a device scalar; NULL: 1).
+ * Outputs and workspace lie apart from the inputs and from each other (others are refused).
  * What masked places hold plays no part.  beta finite and > 0, margin and nll_weight finite,
  * nll_weight >= 0, label_smoothing in [0, 1) and, but for GRPO_PREF_SIGMOID, 0.  2 P L must fit int32.
  */
