@@ -738,11 +738,6 @@ int check_aligned(const void* H, const void* W, const void* dH, const void* dW, 
   if ((uintptr_t)ws % 256 != 0) return fail(GRPO_ERR_WORKSPACE, "workspace is not 256-byte aligned");
   return GRPO_OK;
 }
-
-// The gradients are written while the inputs are still read.
-bool overlaps(const void* a, size_t n, const void* b, size_t m) {
-  return a != nullptr && b != nullptr && (uintptr_t)a < (uintptr_t)b + m && (uintptr_t)b < (uintptr_t)a + n;
-}
 }  // namespace
 
 int grpo_logprobs_fwd(const void* H, const void* W, const int32_t* y, int64_t N, int64_t d,
@@ -765,6 +760,10 @@ int grpo_logprobs_fwd(const void* H, const void* W, const int32_t* y, int64_t N,
   if (workspace == nullptr || workspace_bytes < need)
     return fail(GRPO_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
                 workspace == nullptr ? (size_t)0 : workspace_bytes);
+  const size_t es = esize(dtype), n = (size_t)N * 4;
+  if (!grpo::apart({{lp, n}, {lse, dtype == GRPO_F32 ? 2 * n : n}, {workspace, need}},
+                   {{H, (size_t)(N * d) * es}, {W, (size_t)(V * d) * es}, {y, n}}))
+    return fail(GRPO_ERR_INVALID_ARG, "lp, lse or workspace overlaps an input or another of them");
   hipStream_t s = (hipStream_t)stream;
   char* ws = (char*)workspace;
   if (dtype == GRPO_BF16)
@@ -819,11 +818,15 @@ int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const floa
   const bool bf16_dw = dw_dtype == GRPO_BF16;
   if (dw_dtype != GRPO_F32 && !(bf16_dw && dtype == GRPO_BF16))
     return fail(GRPO_ERR_INVALID_ARG, "dw_dtype %d is neither GRPO_F32 nor the head's type", dw_dtype);
-  const size_t es = esize(dtype), h_bytes = (size_t)(N * d) * es, w_bytes = (size_t)(V * d) * es;
-  const size_t dw_bytes = (size_t)(V * d) * (bf16_dw ? 2 : 4);
-  if (overlaps(dH, h_bytes, H, h_bytes) || overlaps(dH, h_bytes, W, w_bytes) || overlaps(dW, dw_bytes, H, h_bytes) ||
-      overlaps(dW, dw_bytes, W, w_bytes) || overlaps(dH, h_bytes, dW, dw_bytes))
-    return fail(GRPO_ERR_INVALID_ARG, "dH or dW overlaps H, W or the other");
+  const size_t es = esize(dtype), n = (size_t)N * 4;
+  const grpo::Memory dh{dH, (size_t)(N * d) * es}, dw{dW, (size_t)(V * d) * (bf16_dw ? 2 : 4)};
+  const auto overlap = [&](size_t ws_bytes) -> int {
+    if (grpo::apart({dh, dw, {workspace, ws_bytes}},
+                    {{H, (size_t)(N * d) * es}, {W, (size_t)(V * d) * es}, {y, n}, {lp, n},
+                     {lse, dtype == GRPO_F32 ? 2 * n : n}, {grad_lp, n}}))
+      return GRPO_OK;
+    return fail(GRPO_ERR_INVALID_ARG, "dH, dW or workspace overlaps an input or another of them");
+  };
   if (bf16_dw && (accumulate || chunk < N))
     return fail(GRPO_ERR_INVALID_ARG, "a bfloat16 dW is written from one chunk: accumulate 0, chunk >= N");
   hipStream_t s = (hipStream_t)stream;
@@ -832,6 +835,8 @@ int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const floa
     if (workspace == nullptr || workspace_bytes < need)
       return fail(GRPO_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need,
                   workspace == nullptr ? (size_t)0 : workspace_bytes);
+    st = overlap(need);
+    if (st != GRPO_OK) return st;
     if (dtype == GRPO_F32)
       return logprobs_bwd64<float>((const float*)H, (const float*)W, y, lp, lse, grad_lp, N, d, V,
                                    chunk, xf, accumulate, 0, (float*)dH, dW, (char*)workspace, s);
@@ -846,6 +851,8 @@ int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const floa
     return fail(GRPO_ERR_WORKSPACE, "workspace needs at least %zu bytes, got %zu",
                 plan_bwd(N, d, V, dtype, chunk, -1).total,
                 workspace == nullptr ? (size_t)0 : workspace_bytes);
+  st = overlap(std::min(p.total, workspace_bytes));
+  if (st != GRPO_OK) return st;
   lv = grpo::LossVariant{0, 0, 0};
   const DwInto into = bf16_dw ? DwInto::kBf16 : accumulate ? DwInto::kSum : DwInto::kNew;
   if (dtype == GRPO_BF16)

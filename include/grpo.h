@@ -347,8 +347,8 @@ int grpo_loss_fwd_noalloc(const void* H, const void* W, const int32_t* y, const 
  *   and chunk >= N also GRPO_BF16: then each sum is rounded once.
  * workspace: grpo_workspace_bytes(GRPO_OP_LOGPROBS_FWD or GRPO_OP_LOGPROBS_BWD, ...), 256-byte aligned.  A smaller chunk
  *   needs less; results depend on it through the order in which dW's and, in bfloat16, dH's parts are summed.
- * dtype GRPO_F32 or GRPO_BF16.  H, W, dH and dW 16-byte aligned.  Only the logit transform of the opts
- * is used.
+ * dtype GRPO_F32 or GRPO_BF16.  H, W, dH and dW 16-byte aligned.  Outputs and workspace lie apart from the
+ * inputs and from each other (others are refused).  Only the logit transform of the opts is used.
  */
 int grpo_logprobs_fwd(const void* H, const void* W, const int32_t* y, int64_t N, int64_t d,
                       int64_t V, int dtype, int64_t chunk, const grpo_opts* opts, float* lp,
