@@ -222,6 +222,20 @@ int read_plan(const void* image, const void* plan, GradHeader* hd) {
   return GRPO_OK;
 }
 
+// Whether none of `of` shares a byte with a gradient of the plan.  A pass over the image on the host, 2 to 3 ns a
+// tensor.
+bool apart_from_gradients(const void* image, const GradHeader& hd, std::initializer_list<Memory> of) {
+  const char* at = (const char*)image + hd.o_tensors;
+  for (int64_t i = 0; i < hd.count; ++i) {
+    grpo_grad_tensor t;
+    memcpy(&t, at + i * (int64_t)sizeof t, sizeof t);
+    const Memory g{t.n > 0 ? t.grad : nullptr, (size_t)t.n * (t.dtype == GRPO_F32 ? 4 : 2)};
+    for (const Memory& m : of)
+      if (share(g, m)) return false;
+  }
+  return true;
+}
+
 template <int KIND>
 int grad_norm(const GradHeader& hd, const char* plan, double max_norm, float* norm, float* scale,
               void* ws, hipStream_t s) {
@@ -294,6 +308,9 @@ int grpo_grad_norm(const void* image, const void* plan, int kind, double max_nor
                 workspace == nullptr ? (size_t)0 : workspace_bytes);
   if ((uintptr_t)workspace % grpo::kAlign != 0)
     return fail(GRPO_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+  const grpo::Memory n{norm, 4}, f{scale, 4}, ws{workspace, grpo_grad_norm_workspace_bytes()};
+  if (!grpo::apart({n, f, ws}, {}) || !grpo::apart_from_gradients(image, hd, {n, f, ws}))
+    return fail(GRPO_ERR_INVALID_ARG, "norm, scale or workspace overlaps a gradient or another of them");
   hipStream_t s = (hipStream_t)stream;
   const char* p = (const char*)plan;
   return kind == GRPO_GRAD_NORM_L2
@@ -308,6 +325,8 @@ int grpo_grad_clip(const void* image, const void* plan, const float* scale, void
   if (st != GRPO_OK) return st;
   GRPO_CHECK_PTR(scale);
   if (hd.chunks == 0) return GRPO_OK;
+  if (!grpo::apart_from_gradients(image, hd, {{scale, 4}}))
+    return fail(GRPO_ERR_INVALID_ARG, "scale is part of a gradient");
   hipStream_t s = (hipStream_t)stream;
   grpo::ScopedKernelTimer timer(grpo::KK_GRAD_CLIP, s);
   const char* p = (const char*)plan;

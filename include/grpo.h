@@ -461,6 +461,7 @@ int grpo_pref_loss_bwd(const uint8_t* mask, const float* weights, const float* g
  *   grpo_grad_norm_workspace_bytes(), 256-byte aligned.
  * grpo_grad_clip: every gradient times *scale (a device scalar), in place, rounded to its type;
  *   nothing is touched where it is 1.
+ * norm, scale and workspace lie apart from every gradient and from each other (others are refused).
  */
 typedef enum { GRPO_GRAD_NORM_L2 = 0, GRPO_GRAD_NORM_MAX = 1 } grpo_grad_norm_kind;
 
