@@ -371,7 +371,8 @@ int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const floa
  * and its gradient with respect to lp (with w_t the weight of l_t in the loss):
  *   g_t = w_t ((s = r ? -A r : 0) + beta dkl/dlp)
  * What masked places hold (NaN, infinities) plays no part.  Which side of a border a ratio is on is
- * decided in float64 by its logarithm; sums are float64, in a fixed order.
+ * decided in float64 by its logarithm.  Sums are float64, in a fixed order, but that four adjacent tokens' kl, and
+ * r - 1 - log r, which are not negative, first join in float32.
  *   lp, old_lp (NULL), ref_lp (NULL) [N] float32; mask [N] uint8; adv float32 [B], or [N] if
  *   adv_per_token is 1 (GRPO_RATIO_TOKEN only).  lp, old_lp and ref_lp under the same logit transform.
  * grpo_clip_loss_fwd: loss [1] and stats [4] float32, written: over the unmasked tokens the mean of kl
