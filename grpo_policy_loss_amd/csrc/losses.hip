@@ -227,6 +227,12 @@ __device__ __forceinline__ void clip_row(const ClipArgs& a, int64_t t0, int n, i
   }
 }
 
+// What the backward takes of a sequence: the factor of its terms, and its ratio's slope.
+__device__ __forceinline__ void keep_sequence(const ClipArgs& a, int64_t b, float inv, float slope) {
+  a.weights[2 * b] = inv;
+  a.weights[2 * b + 1] = slope;
+}
+
 // What a sequence's own sums decide, in one lane for the sequence: the ratio's terms (SEQ; in
 // float64, since a batch's advantages may nearly cancel), and what the backward takes of it.  Gives
 // the factor of the sequence's loss.
@@ -248,10 +254,7 @@ __device__ __forceinline__ double clip_sequence(const ClipArgs& a, int64_t b, fl
       s.loss -= adv * used * n;
     }
   }
-  if (writes && (SEQ || a.seq_mean)) {
-    a.weights[2 * b] = (float)inv;
-    a.weights[2 * b + 1] = slope;
-  }
+  if (writes) keep_sequence(a, b, (float)inv, slope);
   return inv;
 }
 
@@ -299,6 +302,10 @@ __global__ void __launch_bounds__(kThreads)
                 float* __restrict__ stats) {
   const int lane = threadIdx.x & (width - 1);
   const int64_t groups = (int64_t)gridDim.x * (kThreads / width);
+  // (adjacent lanes, adjacent sequences: in the loop below 1 % slower)
+  if (!SEQ && !a.seq_mean)
+    for (int64_t b = blockIdx.x * kThreads + threadIdx.x; b < a.B; b += (int64_t)gridDim.x * kThreads)
+      keep_sequence(a, b, 1.f, 0.f);
   ClipSums s = {};
   for (int64_t b = (int64_t)blockIdx.x * (kThreads / width) + threadIdx.x / width; b < a.B; b += groups) {
     const float adv = a.adv_per_token ? 0.f : a.adv[b];
@@ -336,7 +343,9 @@ __global__ void __launch_bounds__(kThreads)
   ClipSums s = {};
   clip_row<SEQ>(a, b * a.L + from, n, threadIdx.x, kThreads, adv, s);
   clip_block_sum<kThreads>(s);
-  if (threadIdx.x == 0) parts[blockIdx.x] = s;
+  if (threadIdx.x != 0) return;
+  parts[blockIdx.x] = s;
+  if (!SEQ && !a.seq_mean && seg == 0) keep_sequence(a, b, 1.f, 0.f);
 }
 
 // The finish: of blocks' sums (segs 0), or of rows' segments, `width` lanes for a row.

@@ -378,7 +378,8 @@ int grpo_logprobs_bwd(const void* H, const void* W, const int32_t* y, const floa
  * grpo_clip_loss_fwd: loss [1] and stats [4] float32, written: over the unmasked tokens the mean of kl
  *   (0 without ref_lp), the share of tokens with s > r, the share with s < r, and the mean of
  *   r - 1 - log r (an estimate of the divergence from the old policy).  weights [2 B + 1] float32, written, for
- *   the backward.  workspace: grpo_clip_loss_workspace_bytes(B, L), 256-byte aligned.
+ *   the backward: for each sequence the factor of its terms (1, or 1 / max(n_b, 1) for the mean over sequences) and
+ *   the slope of its ratio (0 for a ratio a token), then the weight of all.  workspace: grpo_clip_loss_workspace_bytes(B, L), 256-byte aligned.
  * grpo_clip_loss_bwd: grad_lp [N] float32, OVERWRITTEN (0 where masked) = g times *grad_loss (a device
  *   scalar; NULL: 1).  Other arguments and opts are the forward's.
  * Outputs and workspace lie apart from the inputs and from each other (others are refused).
