@@ -143,7 +143,8 @@ __device__ __forceinline__ Clipped clip_ratio(const ClipArgs& a, float adv, doub
 // kl of one token, and its slope in lp (see grpo_opts for the estimators).
 __device__ __forceinline__ float kl_term(int kind, float x, float lp) {
   const Exp v = exp_excess(x);
-  if (kind == GRPO_KL_FORWARD) return fmaf(x, v.em, -v.excess);
+  // x e^x - (e^x - 1); near 0 as x (e^x - 1) - (e^x - 1 - x), which far below 0 would carry the rounding of x
+  if (kind == GRPO_KL_FORWARD) return fabsf(x) < 0.5f ? fmaf(x, v.em, -v.excess) : fmaf(x, v.e, -v.em);
   if (kind == GRPO_KL_REVERSE_Q) return expf(lp) * v.excess;
   return v.excess;
 }
