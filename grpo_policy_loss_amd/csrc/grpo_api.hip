@@ -229,6 +229,8 @@ bool small_tiles_fwd(int64_t N, int64_t d, int64_t V, int dtype) {
 //   1024  128000  330   546   656   574
 //   4096  1000    30    117   44    126   95    151   171   195
 //   4096  8000    68    154   175   175   578   245   1136  326
+// (By the products alone the rule takes the slower side of d 64, V 128000 at 1024 tokens and of d 4096, V 1000 at
+// 2048.)
 // float32: unless there is enough of everything for the large ones: for dH's at most 8 shares, for dW's
 // tiles and in all, and a row is not less than a tile.
 //   d     V       N = 256     1024        4096        8192
